@@ -11,12 +11,15 @@ from __future__ import annotations
 import ctypes
 import os
 
+from . import serving
 from ._build import LIB_PATH, build  # noqa: F401  (build() is the in-tree compile step)
+from .serving import kda_la_step, kda_step
 
 __all__ = ["kda_fwd", "kda_fwd_sched", "kda_fwd_ordered", "kda_fwd_transposed_state",
            "kda_fwd_bf16_state",
            "kda_fwd_split", "kda_split_workspace_bytes", "kda_fwd_split_noalloc",
            "kda_longest_first", "kda_fwd_check", "c_args",
+           "kda_step", "kda_la_step",
            "kda_chunk_anchor", "kda_status_string", "KdaError", "library_path", "load_library"]
 
 KDA_OK = 0
@@ -31,6 +34,7 @@ KDA_ERR_BAD_SCHEDULE = -8
 KDA_ERR_HIP = -9
 KDA_ERR_BAD_WORKSPACE = -10
 KDA_ERR_SCRATCH_TOO_SMALL = -11
+KDA_ERR_BAD_LAYOUT = -12
 KDA_DTYPE_BF16 = 0
 KDA_DTYPE_FP32 = 1
 
@@ -87,6 +91,7 @@ def load_library():
     lib.kda_chunk_anchor.restype = f32
     lib.kda_status_string.argtypes = [i32]
     lib.kda_status_string.restype = ctypes.c_char_p
+    serving.declare(lib)
     _lib = lib
     return lib
 

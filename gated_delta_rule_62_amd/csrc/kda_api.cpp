@@ -7,9 +7,15 @@
 #include <mutex>
 
 #include "../../include/kda.h"
+#include "api_util.h"
 #include "kda_params.h"
 
 namespace {
+
+using kda::device_cus;
+using kda::make_range;
+using kda::overlaps;
+using kda::Range;
 
 constexpr double kLog2e = 1.4426950408889634;
 // Largest decay span (base 2) of a chunk.  The operands are centred on the middle
@@ -17,23 +23,6 @@ constexpr double kLog2e = 1.4426950408889634;
 // below the bf16 maximum, and the smallest of them, 2^-118 times a component,
 // keeps 8 binades above the bf16 normal minimum for the components' own range.
 constexpr double kMaxSpan = 236.0;
-
-struct Range {
-  uintptr_t lo;
-  uintptr_t hi;  // exclusive
-};
-
-Range make_range(const void* p, int64_t bytes) {
-  Range r;
-  r.lo = reinterpret_cast<uintptr_t>(p);
-  r.hi = r.lo + (bytes > 0 ? static_cast<uintptr_t>(bytes) : 0);
-  return r;
-}
-
-bool overlaps(Range a, Range b) {
-  if (a.lo == a.hi || b.lo == b.hi) return false;  // empty ranges never overlap
-  return a.lo < b.hi && b.lo < a.hi;
-}
 
 // Decay span (base 2) of a chunk: the largest magnitude of its prefix, chunk |lb| log2(e).
 double chunk_span(double lb, int chunk) { return chunk * std::fabs(lb) * kLog2e; }
@@ -58,17 +47,6 @@ int auto_chunk(double lb) {
   for (int rows = 32; rows > 1; rows /= 2)
     if (chunk_admissible(lb, rows)) return rows;
   return 1;
-}
-
-// Compute units of the current device (256 on MI355X when the query fails, e.g.
-// without a GPU).
-int device_cus() {
-  int dev = 0, cus = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return 256;
-  if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
-      cus <= 0)
-    return 256;
-  return cus;
 }
 
 // One workgroup owns all value rows of a (sequence, head) unless there are so few
@@ -444,6 +422,9 @@ const char* kda_status_string(int status) {
     case KDA_ERR_SCRATCH_TOO_SMALL:
       return "KDA_ERR_SCRATCH_TOO_SMALL: kda_split_workspace_bytes of this call exceeds the "
              "64 MiB scratch of kda_fwd_split_noalloc (use kda_fwd_split with a workspace)";
+    case KDA_ERR_BAD_LAYOUT:
+      return "KDA_ERR_BAD_LAYOUT: a pointer or row stride is not a multiple of 16 bytes, or a row "
+             "stride is shorter than the row";
     default: return "KDA_ERR_UNKNOWN";
   }
 }

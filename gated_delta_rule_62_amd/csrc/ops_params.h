@@ -1,0 +1,38 @@
+// Launch parameters shared by the host API and the kernels of the serving operators.
+#ifndef KDA_OPS_PARAMS_H_
+#define KDA_OPS_PARAMS_H_
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace kda {
+
+// One token of each request: kda_step (delta rule, per-key decay) and kda_la_step.
+struct StepParams {
+  const uint16_t* q;       // bf16 [N, Hk, D], rows q_row elements apart
+  const uint16_t* k;       // bf16 [N, Hk, D], rows k_row apart
+  const uint16_t* v;       // bf16 [N, H, D], rows v_row apart
+  const uint16_t* gate;    // kda_step: bf16 [N, H, D]
+  const uint16_t* beta;    // kda_step: bf16 [N, H] (logits)
+  const float* A_log;      // kda_step: [H]
+  const float* dt_bias;    // kda_step: [H, D]
+  const float* g;          // kda_la_step: fp32 [N, H] log decays or nullptr
+  const float* decay;      // kda_la_step: fp32 [H] log decays or nullptr
+  uint16_t* out;           // bf16 [N, H, D]
+  void* state;             // [num_slots, H, D(v), D(k)], bf16 or fp32
+  const int64_t* slot_in;  // [N] or nullptr (identity)
+  const int64_t* slot_out; // [N] or nullptr (slot_in)
+  int64_t num_slots;
+  int64_t q_row, k_row, v_row;
+  int32_t N, H, group;     // group: heads that share a q/k head
+  float scale, lower_bound;
+};
+
+// delta: kda_step's rule, else kda_la_step's.  Returns a hipError_t.
+hipError_t launch_step(const StepParams& p, bool delta, int D, bool fp32_state,
+                       hipStream_t stream);
+constexpr int kStepThreads = 256;  // threads of its workgroups, at most
+
+}  // namespace kda
+
+#endif  // KDA_OPS_PARAMS_H_

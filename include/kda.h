@@ -70,6 +70,9 @@ extern "C" {
 #define KDA_ERR_BAD_WORKSPACE (-10)  /* kda_fwd_split: workspace smaller than required   */
 #define KDA_ERR_SCRATCH_TOO_SMALL (-11) /* kda_fwd_split_noalloc: the call's workspace   */
                                         /* exceeds kda_split_noalloc_max_bytes()         */
+#define KDA_ERR_BAD_LAYOUT (-12)     /* serving operators: a pointer or row stride is    */
+                                     /* not a multiple of 16 bytes, or a row stride is   */
+                                     /* shorter than the row                             */
 
 /* State dtype codes (initial_state_dtype, final_state_dtype). */
 #define KDA_DTYPE_BF16 0
@@ -330,6 +333,80 @@ int kda_fwd_check(const void* q, const void* k, const void* v, const void* g, co
  * most strongly decayed rows of a chunk need.  Pure host function.
  */
 float kda_chunk_anchor(float lower_bound, int chunk_size);
+
+/* ------------------------------------------------------------------------------
+ * Serving operators: the single-token forms of the recurrences, on states kept in a
+ * pool, and the other layers of a model that mixes KDA with them.  The conventions of
+ * the header apply, and for these:
+ *   - pointers are 16-byte aligned (KDA_ERR_BAD_LAYOUT), fp32 and int64 arrays
+ *     naturally aligned;
+ *   - a *_row argument is the distance in elements between the rows of consecutive
+ *     tokens of that tensor (heads * D when it is contiguous; more when it is a view of
+ *     wider rows, as of one projection's output): a multiple of 8 and at least
+ *     heads * D (KDA_ERR_BAD_LAYOUT).  Heads and D are contiguous inside a row;
+ *   - an output must not overlap any input or other output (KDA_ERR_BAD_ALIAS; the
+ *     bytes from a strided tensor's first row to its last count as that tensor).
+ * Each has a *_check function: the same arguments without the stream, returns the status
+ * the operator would return before launching; host code that needs no GPU.
+ * ------------------------------------------------------------------------------ */
+
+/*
+ * kda_step -- one token of each of N requests through the recurrence of kda_fwd, on
+ * states kept in a pool.
+ *   q, k, v, g     bf16 [N, H, D], contiguous; beta bf16 [N, H] (logits).
+ *   out            bf16 [N, H, D].
+ *   scale, A_log, dt_bias, lower_bound  as for kda_fwd (any finite lower bound below 0;
+ *                  decay factors below the fp32 range are zero).
+ *   state          [num_slots, H, D(v), D(k)] of state_dtype: the layout of kda_fwd's
+ *                  final_state, so a prompt's final states are slots of the pool.
+ *                  The update is fp32; out uses the fp32 state, before a bf16 slot is
+ *                  rounded.
+ *   slot_in        int64 [N] device array: request n's state is slot slot_in[n]; NULL: n.
+ *                  An index outside [0, num_slots) reads zeros (a request's first token).
+ *   slot_out       int64 [N] device array: where the new state goes; NULL: slot_in.  An
+ *                  index outside [0, num_slots) stores no state (a padded row; its out row
+ *                  is still written).  Slots that no request names are left as they were.
+ *                  Several requests may read one slot; a slot that a request writes must be
+ *                  named by no other request of the call (its contents, and the results of
+ *                  the others that read it, are unspecified otherwise).
+ *   N, H, D        requests (0: nothing is done), heads, D in {32, 64, 128};
+ *                  N * H < 2^24.  Without slot_in N <= num_slots.
+ * One kernel on `stream`.  Returns KDA_OK or a negative status.
+ */
+int kda_step(const void* q, const void* k, const void* v, const void* g, const void* beta,
+             float scale, void* out, const float* A_log, const float* dt_bias, float lower_bound,
+             void* state, int state_dtype, int64_t num_slots, const int64_t* slot_in,
+             const int64_t* slot_out, int64_t N, int64_t H, int64_t D, void* stream);
+int kda_step_check(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                   float scale, const void* out, const float* A_log, const float* dt_bias,
+                   float lower_bound, const void* state, int state_dtype, int64_t num_slots,
+                   const int64_t* slot_in, const int64_t* slot_out, int64_t N, int64_t H,
+                   int64_t D);
+
+/*
+ * kda_la_step -- one token of each of N requests through linear attention with one
+ * decay per head:
+ *
+ *     S = exp(g_n + decay) S + v k^T,    out = scale S q       (S: V x K)
+ *
+ *   q, k           bf16 [N, Hk, D]; head h of H uses q/k head h / (H / Hk).
+ *   v, out         bf16 [N, H, D] (out contiguous).
+ *   g              fp32 [N, H] natural-log decays, contiguous, or NULL.
+ *   decay          fp32 [H] natural-log decays, or NULL (both NULL: no decay).  A sum
+ *                  g + decay above zero counts as zero.
+ *   state, slots, N, D  as for kda_step.  H % Hk == 0 (KDA_ERR_BAD_SHAPE).
+ * One kernel on `stream`.
+ */
+int kda_la_step(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
+                int64_t v_row, const float* g, const float* decay, float scale, void* out,
+                void* state, int state_dtype, int64_t num_slots, const int64_t* slot_in,
+                const int64_t* slot_out, int64_t N, int64_t H, int64_t Hk, int64_t D,
+                void* stream);
+int kda_la_step_check(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
+                      int64_t v_row, const float* g, const float* decay, float scale,
+                      const void* out, const void* state, int state_dtype, int64_t num_slots,
+                      const int64_t* slot_in, const int64_t* slot_out, int64_t N, int64_t H,
+                      int64_t Hk, int64_t D);
 
 /* kda_status_string -- a static, human-readable name for a status code. */
 const char* kda_status_string(int status);

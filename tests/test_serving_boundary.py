@@ -1,0 +1,94 @@
+"""Refusals of the serving operators, on the CPU: their *_check functions compare pointer
+values and sizes only, and the bindings refuse tensors before anything is launched."""
+from __future__ import annotations
+
+import os
+
+import pytest
+import torch
+
+import gated_delta_rule_62_amd as kda
+
+GB = 1 << 30
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(kda.library_path()):
+        kda.build()
+    return kda.load_library()
+
+
+def _call(fn, order, base, **over):
+    unknown = set(over) - set(base)
+    assert not unknown, unknown
+    return fn(*[dict(base, **over)[n] for n in order])
+
+
+STEP = ("q k v g beta scale out A_log dt_bias lb state dtype slots slot_in slot_out N H D").split()
+STEP_BASE = dict(q=1 * GB, k=2 * GB, v=3 * GB, g=4 * GB, beta=5 * GB, scale=0.1, out=6 * GB,
+                 A_log=7 * GB, dt_bias=8 * GB, lb=-5.0, state=100 * GB, dtype=1, slots=16,
+                 slot_in=None, slot_out=None, N=8, H=4, D=128)
+
+
+def test_step_refusals(lib):
+    st = lambda **o: _call(lib.kda_step_check, STEP, STEP_BASE, **o)
+    assert st() == kda.KDA_OK
+    assert st(slot_in=9 * GB, slot_out=10 * GB, N=64) == kda.KDA_OK
+    assert st(N=0, q=None, k=None, v=None, g=None, beta=None, out=None) == kda.KDA_OK
+    for name in ("q", "k", "v", "g", "beta", "out", "A_log", "dt_bias", "state"):
+        assert st(**{name: None}) == kda.KDA_ERR_NULL_ARG, name
+    for bad in (dict(N=-1), dict(H=0), dict(D=96), dict(D=0), dict(slots=0), dict(N=17),
+                dict(H=1 << 24), dict(N=1 << 40, slot_in=9 * GB), dict(H=1 << 62),
+                dict(N=1 << 22, slot_in=9 * GB), dict(slots=1 << 50)):
+        assert st(**bad) == kda.KDA_ERR_BAD_SHAPE, bad
+    assert st(dtype=2) == kda.KDA_ERR_BAD_DTYPE
+    for s in (float("inf"), float("nan")):
+        assert st(scale=s) == kda.KDA_ERR_BAD_SCALE
+    for lb in (0.0, 1.0, float("nan"), float("-inf")):
+        assert st(lb=lb) == kda.KDA_ERR_BAD_LOWER_BOUND
+    for name in ("q", "k", "v", "g", "out", "state"):
+        assert st(**{name: STEP_BASE[name] + 8}) == kda.KDA_ERR_BAD_LAYOUT, name
+    pool_end = 100 * GB + 16 * 4 * 128 * 128 * 4
+    for name in ("q", "k", "v", "g", "beta", "out", "A_log", "dt_bias"):
+        assert st(**{name: pool_end - 16}) == kda.KDA_ERR_BAD_ALIAS, name
+        assert st(**{name: pool_end}) == kda.KDA_OK, name
+    assert st(out=1 * GB) == kda.KDA_ERR_BAD_ALIAS
+    assert st(slot_in=6 * GB + 16, out=6 * GB) == kda.KDA_ERR_BAD_ALIAS
+
+
+LA_STEP = ("q q_row k k_row v v_row g decay scale out state dtype slots slot_in slot_out N H Hk "
+           "D").split()
+LA_STEP_BASE = dict(q=1 * GB, q_row=256, k=2 * GB, k_row=256, v=3 * GB, v_row=512, g=4 * GB,
+                    decay=5 * GB, scale=0.1, out=6 * GB, state=100 * GB, dtype=0, slots=16,
+                    slot_in=None, slot_out=None, N=8, H=4, Hk=2, D=128)
+
+
+def test_la_step_refusals(lib):
+    st = lambda **o: _call(lib.kda_la_step_check, LA_STEP, LA_STEP_BASE, **o)
+    assert st() == kda.KDA_OK
+    assert st(g=None, decay=None) == kda.KDA_OK
+    assert st(q_row=264, k_row=1 << 20, v_row=520) == kda.KDA_OK
+    assert st(N=0, q=None, k=None, v=None, g=None, out=None) == kda.KDA_OK
+    for name in ("q", "k", "v", "out", "state"):
+        assert st(**{name: None}) == kda.KDA_ERR_NULL_ARG, name
+    for bad in (dict(Hk=3), dict(Hk=0), dict(Hk=8), dict(D=48), dict(N=17), dict(q_row=1 << 61)):
+        assert st(**bad) == kda.KDA_ERR_BAD_SHAPE, bad
+    for bad in (dict(q_row=248), dict(k_row=257), dict(v_row=0), dict(v_row=-512), dict(q=GB + 2),
+                dict(out=6 * GB + 4)):
+        assert st(**bad) == kda.KDA_ERR_BAD_LAYOUT, bad
+    # views of one projection's rows interleave: inputs may, outputs may not lie between them
+    assert st(q_row=1024, k=GB + 512, k_row=1024, v=GB + 1024, v_row=1024) == kda.KDA_OK
+    assert st(q_row=1024, out=GB + 1024) == kda.KDA_ERR_BAD_ALIAS
+    for name in ("g", "decay", "slot_in", "slot_out"):
+        assert st(**{name: 6 * GB + 64}) == kda.KDA_ERR_BAD_ALIAS, name
+
+
+def test_bindings_refuse_cpu_tensors():
+    x = torch.zeros((2, 4, 32), dtype=torch.bfloat16)
+    b = torch.zeros((2, 4), dtype=torch.bfloat16)
+    pool = torch.zeros((2, 4, 32, 32))
+    with pytest.raises(ValueError, match="GPU"):
+        kda.kda_step(x, x, x, x, b, 1.0, x, torch.zeros(4), torch.zeros(4, 32), -1.0, pool)
+    with pytest.raises(ValueError, match="GPU"):
+        kda.kda_la_step(x, x, x, None, 1.0, x, pool)
