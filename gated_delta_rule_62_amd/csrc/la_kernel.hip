@@ -1,0 +1,479 @@
+// Linear attention with one decay per head over prompts (kda_la_fwd), for gfx950.
+//
+// Per sequence and head, on a V x K state S with log decays lam_t <= 0:
+//     S_t = e^{lam_t} S_{t-1} + v_t k_t^T,      out_t = scale S_t q_t
+// evaluated in chunks of C = 64 tokens.  With G the inclusive prefix sum of lam in the
+// chunk and S the state before it,
+//     out_i = scale (e^{G_i} S q_i + sum_{j<=i} e^{G_i - G_j} (q_i . k_j) v_j)
+//     S'    = e^{G_C} S + sum_j e^{G_C - G_j} v_j k_j^T.
+//
+// One workgroup of four waves (two for D = 32) owns one (sequence, head) and walks its
+// chunks.  The fp32 state stays in accumulators: a wave holds S^T, all D keys by its own
+// value columns, as 16x16 tiles (lane l: value l%16, four keys).  Its keys are ordered so
+// that two tiles of accumulators pack into a matrix operand whose reduction slots are
+// eight consecutive keys, a 16-byte read of a q row in LDS: row 4g + i of an even tile is
+// key 8g + i of its 32-key block, and of an odd tile key 8g + 4 + i.
+//
+// Decay weights never exceed one and never come from a difference of long sums.  Inside
+// each 16-token tile p is the inclusive prefix of lam and s the sum of what follows, each
+// summed directly; across tiles e^{G_i - G_j} = e^{p_i} (whole tiles between) e^{s_j}.
+// Only pairs inside one tile take e^{p_i - p_j}, a difference of at most 16 terms.  So an
+// underflowing factor belongs to a weight below the fp32 range, and 16 + 16 + 4
+// exponentials stand for a row of 64.
+//
+// Roundings.  Scores times weights, and the state as an operand of S q, are rounded to
+// bf16 once each: out is a bf16 sum of two such parts, so its error stays below 1.5 of
+// its own rounding.  The state itself must not lose bits at each of thousands of chunks:
+// its update multiplies k (exact in bf16) by the weighted v in three bf16 parts, whose
+// sum holds the fp32 product to 2^-25.
+//
+// Segments.  One workgroup per (sequence, head) leaves most of the device idle for a few
+// long sequences.  Then three launches split the tokens: a state-only pass sums every
+// segment's own contribution from a zero state (k and v only), an elementwise scan turns
+// these into the state before each segment, and the main pass runs all segments at once.
+#include "api_util.h"
+#include "gfx950.h"
+#include "ops_params.h"
+
+namespace kda {
+namespace {
+
+using namespace dev;
+
+constexpr int C = kLaChunk;
+constexpr int RT = C / 16;  // 16-token tiles of a chunk
+
+template <int D>
+struct LaCfg {
+  static constexpr int NW = D >= 64 ? 4 : 2;     // waves
+  static constexpr int THREADS = NW * 64;
+  static constexpr int NT = D / (16 * NW);       // value tiles per wave
+  static constexpr int KT = D / 16;              // key tiles
+  static constexpr int KS = D / 32;              // 32-key steps
+  static constexpr int LD = D + 16;              // row stride of the token tiles (bf16)
+  static constexpr int LDA = C + 8;              // row stride of the score tile
+  static constexpr int TPR = D / 8;              // threads per token row (16 bytes each)
+  static constexpr int RPP = THREADS / TPR;      // rows per pass of the workgroup
+  static constexpr int PASSES = C / RPP;
+};
+
+template <int D, bool STATE_ONLY>
+struct alignas(16) LaSmem {
+  using F = LaCfg<D>;
+  u16 Q[STATE_ONLY ? 1 : C][F::LD];
+  u16 K[C][F::LD];
+  u16 V[C][F::LD];
+  u16 A[STATE_ONLY ? 1 : C][F::LDA];  // scores; columns in the order of a reduction's slots
+  float p[C];       // inclusive prefix of the base-2 log decay inside its 16-token tile
+  float ep[C];      // 2^p
+  float es[C];      // 2^(sum of what follows in the tile)
+  float w[C];       // 2^(sum of what follows in the chunk): weight of a token in the state
+  float tile[RT];   // 2^(sum of the tile)
+};
+
+// One launch unit: which sequence and head, its tokens [t0, t1), its segment.
+struct Unit {
+  int n, h, hk;
+  int64_t t0, t1;
+  int64_t slot;  // of this segment
+  int nseg, s;
+};
+
+__device__ __forceinline__ void seq_bounds(const LaParams& p, int n, int64_t& a, int64_t& b) {
+  if (p.cu != nullptr) {
+    a = p.cu[n];
+    b = p.cu[n + 1];
+    a = a < 0 ? 0 : (a > p.T_total ? p.T_total : a);
+    b = b < a ? a : (b > p.T_total ? p.T_total : b);
+  } else {
+    a = (int64_t)n * p.T;
+    b = a + p.T;
+  }
+}
+
+// The heads of one group read the same q and k: blocks go to the eight XCDs round robin,
+// so a group's heads sit 8 blocks apart, on one XCD and its L2.  False: no such unit.
+__device__ __forceinline__ bool find_unit(const LaParams& p, unsigned block, Unit& u) {
+  const unsigned run = 8u * (unsigned)p.group;
+  const int64_t c = (int64_t)(block / run) * 8 + block % 8;
+  const int Hk = p.H / p.group;
+  const int64_t item = c / Hk;
+  u.hk = (int)(c % Hk);
+  u.h = u.hk * p.group + (int)((block / 8) % (unsigned)p.group);
+  if (p.seg == 0) {
+    if (item >= p.N) return false;
+    u.n = (int)item;
+    u.nseg = 1;
+    u.s = 0;
+    u.slot = 0;
+    seq_bounds(p, u.n, u.t0, u.t1);
+    return true;
+  }
+  if (item >= p.slots) return false;
+  // the last sequence whose first slot is not behind this one (first slots grow strictly)
+  int lo = 0, hi = p.N - 1;
+  int64_t a, b;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    seq_bounds(p, mid, a, b);
+    if (a / p.seg + mid <= item) lo = mid;
+    else hi = mid - 1;
+  }
+  seq_bounds(p, lo, a, b);
+  const int64_t s = item - (a / p.seg + lo);
+  const int64_t nseg = b > a ? (b - a + p.seg - 1) / p.seg : 1;  // an empty sequence keeps one
+  if (s < 0 || s >= nseg) return false;
+  u.n = lo;
+  u.slot = item;
+  u.nseg = (int)nseg;
+  u.s = (int)s;
+  u.t0 = a + s * p.seg;
+  u.t1 = u.t0 + p.seg < b ? u.t0 + p.seg : b;
+  return true;
+}
+
+// First of the four keys that row 4g + i of key tile kt holds for lane group g.
+__device__ __forceinline__ int key0(int kt, int g) { return 32 * (kt >> 1) + 8 * g + 4 * (kt & 1); }
+
+template <int CTRL>
+__device__ __forceinline__ float dpp0(float v) {  // lanes without a source read zero
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL,
+                                                               0xf, 0xf, true));
+}
+
+template <int D, bool STATE_ONLY>
+__global__ __launch_bounds__(LaCfg<D>::THREADS, 2) void la_kernel(LaParams p) {
+  using F = LaCfg<D>;
+  __shared__ LaSmem<D, STATE_ONLY> sm;
+  Unit u;
+  if (!find_unit(p, blockIdx.x, u)) return;  // uniform per workgroup
+  if (STATE_ONLY && u.s == u.nseg - 1) return;  // no segment starts from this one's end
+
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int vw = wave * 16 * F::NT;  // first value column of this wave
+  const int64_t H = p.H;
+
+  // ---- the state before the segment: tile [kt][nt] holds keys key0(kt, lg) .. +3 of value
+  // vw + 16 nt + l16
+  f32x4_t S[F::KT][F::NT];
+#pragma unroll
+  for (int kt = 0; kt < F::KT; ++kt)
+#pragma unroll
+    for (int nt = 0; nt < F::NT; ++nt) S[kt][nt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  float* const wseg = p.ws + (u.slot * H + u.h) * (int64_t)(D * D);
+  const int64_t head = ((int64_t)u.n * H + u.h) * (D * D);
+  if constexpr (!STATE_ONLY) {
+    if (u.nseg > 1) {
+#pragma unroll
+      for (int kt = 0; kt < F::KT; ++kt)
+#pragma unroll
+        for (int nt = 0; nt < F::NT; ++nt)
+          S[kt][nt] = *reinterpret_cast<const f32x4_t*>(
+              wseg + ((kt * F::NT + nt) * F::THREADS + tid) * 4);
+    } else if (p.s_in != nullptr) {
+#pragma unroll
+      for (int kt = 0; kt < F::KT; ++kt)
+#pragma unroll
+        for (int nt = 0; nt < F::NT; ++nt) {
+          const int64_t at = head + (vw + 16 * nt + l16) * D + key0(kt, lg);
+          if (p.s_in_fp32) {
+            S[kt][nt] = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p.s_in) + at);
+          } else {
+            const u32x2_t w =
+                *reinterpret_cast<const u32x2_t*>(static_cast<const u16*>(p.s_in) + at);
+            S[kt][nt] = f32x4_t{bf_lo(w[0]), bf_hi(w[0]), bf_lo(w[1]), bf_hi(w[1])};
+          }
+        }
+    }
+  }
+
+  // ---- raw chunk loads, one chunk ahead: 16 bytes per thread and pass; rows past the end
+  // read zero
+  const int lrow = tid / F::TPR, lcol = (tid % F::TPR) * 8;
+  u32x4_t rq[F::PASSES], rk[F::PASSES], rv[F::PASSES];
+  float rg = 0.f;
+  auto fetch = [&](u32x4_t* r, const u16* base, int64_t row, int heads_off, int64_t t, int valid) {
+    const uint32_t row_bytes = (uint32_t)row * 2u;  // below 2^25
+    const __amdgpu_buffer_rsrc_t rs =
+        make_rsrc(base + t * row + heads_off, (uint32_t)(valid - 1) * row_bytes + D * 2u);
+#pragma unroll
+    for (int i = 0; i < F::PASSES; ++i)
+      r[i] = __builtin_bit_cast(
+          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                       rs, (uint32_t)(lrow + i * F::RPP) * row_bytes + lcol * 2u, 0, 0));
+  };
+  const float dec = p.decay ? p.decay[u.h] : 0.f;
+  auto load = [&](int64_t t) {
+    const int valid = (int)(u.t1 - t < C ? u.t1 - t : C);
+    if constexpr (!STATE_ONLY) fetch(rq, p.q, p.q_row, u.hk * D, t, valid);
+    fetch(rk, p.k, p.k_row, u.hk * D, t, valid);
+    fetch(rv, p.v, p.v_row, u.h * D, t, valid);
+    if (wave == 0 && p.g != nullptr) rg = lane < valid ? p.g[(t + lane) * H + u.h] : 0.f;
+  };
+
+  if (u.t0 < u.t1) load(u.t0);
+  float seg_decay = 1.f;
+  for (int64_t t = u.t0; t < u.t1; t += C) {
+    const int valid = (int)(u.t1 - t < C ? u.t1 - t : C);
+    lds_barrier();  // the previous chunk's reads are done
+#pragma unroll
+    for (int i = 0; i < F::PASSES; ++i) {
+      const int r = lrow + i * F::RPP;
+      if constexpr (!STATE_ONLY) *reinterpret_cast<u32x4_t*>(&sm.Q[r][lcol]) = rq[i];
+      *reinterpret_cast<u32x4_t*>(&sm.K[r][lcol]) = rk[i];
+      *reinterpret_cast<u32x4_t*>(&sm.V[r][lcol]) = rv[i];
+    }
+    if (wave == 0) {  // lane = token: the chunk's decays
+      float lam = rg + dec;
+      lam = (lam > 0.f ? 0.f : lam) * kLog2e;
+      lam = lam < -126.f ? -126.f : lam;  // 2^-126: zero to every weight; keeps sums finite
+      if (lane >= valid) lam = 0.f;
+      float pre = lam, suf = dpp0<0x101>(lam);  // row_shl:1, what follows
+      pre += dpp0<0x111>(pre);                  // row_shr:1, 2, 4, 8
+      pre += dpp0<0x112>(pre);
+      pre += dpp0<0x114>(pre);
+      pre += dpp0<0x118>(pre);
+      suf += dpp0<0x101>(suf);
+      suf += dpp0<0x102>(suf);
+      suf += dpp0<0x104>(suf);
+      suf += dpp0<0x108>(suf);
+      const float ep = __builtin_amdgcn_exp2f(pre), es = __builtin_amdgcn_exp2f(suf);
+      sm.p[lane] = pre;
+      sm.ep[lane] = ep;
+      sm.es[lane] = es;
+      if (l16 == 15) sm.tile[lg] = ep;
+      // weight of a token in the state: the tiles behind its own
+      float w = es;
+      const float e1 = __shfl(ep, 31), e2 = __shfl(ep, 47), e3 = __shfl(ep, 63);
+      if (lg < 3) w *= e3;
+      if (lg < 2) w *= e2;
+      if (lg < 1) w *= e1;
+      sm.w[lane] = w;
+    }
+    lds_barrier();
+    if (t + C < u.t1) load(t + C);
+
+    const float d0 = sm.tile[0], d1 = sm.tile[1], d2 = sm.tile[2], d3 = sm.tile[3];
+    const float d_all = d0 * d1 * d2 * d3;
+    f32x4_t O[RT][F::NT];
+    if constexpr (!STATE_ONLY) {
+      // ---- scores: ten 16x16 tiles (i, j <= i) over the waves, as K Q^T: lane holds token
+      // i = l16 and four j
+      for (int m = wave; m < RT * (RT + 1) / 2; m += F::NW) {
+        const int i = m < 1 ? 0 : m < 3 ? 1 : m < 6 ? 2 : 3, j = m - i * (i + 1) / 2;
+        f32x4_t a = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < F::KS; ++ks)
+          a = mfma(*reinterpret_cast<const u32x4_t*>(&sm.K[16 * j + l16][32 * ks + 8 * lg]),
+                   *reinterpret_cast<const u32x4_t*>(&sm.Q[16 * i + l16][32 * ks + 8 * lg]), a);
+        const int ti = 16 * i + l16, tj = 16 * j + 4 * lg;
+        if (i == j) {
+          const float pi = sm.p[ti];
+          const f32x4_t pj = *reinterpret_cast<const f32x4_t*>(&sm.p[tj]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            a[r] = tj + r <= ti ? a[r] * __builtin_amdgcn_exp2f(pi - pj[r]) : 0.f;
+        } else {
+          float f = sm.ep[ti];
+          if (i - j > 1) f *= sm.tile[j + 1];
+          if (i - j > 2) f *= sm.tile[j + 2];
+          const f32x4_t ej = *reinterpret_cast<const f32x4_t*>(&sm.es[tj]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) a[r] *= f * ej[r];
+        }
+        *reinterpret_cast<u32x2_t*>(&sm.A[ti][32 * (j >> 1) + 8 * lg + 4 * (j & 1)]) =
+            u32x2_t{pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])};
+      }
+      // ---- the state's part: O^T = S Q^T, lane holds token l16 and four values
+      u32x4_t s_op[F::KS][F::NT];
+#pragma unroll
+      for (int ks = 0; ks < F::KS; ++ks)
+#pragma unroll
+        for (int nt = 0; nt < F::NT; ++nt) {
+          const f32x4_t x = S[2 * ks][nt], y = S[2 * ks + 1][nt];
+          s_op[ks][nt] = u32x4_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                                 pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+        }
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+#pragma unroll
+        for (int nt = 0; nt < F::NT; ++nt) O[i][nt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < F::KS; ++ks) {
+          const u32x4_t q = *reinterpret_cast<const u32x4_t*>(&sm.Q[16 * i + l16][32 * ks + 8 * lg]);
+#pragma unroll
+          for (int nt = 0; nt < F::NT; ++nt) O[i][nt] = mfma(s_op[ks][nt], q, O[i][nt]);
+        }
+        float f = sm.ep[16 * i + l16];
+        if (i > 0) f *= d0;
+        if (i > 1) f *= d1;
+        if (i > 2) f *= d2;
+#pragma unroll
+        for (int nt = 0; nt < F::NT; ++nt) O[i][nt] *= f;
+      }
+      lds_barrier();  // the scores are written
+    }
+
+    // ---- per 32 tokens: the chunk's own part of the output, and the state update
+#pragma unroll
+    for (int kt = 0; kt < F::KT; ++kt)
+#pragma unroll
+      for (int nt = 0; nt < F::NT; ++nt) S[kt][nt] *= d_all;
+#pragma unroll
+    for (int b = 0; b < C / 32; ++b) {
+      // V^T: rows are values, slots tokens 32 b + 4g + i and 32 b + 16 + 4g + i
+      u32x4_t vt[F::NT], w1[F::NT], w2[F::NT], w3[F::NT];
+      const int tr = 32 * b + 4 * lg + (l16 >> 2);
+      const f32x4_t wa = *reinterpret_cast<const f32x4_t*>(&sm.w[32 * b + 4 * lg]);
+      const f32x4_t wb = *reinterpret_cast<const f32x4_t*>(&sm.w[32 * b + 16 + 4 * lg]);
+#pragma unroll
+      for (int nt = 0; nt < F::NT; ++nt) {
+        const int c = vw + 16 * nt + 4 * (l16 & 3);
+        const u32x2_t lo = ds_read_tr(&sm.V[tr][c]), hi = ds_read_tr(&sm.V[tr + 16][c]);
+        vt[nt] = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+        // weight times v in three bf16 parts
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = bf_lo(vt[nt][e]) * (e < 2 ? wa[2 * e] : wb[2 * e - 4]);
+          const float y = bf_hi(vt[nt][e]) * (e < 2 ? wa[2 * e + 1] : wb[2 * e - 3]);
+          const unsigned h = pack_bf16(x, y);
+          const float x1 = x - bf_lo(h), y1 = y - bf_hi(h);
+          const unsigned m = pack_bf16(x1, y1);
+          w1[nt][e] = h;
+          w2[nt][e] = m;
+          w3[nt][e] = pack_bf16(x1 - bf_lo(m), y1 - bf_hi(m));
+        }
+      }
+      if constexpr (!STATE_ONLY) {
+#pragma unroll
+        for (int i = 2 * b; i < RT; ++i) {
+          // tile 2 b's columns past the diagonal tile are not written: slots 4-7 zero
+          u32x4_t a;
+          if (i == 2 * b) {
+            const u32x4_t w = *reinterpret_cast<const u32x4_t*>(&sm.A[16 * i + l16][32 * b + 8 * lg]);
+            a = u32x4_t{w[0], w[1], 0u, 0u};
+          } else {
+            a = *reinterpret_cast<const u32x4_t*>(&sm.A[16 * i + l16][32 * b + 8 * lg]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < F::NT; ++nt) O[i][nt] = mfma(vt[nt], a, O[i][nt]);
+        }
+      }
+#pragma unroll
+      for (int kt = 0; kt < F::KT; ++kt) {
+        const int c = 32 * (kt >> 1) + 8 * (l16 & 3) + 4 * (kt & 1);
+        const u32x2_t lo = ds_read_tr(&sm.K[tr][c]), hi = ds_read_tr(&sm.K[tr + 16][c]);
+        const u32x4_t kop = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+#pragma unroll
+        for (int nt = 0; nt < F::NT; ++nt) {
+          S[kt][nt] = mfma(kop, w3[nt], S[kt][nt]);
+          S[kt][nt] = mfma(kop, w2[nt], S[kt][nt]);
+          S[kt][nt] = mfma(kop, w1[nt], S[kt][nt]);
+        }
+      }
+    }
+    if constexpr (STATE_ONLY) {
+      seg_decay *= d_all;
+    } else {
+      const uint32_t out_row = (uint32_t)H * D * 2u;
+      const __amdgpu_buffer_rsrc_t ro =
+          make_rsrc(p.out + (t * H + u.h) * D, (uint32_t)(valid - 1) * out_row + D * 2u);
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int nt = 0; nt < F::NT; ++nt) {
+          const f32x4_t o = O[i][nt] * p.scale;
+          const u32x2_t w = {pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+          __builtin_amdgcn_raw_buffer_store_b64(
+              w, ro, (uint32_t)(16 * i + l16) * out_row + (uint32_t)(vw + 16 * nt + 4 * lg) * 2u, 0, 0);
+        }
+    }
+  }
+
+  if constexpr (STATE_ONLY) {
+#pragma unroll
+    for (int kt = 0; kt < F::KT; ++kt)
+#pragma unroll
+      for (int nt = 0; nt < F::NT; ++nt)
+        *reinterpret_cast<f32x4_t*>(wseg + ((kt * F::NT + nt) * F::THREADS + tid) * 4) = S[kt][nt];
+    if (tid == 0) p.ws_decay[u.slot * H + u.h] = seg_decay;
+  } else if (p.s_out != nullptr && u.s == u.nseg - 1) {
+#pragma unroll
+    for (int kt = 0; kt < F::KT; ++kt)
+#pragma unroll
+      for (int nt = 0; nt < F::NT; ++nt) {
+        const int64_t at = head + (vw + 16 * nt + l16) * D + key0(kt, lg);
+        const f32x4_t x = S[kt][nt];
+        if (p.s_out_fp32) {
+          *reinterpret_cast<f32x4_t*>(static_cast<float*>(p.s_out) + at) = x;
+        } else {
+          *reinterpret_cast<u32x2_t*>(static_cast<u16*>(p.s_out) + at) =
+              u32x2_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+        }
+      }
+  }
+}
+
+// Turns the segments' own sums into the state before each segment, in place: four
+// consecutive floats of one head's accumulator image per thread, segments in order.  Also
+// reads the initial state, so that the main pass never does when it runs in segments and
+// final_state may be the same buffer.
+template <int D>
+__global__ __launch_bounds__(256) void la_scan_kernel(LaParams p) {
+  using F = LaCfg<D>;
+  constexpr int QUADS = D * D / 4, BLOCKS = (QUADS + 255) / 256;
+  const int64_t unit = blockIdx.x / BLOCKS;
+  const int n = (int)(unit / p.H), h = (int)(unit % p.H);
+  const int e = (int)(blockIdx.x % BLOCKS) * 256 + threadIdx.x;
+  int64_t a, b;
+  seq_bounds(p, n, a, b);
+  const int nseg = (int)((b - a + p.seg - 1) / p.seg);
+  if (nseg <= 1 || e >= QUADS) return;
+  const int64_t slot = a / p.seg + n;
+  f32x4_t S = {0.f, 0.f, 0.f, 0.f};
+  if (p.s_in != nullptr) {
+    const int tid = e % F::THREADS, tile = e / F::THREADS, kt = tile / F::NT, nt = tile % F::NT;
+    const int v = (tid >> 6) * 16 * F::NT + 16 * nt + (tid & 15);
+    const int64_t at = ((int64_t)n * p.H + h) * (D * D) + v * D + key0(kt, (tid & 63) >> 4);
+    if (p.s_in_fp32) {
+      S = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p.s_in) + at);
+    } else {
+      const u32x2_t w = *reinterpret_cast<const u32x2_t*>(static_cast<const u16*>(p.s_in) + at);
+      S = f32x4_t{bf_lo(w[0]), bf_hi(w[0]), bf_lo(w[1]), bf_hi(w[1])};
+    }
+  }
+  const int64_t step = (int64_t)p.H * (D * D);
+  float* w = p.ws + (slot * p.H + h) * (int64_t)(D * D) + e * 4;
+  const float* d = p.ws_decay + slot * p.H + h;
+  for (int s = 0; s < nseg - 1; ++s) {
+    const f32x4_t own = *reinterpret_cast<const f32x4_t*>(w);
+    *reinterpret_cast<f32x4_t*>(w) = S;
+    S = S * d[(int64_t)s * p.H] + own;
+    w += step;
+  }
+  *reinterpret_cast<f32x4_t*>(w) = S;
+}
+
+template <int D>
+hipError_t go(const LaParams& p, hipStream_t stream) {
+  using F = LaCfg<D>;
+  const int64_t run = 8 * (int64_t)p.group;
+  const int64_t items = p.seg ? p.slots : p.N;
+  const int64_t blocks = (items * (p.H / p.group) + 7) / 8 * run;
+  if (p.seg) {
+    la_kernel<D, true><<<dim3((unsigned)blocks), F::THREADS, 0, stream>>>(p);
+    constexpr int BLOCKS = (D * D / 4 + 255) / 256;
+    la_scan_kernel<D><<<dim3((unsigned)((int64_t)p.N * p.H * BLOCKS)), 256, 0, stream>>>(p);
+  }
+  la_kernel<D, false><<<dim3((unsigned)blocks), F::THREADS, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_la(const LaParams& p, int D, hipStream_t stream) {
+  return D == 32 ? go<32>(p, stream) : D == 64 ? go<64>(p, stream) : go<128>(p, stream);
+}
+
+}  // namespace kda

@@ -104,6 +104,112 @@ int la_step_check(const void* q, int64_t q_row, const void* k, int64_t k_row, co
   return KDA_OK;
 }
 
+// Tokens per segment of kda_la_fwd when the caller leaves the choice, 0 for none.  Times in
+// microseconds.  Unsegmented, one workgroup walks a sequence (whose length is only known
+// on average) at kStep per chunk, unless the device is full and HBM bounds it.  In
+// segments all tokens' k and v are read twice, and each segment's state is written, scanned
+// and read; a few segments per compute unit fill the device.
+int64_t la_auto_segment(int64_t T_total, int64_t N, int64_t H, int64_t D) {
+  constexpr double kStep = 1.7, kRate = 5.0e6 /* bytes per us */, kLaunches = 8.0;
+  const int64_t C = kda::kLaChunk;
+  const int64_t units = N * H, cus = kda::device_cus(), mean = T_total / N;
+  const double bytes = 8.0 * T_total * H * D;
+  const double waves = std::ceil(units / (2.0 * cus));
+  const double whole = std::fmax(bytes / kRate, waves * kStep * mean / C);
+  // segments that give each compute unit two workgroups, of at least four chunks
+  int64_t per_seq = (2 * cus + units - 1) / units;
+  int64_t seg = (mean / (per_seq > 0 ? per_seq : 1) + C - 1) / C * C;
+  if (seg < 4 * C) seg = 4 * C;
+  if (seg > (1 << 20)) seg = 1 << 20;
+  if (2 * seg > mean) return 0;
+  const double state = 4.0 * 4.0 * D * D * H * (double(T_total) / seg);
+  const double split = std::fmax((1.5 * bytes + state) / kRate, 1.75 * kStep * seg / C) + kLaunches;
+  return split < whole ? seg : 0;
+}
+
+// A segment length as given (0: automatic) to the one used, or a negative status.
+int64_t la_segment(int64_t T_total, int64_t N, int64_t H, int64_t D, int64_t segment) {
+  if (segment < 0 || segment % kda::kLaChunk != 0 || segment > (1 << 20))
+    return KDA_ERR_BAD_SCHEDULE;
+  return segment ? segment : la_auto_segment(T_total, N, H, D);
+}
+
+// Whether every launch of a la call stays below 2^32 work-items and its slots in range.
+bool la_grid_ok(int64_t T_total, int64_t N, int64_t H, int64_t seg) {
+  const int64_t most = (((int64_t)1 << 32) - 1) / 256 / 8;  // in units of eight workgroups
+  const int64_t items = seg ? kda::la_slots(T_total, N, seg) : N;
+  if (items > most * 8 / H - 8) return false;
+  return !seg || N <= most / H / 2;  // the scan: up to 16 workgroups per (sequence, head)
+}
+
+// Bytes of the workspace of a la call in segments of seg tokens, or a negative status.
+int64_t la_ws_bytes(int64_t T_total, int64_t N, int64_t H, int64_t D, int64_t seg) {
+  if (seg == 0) return 0;
+  if (!la_grid_ok(T_total, N, H, seg)) return KDA_ERR_BAD_SHAPE;
+  return kda::la_ws_floats(kda::la_slots(T_total, N, seg), H, D) * 4;
+}
+
+// The sizes of a packed or batched call; num_seqs sequences.
+int batch_ok(const int64_t* cu, int64_t N, int64_t B, int64_t T) {
+  if (B < 1 || T < 0) return KDA_ERR_BAD_SHAPE;
+  if (T == 0 && !cu) return KDA_ERR_BAD_SHAPE;
+  if (T > ((int64_t)1 << 40) / B) return KDA_ERR_BAD_SHAPE;
+  if (cu ? (B != 1 || N < 1) : N != B) return KDA_ERR_BAD_VARLEN;
+  return KDA_OK;
+}
+
+int la_check(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
+             int64_t v_row, const float* g, const float* decay, float scale, const void* out,
+             const void* s_in, int in_dtype, const void* s_out, int out_dtype, const int64_t* cu,
+             int64_t N, int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t D, int64_t segment,
+             const void* workspace, int64_t workspace_bytes, int64_t* seg_out) {
+  if (D != 32 && D != 64 && D != 128) return KDA_ERR_BAD_SHAPE;
+  if (H < 1 || Hk < 1 || H % Hk != 0) return KDA_ERR_BAD_SHAPE;
+  // a chunk's 64 token rows are addressed with 32-bit byte offsets
+  if (H >= ((int64_t)1 << 24) / D || q_row >= (1 << 24) || k_row >= (1 << 24) ||
+      v_row >= (1 << 24))
+    return KDA_ERR_BAD_SHAPE;
+  const int sizes = batch_ok(cu, N, B, T);
+  if (sizes != KDA_OK) return sizes;
+  const int64_t tok = B * T;
+  if (N > (((int64_t)1 << 31) - 1) / H || !la_grid_ok(tok, N, H, 0)) return KDA_ERR_BAD_SHAPE;
+  if ((s_in && !state_dtype_ok(in_dtype)) || (s_out && !state_dtype_ok(out_dtype)))
+    return KDA_ERR_BAD_DTYPE;
+  if (!std::isfinite(scale)) return KDA_ERR_BAD_SCALE;
+  if (tok > 0 && (!q || !k || !v || !out)) return KDA_ERR_NULL_ARG;
+  if (!row_ok(q_row, Hk, D) || !row_ok(k_row, Hk, D) || !row_ok(v_row, H, D) || !aligned16(q) ||
+      !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(s_in) || !aligned16(s_out) ||
+      !aligned16(workspace))
+    return KDA_ERR_BAD_LAYOUT;
+  int64_t seg = la_segment(tok, N, H, D, segment);
+  if (seg < 0) return static_cast<int>(seg);
+  if (segment == 0 && !workspace) seg = 0;  // left to the library: without one, no segments
+  const int64_t need = la_ws_bytes(tok, N, H, D, seg);
+  if (need < 0) return static_cast<int>(need);
+  if (need > 0 && !workspace) return KDA_ERR_NULL_ARG;
+  if (need > workspace_bytes) return KDA_ERR_BAD_WORKSPACE;
+
+  const int64_t st = N * H * D * D;
+  const Range ro = make_range(out, tok * H * D * 2),
+              rs = make_range(s_out, s_out ? st * (out_dtype ? 4 : 2) : 0),
+              ri = make_range(s_in, s_in ? st * (in_dtype ? 4 : 2) : 0),
+              rw = make_range(workspace, need);
+  const Range ins[] = {make_range(q, span_bytes(tok, q_row, Hk, D)),
+                       make_range(k, span_bytes(tok, k_row, Hk, D)),
+                       make_range(v, span_bytes(tok, v_row, H, D)),
+                       make_range(g, g ? tok * H * 4 : 0),
+                       make_range(decay, decay ? H * 4 : 0),
+                       make_range(cu, cu ? (N + 1) * 8 : 0)};
+  if (any_overlap(ro, ins, 6) || any_overlap(rs, ins, 6) || any_overlap(rw, ins, 6))
+    return KDA_ERR_BAD_ALIAS;
+  if (overlaps(ro, rs) || overlaps(ro, ri) || overlaps(ro, rw) || overlaps(rs, rw) ||
+      overlaps(ri, rw))
+    return KDA_ERR_BAD_ALIAS;
+  if (overlaps(rs, ri) && !(s_in == s_out && in_dtype == out_dtype)) return KDA_ERR_BAD_ALIAS;
+  *seg_out = seg;
+  return KDA_OK;
+}
+
 int status(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_HIP; }
 
 }  // namespace
@@ -186,6 +292,69 @@ int kda_la_step(const void* q, int64_t q_row, const void* k, int64_t k_row, cons
   p.scale = scale;
   return status(kda::launch_step(p, false, static_cast<int>(D), state_dtype == KDA_DTYPE_FP32,
                                  static_cast<hipStream_t>(stream)));
+}
+
+int64_t kda_la_workspace_bytes(int64_t T_total, int64_t num_seqs, int64_t H, int64_t D,
+                               int64_t segment) {
+  if (T_total < 0 || T_total > ((int64_t)1 << 40) || num_seqs < 1 || H < 1 ||
+      (D != 32 && D != 64 && D != 128) || H >= ((int64_t)1 << 24) / D ||
+      num_seqs > (((int64_t)1 << 31) - 1) / H)
+    return KDA_ERR_BAD_SHAPE;
+  const int64_t seg = la_segment(T_total, num_seqs, H, D, segment);
+  return seg < 0 ? seg : la_ws_bytes(T_total, num_seqs, H, D, seg);
+}
+
+int kda_la_fwd_check(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
+                     int64_t v_row, const float* g, const float* decay, float scale,
+                     const void* out, const void* initial_state, int initial_state_dtype,
+                     const void* final_state, int final_state_dtype, const int64_t* cu_seqlens,
+                     int64_t num_seqs, int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t D,
+                     int64_t segment, const void* workspace, int64_t workspace_bytes) {
+  int64_t seg = 0;
+  return la_check(q, q_row, k, k_row, v, v_row, g, decay, scale, out, initial_state,
+                  initial_state_dtype, final_state, final_state_dtype, cu_seqlens, num_seqs, B, T,
+                  H, Hk, D, segment, workspace, workspace_bytes, &seg);
+}
+
+int kda_la_fwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
+               int64_t v_row, const float* g, const float* decay, float scale, void* out,
+               const void* initial_state, int initial_state_dtype, void* final_state,
+               int final_state_dtype, const int64_t* cu_seqlens, int64_t num_seqs, int64_t B,
+               int64_t T, int64_t H, int64_t Hk, int64_t D, int64_t segment, void* workspace,
+               int64_t workspace_bytes, void* stream) {
+  int64_t seg = 0;
+  const int st = la_check(q, q_row, k, k_row, v, v_row, g, decay, scale, out, initial_state,
+                          initial_state_dtype, final_state, final_state_dtype, cu_seqlens,
+                          num_seqs, B, T, H, Hk, D, segment, workspace, workspace_bytes, &seg);
+  if (st != KDA_OK) return st;
+  kda::LaParams p = {};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.g = g;
+  p.decay = decay;
+  p.out = static_cast<uint16_t*>(out);
+  p.s_in = initial_state;
+  p.s_out = final_state;
+  p.cu = cu_seqlens;
+  p.q_row = q_row;
+  p.k_row = k_row;
+  p.v_row = v_row;
+  p.T = T;
+  p.T_total = B * T;
+  p.N = static_cast<int32_t>(num_seqs);
+  p.H = static_cast<int32_t>(H);
+  p.group = static_cast<int32_t>(H / Hk);
+  p.s_in_fp32 = initial_state_dtype == KDA_DTYPE_FP32 ? 1 : 0;
+  p.s_out_fp32 = final_state_dtype == KDA_DTYPE_FP32 ? 1 : 0;
+  p.scale = scale;
+  p.seg = static_cast<int32_t>(seg);
+  if (seg) {
+    p.slots = kda::la_slots(B * T, num_seqs, seg);
+    p.ws = static_cast<float*>(workspace);
+    p.ws_decay = p.ws + p.slots * H * D * D;
+  }
+  return status(kda::launch_la(p, static_cast<int>(D), static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

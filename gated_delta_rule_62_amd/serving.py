@@ -12,15 +12,20 @@ _VP, _I64, _F32, _I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.
 
 _STEP = [_VP] * 5 + [_F32] + [_VP] * 3 + [_F32, _VP, _I32, _I64, _VP, _VP] + [_I64] * 3
 _LA_STEP = ([_VP, _I64] * 3 + [_VP, _VP, _F32, _VP, _VP, _I32, _I64, _VP, _VP] + [_I64] * 4)
+_LA_FWD = ([_VP, _I64] * 3 + [_VP, _VP, _F32, _VP, _VP, _I32, _VP, _I32, _VP] + [_I64] * 7
+           + [_VP, _I64])
 
 
 def declare(lib) -> None:
     """Sets the argument types of the serving operators' C functions."""
-    for name, args in (("kda_step", _STEP), ("kda_la_step", _LA_STEP)):
+    for name, args in (("kda_step", _STEP), ("kda_la_step", _LA_STEP),
+                       ("kda_la_fwd", _LA_FWD)):
         getattr(lib, name).argtypes = args + [_VP]
         getattr(lib, name).restype = _I32
         getattr(lib, name + "_check").argtypes = args
         getattr(lib, name + "_check").restype = _I32
+    lib.kda_la_workspace_bytes.argtypes = [_I64] * 5
+    lib.kda_la_workspace_bytes.restype = _I64
 
 
 def _lib():
@@ -155,3 +160,76 @@ def kda_la_step(q, k, v, g, scale, out, state, decay=None, slot_in=None, slot_ou
             *_pool(state, slot_in, slot_out, N, H, D, dev), N, H, Hk, D,
             _stream_ptr(stream, dev))
     _launch(_lib().kda_la_step, dev, args)
+
+
+def _state(name, t, N, H, D, dev):
+    """Address and dtype code of a prompt's initial or final states, or nothing."""
+    from . import _state_dtype_code
+    if t is None:
+        return None, 0
+    return _tensor(name, t, t.dtype, (N, H, D, D), dev), _state_dtype_code(t)
+
+
+def _workspace(workspace, need, dev, stream):
+    """The caller's workspace, or one from torch's allocator for this call."""
+    import torch
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        if stream is not None:  # the allocator knows only the current stream
+            s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream, dev)
+            workspace.record_stream(s)
+    elif workspace.dtype != torch.uint8 or workspace.dim() != 1:
+        raise ValueError("workspace must be a 1-d uint8 tensor")
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and live on the same GPU")
+    return workspace.data_ptr(), workspace.numel(), workspace
+
+
+def kda_la_workspace_bytes(T_total: int, num_seqs: int, H: int, D: int, segment: int = 0) -> int:
+    """Bytes of the workspace of ``kda_la_fwd`` (0: this call needs none)."""
+    n = _lib().kda_la_workspace_bytes(int(T_total), int(num_seqs), int(H), int(D), int(segment))
+    if n < 0:
+        _raise(int(n))
+    return int(n)
+
+
+def kda_la_fwd(q, k, v, g, scale, out, decay=None, initial_state=None, final_state=None,
+               cu_seqlens=None, segment: int = 0, workspace=None, stream=None) -> None:
+    """Prompts through linear attention with one decay per head (asynchronous on ``stream``):
+    ``S = exp(g_t + decay) S + v_t k_t^T``, ``out_t = scale S q_t``.
+
+    q, k: bf16 ``[B,T,Hk,D]``, v: bf16 ``[B,T,H,D]`` with H a multiple of Hk (views with one
+    row stride are taken as they are); out: bf16 ``[B,T,H,D]``; g: fp32 ``[B,T,H]`` log decays
+    or None; decay: fp32 ``[H]`` log decays or None; states ``[N,H,D,D]`` bf16 or fp32 or
+    None, and ``cu_seqlens``, as for ``kda_fwd``.  ``segment``: 0 (automatic) or tokens per
+    segment (a multiple of 64).  ``workspace``: a uint8 tensor of at least
+    ``kda_la_workspace_bytes(B*T, N, H, D, segment)`` bytes for this call alone; None takes
+    one from torch's allocator where the call needs it.
+    """
+    import torch
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q and v must be [B,T,heads,D]")
+    B, T, H, D = v.shape
+    Hk = q.shape[2]
+    dev = _device(q)
+    if torch.cuda.current_device() != dev.index:  # schedules go by the current device
+        with torch.cuda.device(dev):
+            return kda_la_fwd(q, k, v, g, scale, out, decay, initial_state, final_state,
+                              cu_seqlens, segment, workspace, stream)
+    cu, N = None, B
+    if cu_seqlens is not None:
+        N = cu_seqlens.numel() - 1
+        cu = _tensor("cu_seqlens", cu_seqlens, torch.int64, (N + 1,), dev)
+    lib = _lib()
+    need = lib.kda_la_workspace_bytes(B * T, N, H, D, int(segment))
+    ws, ws_bytes, _keep = _workspace(workspace, max(need, 0), dev, stream)
+    args = (*_rows("q", q, (B, T, Hk, D), dev), *_rows("k", k, (B, T, Hk, D), dev),
+            *_rows("v", v, (B, T, H, D), dev), _optional("g", g, torch.float32, (B, T, H), dev),
+            _optional("decay", decay, torch.float32, (H,), dev), float(scale),
+            _tensor("out", out, torch.bfloat16, (B, T, H, D), dev),
+            *_state("initial_state", initial_state, N, H, D, dev),
+            *_state("final_state", final_state, N, H, D, dev), cu, N, B, T, H, Hk, D,
+            int(segment), ws, ws_bytes, _stream_ptr(stream, dev))
+    _launch(lib.kda_la_fwd, dev, args)

@@ -408,6 +408,61 @@ int kda_la_step_check(const void* q, int64_t q_row, const void* k, int64_t k_row
                       const int64_t* slot_in, const int64_t* slot_out, int64_t N, int64_t H,
                       int64_t Hk, int64_t D);
 
+/*
+ * kda_la_fwd -- prompts through linear attention with one decay per head.  Per sequence
+ * and head the V x K state S evolves token by token as
+ *
+ *     S = exp(g_t + decay) S + v_t k_t^T,    out_t = scale S q_t
+ *
+ * evaluated in chunks of 64 tokens with bf16 matrix-core products and an fp32 state.
+ *   q, k           bf16 [B, T, Hk, D] with row strides q_row, k_row (below 2^24); head h of
+ *                  H uses q/k head h / (H / Hk).  Batch rows follow each other: token t of
+ *                  batch row b is row b * T + t.
+ *   v              bf16 [B, T, H, D], row stride v_row (below 2^24).
+ *   out            bf16 [B, T, H, D], contiguous.
+ *   g              fp32 [B, T, H] natural-log decays, contiguous, or NULL.
+ *   decay          fp32 [H] natural-log decays, or NULL (both NULL: no decay).  A sum
+ *                  g + decay above zero counts as zero, and below -87.3 (a factor of
+ *                  2^-126, minus infinity included) as -87.3; NaN reaches the outputs of
+ *                  its head's chunk and all that follow.
+ *   initial_state, final_state, cu_seqlens, num_seqs, B, T  as for kda_fwd, the in-place
+ *                  state alias included.  An empty sequence passes its state through.
+ *   H, Hk, D       H % Hk == 0, H * D < 2^24, D in {32, 64, 128}.
+ *   segment        0 (automatic), or tokens per segment: a multiple of 64, at most 2^20
+ *                  (KDA_ERR_BAD_SCHEDULE).  A few long sequences do not fill the device
+ *                  one workgroup per (sequence, head): their tokens are then split into
+ *                  segments, whose own sums are formed first (three kernels instead of
+ *                  one).  The state before a segment is then a sum in another order, so
+ *                  results differ from the unsegmented ones by fp32 roundings of the state.
+ *   workspace      caller-owned device memory, 16-byte aligned, of at least
+ *                  kda_la_workspace_bytes(B * T, num_seqs, H, D, segment) bytes
+ *                  (KDA_ERR_BAD_WORKSPACE), scratch on return: calls that may overlap in
+ *                  time need one each.  With segment 0 it may be NULL: no segments then.
+ * A non-finite q, k or v of one token may reach the outputs of earlier tokens of its
+ * sequence and head inside the same 64-token chunk (zero weights times it).
+ */
+int kda_la_fwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
+               int64_t v_row, const float* g, const float* decay, float scale, void* out,
+               const void* initial_state, int initial_state_dtype, void* final_state,
+               int final_state_dtype, const int64_t* cu_seqlens, int64_t num_seqs, int64_t B,
+               int64_t T, int64_t H, int64_t Hk, int64_t D, int64_t segment, void* workspace,
+               int64_t workspace_bytes, void* stream);
+int kda_la_fwd_check(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
+                     int64_t v_row, const float* g, const float* decay, float scale,
+                     const void* out, const void* initial_state, int initial_state_dtype,
+                     const void* final_state, int final_state_dtype, const int64_t* cu_seqlens,
+                     int64_t num_seqs, int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t D,
+                     int64_t segment, const void* workspace, int64_t workspace_bytes);
+
+/*
+ * kda_la_workspace_bytes -- bytes of kda_la_fwd's workspace for T_total = B * T tokens of
+ * num_seqs sequences: zero when the (automatic) schedule uses no segments, else one fp32
+ * state and decay per head for each of T_total / segment + num_seqs + 1 slots.  Returns the
+ * size or a negative status (KDA_ERR_BAD_SHAPE, KDA_ERR_BAD_SCHEDULE).
+ */
+int64_t kda_la_workspace_bytes(int64_t T_total, int64_t num_seqs, int64_t H, int64_t D,
+                               int64_t segment);
+
 /* kda_status_string -- a static, human-readable name for a status code. */
 const char* kda_status_string(int status);
 

@@ -38,6 +38,21 @@ def la_step(q, k, v, lam, scale, S):
     return out, new, abs(scale) * (mag * q.abs()[..., None, :]).sum(-1), mag
 
 
+def la_prompt(q, k, v, lam, scale, S):
+    """A prompt token by token: q, k [T, H, D] (one per head), v [T, H, D], lam [T, H], S
+    [H, V, K].  Returns out, S', |out|, |S'|."""
+    out, mag = torch.zeros_like(v), torch.zeros_like(v)
+    S, S_mag = S.clone(), S.abs()
+    a = torch.exp(lam)
+    for t in range(v.shape[0]):
+        add = v[t][:, :, None] * k[t][:, None, :]
+        S = S * a[t][:, None, None] + add
+        S_mag = S_mag * a[t][:, None, None] + add.abs()
+        out[t] = scale * (S @ q[t][:, :, None])[..., 0]
+        mag[t] = abs(scale) * (S_mag @ q[t].abs()[:, :, None])[..., 0]
+    return out, S, mag, S_mag
+
+
 def check(got, want, bound, what):
     """Every element within its bound; NaN and infinities where they are wanted."""
     got, want = got.to(torch.float64), want.to(torch.float64)

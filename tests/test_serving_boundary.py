@@ -92,3 +92,54 @@ def test_bindings_refuse_cpu_tensors():
         kda.kda_step(x, x, x, x, b, 1.0, x, torch.zeros(4), torch.zeros(4, 32), -1.0, pool)
     with pytest.raises(ValueError, match="GPU"):
         kda.kda_la_step(x, x, x, None, 1.0, x, pool)
+
+
+LA = ("q q_row k k_row v v_row g decay scale out s_in in_dtype s_out out_dtype cu N B T H Hk D "
+      "segment ws ws_bytes").split()
+LA_BASE = dict(q=1 * GB, q_row=256, k=2 * GB, k_row=256, v=3 * GB, v_row=512, g=4 * GB,
+               decay=5 * GB, scale=0.1, out=6 * GB, s_in=7 * GB, in_dtype=1, s_out=8 * GB,
+               out_dtype=0, cu=None, N=2, B=2, T=100, H=4, Hk=2, D=128, segment=0, ws=None,
+               ws_bytes=0)
+
+
+def test_la_fwd_refusals(lib):
+    st = lambda **o: _call(lib.kda_la_fwd_check, LA, LA_BASE, **o)
+    packed = dict(cu=9 * GB, B=1, N=5)
+    assert st() == kda.KDA_OK and st(**packed) == kda.KDA_OK
+    assert st(g=None, decay=None, s_in=None, s_out=None) == kda.KDA_OK
+    assert st(**packed, T=0, q=None, k=None, v=None, out=None, g=None) == kda.KDA_OK
+    for name in ("q", "k", "v", "out"):
+        assert st(**{name: None}) == kda.KDA_ERR_NULL_ARG, name
+    for bad in (dict(Hk=3), dict(Hk=0), dict(D=96), dict(B=0), dict(T=0), dict(T=-1),
+                dict(q_row=1 << 24), dict(v_row=1 << 40), dict(H=1 << 17), dict(T=1 << 41),
+                dict(H=1 << 62), dict(N=1 << 30, B=1 << 30)):
+        assert st(**bad) == kda.KDA_ERR_BAD_SHAPE, bad
+    for bad in (dict(N=3), dict(cu=9 * GB), dict(cu=9 * GB, B=1, N=0)):
+        assert st(**bad) == kda.KDA_ERR_BAD_VARLEN, bad
+    assert st(in_dtype=2) == st(out_dtype=-1) == kda.KDA_ERR_BAD_DTYPE
+    assert st(scale=float("nan")) == kda.KDA_ERR_BAD_SCALE
+    for bad in (dict(q_row=248), dict(k_row=260), dict(v_row=504), dict(s_in=7 * GB + 4),
+                dict(s_out=8 * GB + 8), dict(out=6 * GB + 2), dict(ws=20 * GB + 8)):
+        assert st(**bad) == kda.KDA_ERR_BAD_LAYOUT, bad
+    for seg in (-64, 1, 63, 100, 1 << 21):
+        assert st(segment=seg) == kda.KDA_ERR_BAD_SCHEDULE, seg
+    # the exact state alias only
+    assert st(s_out=7 * GB, out_dtype=1) == kda.KDA_OK
+    assert st(s_out=7 * GB, out_dtype=0) == kda.KDA_ERR_BAD_ALIAS
+    assert st(s_out=7 * GB + 64, out_dtype=1) == kda.KDA_ERR_BAD_ALIAS
+    for over in (dict(out=1 * GB), dict(out=7 * GB), dict(s_out=3 * GB), dict(s_out=6 * GB),
+                 dict(out=4 * GB + 64)):
+        assert st(**over) == kda.KDA_ERR_BAD_ALIAS, over
+    # segments need their workspace
+    need = lib.kda_la_workspace_bytes(200, 2, 4, 128, 64)
+    assert need == (200 // 64 + 3) * 4 * (128 * 128 + 1) * 4
+    assert st(segment=64) == kda.KDA_ERR_NULL_ARG
+    assert st(segment=64, ws=20 * GB, ws_bytes=need - 1) == kda.KDA_ERR_BAD_WORKSPACE
+    assert st(segment=64, ws=20 * GB, ws_bytes=need) == kda.KDA_OK
+    for at in (6 * GB, 8 * GB, 7 * GB, 1 * GB):
+        assert st(segment=64, ws=at, ws_bytes=need) == kda.KDA_ERR_BAD_ALIAS, at
+    assert lib.kda_la_workspace_bytes(200, 2, 4, 128, 0) == 0
+    assert lib.kda_la_workspace_bytes(1 << 15, 1, 32, 128, 0) > 0
+    for bad in ((-1, 1, 4, 128, 0), (1, 0, 4, 128, 0), (1, 1, 0, 128, 0), (1, 1, 4, 100, 0),
+                (1 << 40, 1, 1 << 10, 128, 64), (1 << 62, 1, 4, 128, 0)):
+        assert lib.kda_la_workspace_bytes(*bad) == kda.KDA_ERR_BAD_SHAPE, bad
