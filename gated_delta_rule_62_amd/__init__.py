@@ -13,13 +13,15 @@ import os
 
 from . import serving
 from ._build import LIB_PATH, build  # noqa: F401  (build() is the in-tree compile step)
-from .serving import kda_la_fwd, kda_la_step, kda_la_workspace_bytes, kda_step
+from .serving import (kda_attn_fwd, kda_attn_workspace_bytes, kda_la_fwd, kda_la_step,
+                      kda_la_workspace_bytes, kda_step)
 
 __all__ = ["kda_fwd", "kda_fwd_sched", "kda_fwd_ordered", "kda_fwd_transposed_state",
            "kda_fwd_bf16_state",
            "kda_fwd_split", "kda_split_workspace_bytes", "kda_fwd_split_noalloc",
            "kda_longest_first", "kda_fwd_check", "c_args",
            "kda_step", "kda_la_step", "kda_la_fwd", "kda_la_workspace_bytes",
+           "kda_attn_fwd", "kda_attn_workspace_bytes",
            "kda_chunk_anchor", "kda_status_string", "KdaError", "library_path", "load_library"]
 
 KDA_OK = 0

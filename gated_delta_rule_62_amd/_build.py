@@ -8,7 +8,7 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_PATH = os.path.join(PKG_DIR, "libkda.so")
 SOURCES = ["kda_kernel.hip", "kda_api.cpp", "step_kernel.hip", "la_kernel.hip",
-           "ops_api.cpp"]
+           "attn_kernel.hip", "ops_api.cpp"]
 
 # Packed fp32 VALU forms are disabled for every device compile; hipcc's host pass
 # warns that it does not know the feature, which is harmless.

@@ -1,0 +1,597 @@
+// Causal softmax attention with grouped heads (kda_attn_fwd), for gfx950.
+//
+// Query i of a sequence with Lq queries and Lk keys sees keys j <= i + Lk - Lq:
+//     x_ij = scale q_i . k_j,   out_i = sum_j e^{x_ij} v_j / sum_j e^{x_ij},
+//     lse_i = log sum_j e^{x_ij}     (no visible key: out 0, lse minus infinity).
+//
+// Rows.  The G query heads of a key/value head read the same keys, so a row is a pair
+// (query token, head of the group): row r is token r / G, head r % G.  A workgroup owns a
+// tile of rows of one key/value head whatever G is, and a single token already fills G of
+// them.
+//
+// One pass over the keys with a running maximum and sum.  Both products keep the row in
+// the accumulator's column, x^T = K Q^T and out^T = V^T P^T: a lane then holds one row
+// (l % 16) and four keys, so the maximum, the sum and the rescaling factor are one value
+// per lane and tile, two cross-lane steps reduce a row, and two accumulator tiles of P^T
+// pack into the operand of the second product without passing through LDS (V^T is read
+// transposed from LDS in the same key order).  The maximum is only raised when a row
+// outgrows it by 2^8: p then reaches 256 at most, which costs no accuracy in a float, and
+// almost every step skips the rescaling of the output.  p is rounded to bf16 for the
+// product (the sum uses the unrounded p): with the output's own rounding that stays below
+// 1.5 roundings of out.
+//
+// Few rows leave the device idle; then `splits` workgroups share a tile's keys, write
+// unnormalised fp32 outputs with their maximum and sum, and a second kernel joins them.
+#include "api_util.h"
+#include "gfx950.h"
+#include "ops_params.h"
+
+namespace kda {
+namespace {
+
+using namespace dev;
+
+constexpr float kRaise = 8.f;  // base-2 slack of the running maximum
+constexpr float kNone = -__builtin_inff();
+
+// A tile of rows: its sequence's queries and keys, its rows.
+struct Tile {
+  int n;
+  int64_t q0, k0;   // first query and key token
+  int Lq, Lk;       // lengths
+  int row0, rows;   // first row of the tile, rows of the sequence (Lq * G)
+};
+
+__device__ __forceinline__ int64_t clamp64(int64_t x, int64_t lo, int64_t hi) {
+  return x < lo ? lo : (x > hi ? hi : x);
+}
+
+__device__ __forceinline__ void query_bounds(const AttnParams& p, int n, int64_t& a, int64_t& b) {
+  if (p.cu_q != nullptr) {
+    a = clamp64(p.cu_q[n], 0, p.Tq_total);
+    b = clamp64(p.cu_q[n + 1], a, p.Tq_total);
+  } else {
+    a = (int64_t)n * p.Tq;
+    b = a + p.Tq;
+  }
+}
+
+// Slot `slot` of a key/value head's tiles of ROWS rows; false if no tile has it.
+__device__ __forceinline__ bool find_tile(const AttnParams& p, int64_t slot, int tile_rows,
+                                          Tile& t) {
+  int lo = 0, hi = p.N - 1;
+  int64_t a, b;
+  if (p.cu_q == nullptr) {
+    const int64_t per = (p.Tq * p.G + tile_rows - 1) / tile_rows;
+    lo = (int)(slot / per);
+    if (lo >= p.N) return false;
+    t.row0 = (int)(slot % per) * tile_rows;
+    query_bounds(p, lo, a, b);
+  } else {
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      query_bounds(p, mid, a, b);
+      if (a * p.G / tile_rows + mid <= slot) lo = mid;
+      else hi = mid - 1;
+    }
+    query_bounds(p, lo, a, b);
+    const int64_t at = (slot - (a * p.G / tile_rows + lo)) * tile_rows;
+    if (at < 0 || at >= (b - a) * p.G) return false;
+    t.row0 = (int)at;
+  }
+  t.n = lo;
+  t.q0 = a;
+  t.Lq = (int)(b - a);
+  t.rows = t.Lq * p.G;
+  int64_t len;
+  if (p.cu_k != nullptr) {
+    t.k0 = clamp64(p.cu_k[lo], 0, p.Tk);
+    len = clamp64(p.cu_k[lo + 1], t.k0, p.Tk) - t.k0;
+  } else {
+    t.k0 = (int64_t)lo * p.Tk;
+    len = p.k_lens != nullptr ? clamp64(p.k_lens[lo], 0, p.Tk) : p.Tk;
+  }
+  t.Lk = (int)len;
+  return true;
+}
+
+__device__ __forceinline__ float max_over_groups(float x) {
+  Two t = swap16(x);
+  x = fmaxf(t.a, t.b);
+  t = swap32(x);
+  return fmaxf(t.a, t.b);
+}
+__device__ __forceinline__ float sum_over_groups(float x) {
+  Two t = swap16(x);
+  x = t.a + t.b;
+  t = swap32(x);
+  return t.a + t.b;
+}
+
+// Descriptor of `tokens` rows of one head from `base`; nothing when there are none.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const u16* base, int64_t row,
+                                                            int tokens, int D) {
+  return make_rsrc(base, tokens > 0 ? (uint32_t)(tokens - 1) * (uint32_t)(row * 2) + D * 2u : 0u);
+}
+
+__device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
+// Row state and output tiles of NI 16-row tiles: lane = row l16, d = 16 dt + 4 lg + i.
+template <int D, int NI>
+struct Acc {
+  static constexpr int DT = D / 16;
+  f32x4_t o[DT][NI];
+  float m[NI], l[NI];  // maximum of the scaled scores (base 2), this lane's part of the sum
+
+  __device__ __forceinline__ void init() {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      m[i] = kNone;
+      l[i] = 0.f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[d][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+  }
+
+  // Scores x (scaled, masked ones minus infinity) of JT 16-key tiles to probabilities.
+  template <int JT>
+  __device__ __forceinline__ void softmax(f32x4_t (&x)[JT][NI]) {
+    float top[NI];
+    bool raise = false;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      float t = kNone;
+#pragma unroll
+      for (int j = 0; j < JT; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) t = fmaxf(t, x[j][i][r]);
+      top[i] = max_over_groups(t);
+      raise |= top[i] > m[i] + kRaise;  // minus infinity plus kRaise: any score raises it
+    }
+    if (__any(raise)) {  // uniform
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const float now = fmaxf(m[i], top[i]);
+        const float f = now == kNone ? 1.f : __builtin_amdgcn_exp2f(m[i] - now);
+        m[i] = now;
+        l[i] *= f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d][i] *= f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const float base = m[i] == kNone ? 0.f : m[i];
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < JT; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float e = __builtin_amdgcn_exp2f(x[j][i][r] - base);
+          x[j][i][r] = e;
+          s += e;
+        }
+      l[i] += s;
+    }
+  }
+};
+
+// Probability tiles 2 js and 2 js + 1 as the operand of 32 keys.
+__device__ __forceinline__ u32x4_t p_op(f32x4_t a, f32x4_t b) {
+  return u32x4_t{pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(b[0], b[1]),
+                 pack_bf16(b[2], b[3])};
+}
+
+// One row's outputs, or with several splits its partial ones.  l is the whole sum.
+template <int D>
+__device__ __forceinline__ void store_row(const AttnParams& p, int64_t token, int head, int split,
+                                          int lg, const f32x4_t* o, float m, float l) {
+  const int64_t at = token * p.Hq + head;
+  if (p.splits > 1) {
+    const int64_t w = (int64_t)split * p.Tq_total * p.Hq + at;
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d)
+      *reinterpret_cast<f32x4_t*>(p.ws_o + w * D + 16 * d + 4 * lg) = o[d];
+    if (lg == 0) *reinterpret_cast<f32x2_t*>(p.ws_ml + 2 * w) = f32x2_t{m, l};
+    return;
+  }
+  const float f = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // no key: zero; NaN stays
+#pragma unroll
+  for (int d = 0; d < D / 16; ++d)
+    *reinterpret_cast<u32x2_t*>(p.out + at * D + 16 * d + 4 * lg) =
+        u32x2_t{pack_bf16(o[d][0] * f, o[d][1] * f), pack_bf16(o[d][2] * f, o[d][3] * f)};
+  if (p.lse != nullptr && lg == 0)
+    p.lse[at] = l == 0.f ? kNone : (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// ---- prompts: four waves share the keys' tiles in LDS, each owns NI 16-row tiles.
+template <int D, int NI>
+__global__ __launch_bounds__(kAttnThreads, NI <= 2 ? 2 : 1) void attn_tile_kernel(AttnParams p) {
+  constexpr int BN = kAttnKeys, JT = BN / 16, KS = D / 32, DT = D / 16;
+  constexpr int ROWS = 4 * 16 * NI;
+  constexpr int LD = D + 16;
+  constexpr int TPR = D / 8, RPP = kAttnThreads / TPR, PASSES = BN / RPP;
+  __shared__ alignas(16) u16 sk[2][BN][LD];
+  __shared__ alignas(16) u16 sv[2][BN][LD];
+
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // a key/value head's tiles share an XCD and its L2 (blocks go to the XCDs round robin);
+  // the last tiles of a sequence see the most keys and start first
+  const unsigned units = gridDim.x / (unsigned)p.splits;
+  const int split = (int)(blockIdx.x / units);
+  const unsigned unit = blockIdx.x % units;
+  const int hk = (int)(unit % (unsigned)p.Hk);
+  Tile t;
+  if (!find_tile(p, units / (unsigned)p.Hk - 1 - unit / (unsigned)p.Hk, ROWS, t)) return;
+
+  // ---- this wave's rows: their operand of the first product, their last visible key
+  const int off = t.Lk - t.Lq;
+  const int wrow = t.row0 + wave * 16 * NI;
+  u32x4_t q[KS][NI];
+  int last[NI];
+  int64_t tok[NI];
+  int head[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int r = wrow + 16 * i + l16;
+    const int w = r / p.G;
+    tok[i] = t.q0 + w;
+    head[i] = hk * p.G + r % p.G;
+    last[i] = r < t.rows ? w + off : -1;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) q[ks][i] = u32x4_t{0u, 0u, 0u, 0u};
+    if (r < t.rows) {
+      const u16* src = p.q + tok[i] * p.q_row + head[i] * D + 8 * lg;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) q[ks][i] = *reinterpret_cast<const u32x4_t*>(src + 32 * ks);
+    }
+  }
+  // keys some row of the tile, of this wave sees; keys every row of this wave sees
+  const int tile_end = min(t.rows, t.row0 + ROWS) - 1;
+  const int keys = max(0, min(t.Lk, tile_end / p.G + off + 1));
+  const int wave_keys =
+      wrow < t.rows ? max(0, min(t.Lk, (min(t.rows, wrow + 16 * NI) - 1) / p.G + off + 1)) : 0;
+  const int all_keys = wrow / p.G + off + 1;
+  // this split's steps
+  const int steps = (keys + BN - 1) / BN, per = (steps + p.splits - 1) / p.splits;
+  const int first = min(steps, split * per), end = min(steps, first + per);
+
+  const int lrow = tid / TPR, lcol = (tid % TPR) * 8;
+  const u16* kb = p.k + t.k0 * p.k_row + hk * D;
+  const u16* vb = p.v + t.k0 * p.v_row + hk * D;
+  u32x4_t rk[PASSES], rv[PASSES];
+  auto load = [&](int s) {
+    const int valid = min(BN, t.Lk - s * BN);
+    const __amdgpu_buffer_rsrc_t dk = rows_rsrc(kb + (int64_t)s * BN * p.k_row, p.k_row, valid, D),
+                                 dv = rows_rsrc(vb + (int64_t)s * BN * p.v_row, p.v_row, valid, D);
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      rk[i] = load16(dk, (uint32_t)(lrow + i * RPP) * (uint32_t)(p.k_row * 2) + lcol * 2u);
+      rv[i] = load16(dv, (uint32_t)(lrow + i * RPP) * (uint32_t)(p.v_row * 2) + lcol * 2u);
+    }
+  };
+  auto stage = [&](int b) {
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      *reinterpret_cast<u32x4_t*>(&sk[b][lrow + i * RPP][lcol]) = rk[i];
+      *reinterpret_cast<u32x4_t*>(&sv[b][lrow + i * RPP][lcol]) = rv[i];
+    }
+  };
+
+  Acc<D, NI> acc;
+  acc.init();
+  if (first < end) {
+    load(first);
+    stage(0);
+    if (first + 1 < end) load(first + 1);
+  }
+  lds_barrier();
+  for (int s = first; s < end; ++s) {
+    const int b = (s - first) & 1;
+    if (s + 1 < end) stage(b ^ 1);
+    if (s + 2 < end) load(s + 2);
+    if (s * BN < wave_keys) {  // uniform per wave
+      f32x4_t x[JT][NI];
+#pragma unroll
+      for (int j = 0; j < JT; ++j) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) x[j][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const u32x4_t k = *reinterpret_cast<const u32x4_t*>(&sk[b][16 * j + l16][32 * ks + 8 * lg]);
+#pragma unroll
+          for (int i = 0; i < NI; ++i) x[j][i] = mfma(k, q[ks][i], x[j][i]);
+        }
+      }
+      if ((s + 1) * BN > all_keys) {  // uniform: some row does not see all of these keys
+#pragma unroll
+        for (int j = 0; j < JT; ++j)
+#pragma unroll
+          for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              x[j][i][r] = s * BN + 16 * j + 4 * lg + r <= last[i] ? x[j][i][r] * p.c : kNone;
+      } else {
+#pragma unroll
+        for (int j = 0; j < JT; ++j)
+#pragma unroll
+          for (int i = 0; i < NI; ++i) x[j][i] *= p.c;
+      }
+      acc.softmax(x);
+#pragma unroll
+      for (int js = 0; js < JT / 2; ++js) {
+        u32x4_t pr[NI];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) pr[i] = p_op(x[2 * js][i], x[2 * js + 1][i]);
+        const int row = 32 * js + 4 * lg + (l16 >> 2);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          const int c = 16 * d + 4 * (l16 & 3);
+          const u32x2_t lo = ds_read_tr(&sv[b][row][c]), hi = ds_read_tr(&sv[b][row + 16][c]);
+          const u32x4_t vt = {lo[0], lo[1], hi[0], hi[1]};
+#pragma unroll
+          for (int i = 0; i < NI; ++i) acc.o[d][i] = mfma(vt, pr[i], acc.o[d][i]);
+        }
+      }
+    }
+    lds_barrier();
+  }
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const float l = sum_over_groups(acc.l[i]);
+    if (wrow + 16 * i + l16 < t.rows) {
+      f32x4_t o[DT];
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[d] = acc.o[d][i];
+      store_row<D>(p, tok[i], head[i], split, lg, o, acc.m[i], l);
+    }
+  }
+}
+
+// ---- single tokens: the four waves share NI 16-row tiles and take 32 keys each in turn.
+// A key is read by one wave only, so k goes from memory into operand registers and v
+// through a piece of LDS of the wave's own (for its transposed reads); no barrier until
+// the waves join their results.
+template <int D, int NI>
+__global__ __launch_bounds__(kAttnThreads, NI <= 2 ? 2 : 1) void attn_token_kernel(AttnParams p) {
+  constexpr int KEYS = 32, JT = 2, KS = D / 32, DT = D / 16;
+  constexpr int ROWS = 16 * NI;
+  constexpr int LD = D + 16;
+  constexpr int TPR = D / 8, RPP = 64 / TPR, PASSES = KEYS / RPP;
+  constexpr int LO = D + 4;  // row stride of the join buffer (floats)
+  union Smem {
+    u16 v[4][KEYS][LD];
+    float o[4][16][LO];
+  };
+  __shared__ alignas(16) Smem sm;
+  __shared__ float sml[4][ROWS][2];
+
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const unsigned units = gridDim.x / (unsigned)p.splits;
+  const int split = (int)(blockIdx.x / units);
+  const unsigned unit = blockIdx.x % units;
+  const int hk = (int)(unit % (unsigned)p.Hk);
+  Tile t;
+  if (!find_tile(p, unit / (unsigned)p.Hk, ROWS, t)) return;
+
+  const int off = t.Lk - t.Lq;
+  u32x4_t q[KS][NI];
+  int last[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int r = t.row0 + 16 * i + l16;
+    last[i] = r < t.rows ? r / p.G + off : -1;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) q[ks][i] = u32x4_t{0u, 0u, 0u, 0u};
+    if (r < t.rows) {
+      const u16* src = p.q + (t.q0 + r / p.G) * p.q_row + (hk * p.G + r % p.G) * D + 8 * lg;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) q[ks][i] = *reinterpret_cast<const u32x4_t*>(src + 32 * ks);
+    }
+  }
+  const int keys = max(0, min(t.Lk, (min(t.rows, t.row0 + ROWS) - 1) / p.G + off + 1));
+  const int all_keys = t.row0 / p.G + off + 1;
+  const int steps = (keys + KEYS - 1) / KEYS, per = (steps + p.splits - 1) / p.splits;
+  const int first = min(steps, split * per), end = min(steps, first + per);
+
+  const int lrow = lane / TPR, lcol = (lane % TPR) * 8;
+  const u16* kb = p.k + t.k0 * p.k_row + hk * D;
+  const u16* vb = p.v + t.k0 * p.v_row + hk * D;
+  const uint32_t k_row = (uint32_t)(p.k_row * 2), v_row = (uint32_t)(p.v_row * 2);
+  u32x4_t rk[JT][KS], rv[PASSES];
+  auto load = [&](int s) {
+    const int valid = min(KEYS, t.Lk - s * KEYS);
+    const __amdgpu_buffer_rsrc_t dk =
+                                     rows_rsrc(kb + (int64_t)s * KEYS * p.k_row, p.k_row, valid, D),
+                                 dv =
+                                     rows_rsrc(vb + (int64_t)s * KEYS * p.v_row, p.v_row, valid, D);
+#pragma unroll
+    for (int j = 0; j < JT; ++j)
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+        rk[j][ks] = load16(dk, (uint32_t)(16 * j + l16) * k_row + 64u * ks + 16u * lg);
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i)
+      rv[i] = load16(dv, (uint32_t)(lrow + i * RPP) * v_row + lcol * 2u);
+  };
+
+  Acc<D, NI> acc;
+  acc.init();
+  int s = first + wave;
+  if (s < end) load(s);
+  for (; s < end; s += 4) {
+    f32x4_t x[JT][NI];
+#pragma unroll
+    for (int j = 0; j < JT; ++j) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) x[j][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int i = 0; i < NI; ++i) x[j][i] = mfma(rk[j][ks], q[ks][i], x[j][i]);
+    }
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i)
+      *reinterpret_cast<u32x4_t*>(&sm.v[wave][lrow + i * RPP][lcol]) = rv[i];
+    if (s + 4 < end) load(s + 4);
+    if ((s + 1) * KEYS > all_keys) {
+#pragma unroll
+      for (int j = 0; j < JT; ++j)
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            x[j][i][r] = s * KEYS + 16 * j + 4 * lg + r <= last[i] ? x[j][i][r] * p.c : kNone;
+    } else {
+#pragma unroll
+      for (int j = 0; j < JT; ++j)
+#pragma unroll
+        for (int i = 0; i < NI; ++i) x[j][i] *= p.c;
+    }
+    acc.softmax(x);
+    wave_lds_sync();
+    u32x4_t pr[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) pr[i] = p_op(x[0][i], x[1][i]);
+    const int row = 4 * lg + (l16 >> 2);
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+      const int c = 16 * d + 4 * (l16 & 3);
+      const u32x2_t lo = ds_read_tr(&sm.v[wave][row][c]), hi = ds_read_tr(&sm.v[wave][row + 16][c]);
+      const u32x4_t vt = {lo[0], lo[1], hi[0], hi[1]};
+#pragma unroll
+      for (int i = 0; i < NI; ++i) acc.o[d][i] = mfma(vt, pr[i], acc.o[d][i]);
+    }
+    wave_lds_sync();
+  }
+
+  // ---- join the waves: maxima and sums first, then the outputs, one 16-row tile at a time
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const float l = sum_over_groups(acc.l[i]);
+    if (lg == 0) {
+      sml[wave][16 * i + l16][0] = acc.m[i];
+      sml[wave][16 * i + l16][1] = l;
+    }
+  }
+  lds_barrier();  // also: every wave's reads of v are done
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    float m = kNone, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m = fmaxf(m, sml[w][16 * i + l16][0]);
+    const float base = m == kNone ? 0.f : m;
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      l += sml[w][16 * i + l16][1] * __builtin_amdgcn_exp2f(sml[w][16 * i + l16][0] - base);
+    const float f = __builtin_amdgcn_exp2f(acc.m[i] - base);
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+      *reinterpret_cast<f32x4_t*>(&sm.o[wave][l16][16 * d + 4 * lg]) = acc.o[d][i] * f;
+    lds_barrier();
+    // thread: row tid / 16, D / 16 columns from (tid % 16) * 4 in strides of 64
+    const int rr = tid >> 4, r = t.row0 + 16 * i + rr;
+    float mr = kNone, lr = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) mr = fmaxf(mr, sml[w][16 * i + rr][0]);
+    const float br = mr == kNone ? 0.f : mr;
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      lr += sml[w][16 * i + rr][1] * __builtin_amdgcn_exp2f(sml[w][16 * i + rr][0] - br);
+    if (r < t.rows) {
+      const int64_t at = (t.q0 + r / p.G) * p.Hq + hk * p.G + r % p.G;
+      const int64_t w = (int64_t)split * p.Tq_total * p.Hq + at;
+      const float g = lr > 0.f ? 1.f / lr : lr == 0.f ? 0.f : lr;
+#pragma unroll
+      for (int cc = 0; cc < D / 64; ++cc) {
+        const int c = 64 * cc + 4 * (tid & 15);
+        f32x4_t o = *reinterpret_cast<const f32x4_t*>(&sm.o[0][rr][c]);
+#pragma unroll
+        for (int ww = 1; ww < 4; ++ww) o += *reinterpret_cast<const f32x4_t*>(&sm.o[ww][rr][c]);
+        if (p.splits > 1) {
+          *reinterpret_cast<f32x4_t*>(p.ws_o + w * D + c) = o;
+        } else {
+          *reinterpret_cast<u32x2_t*>(p.out + at * D + c) =
+              u32x2_t{pack_bf16(o[0] * g, o[1] * g), pack_bf16(o[2] * g, o[3] * g)};
+        }
+      }
+      if ((tid & 15) == 0) {
+        if (p.splits > 1) *reinterpret_cast<f32x2_t*>(p.ws_ml + 2 * w) = f32x2_t{mr, lr};
+        else if (p.lse != nullptr)
+          p.lse[at] = lr == 0.f ? kNone : (mr + __builtin_amdgcn_logf(lr)) * kLn2;
+      }
+    }
+    if (i + 1 < NI) lds_barrier();
+  }
+}
+
+// Joins the splits of a row: D / 4 threads per (query token, head).
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
+  constexpr int TPR = D / 4;
+  const int64_t at = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
+  const int64_t rows = p.Tq_total * p.Hq;
+  if (at >= rows) return;
+  if (p.cu_q != nullptr) {  // a query outside every sequence keeps its rows
+    const int64_t token = at / p.Hq;
+    if (token < p.cu_q[0] || token >= p.cu_q[p.N]) return;
+  }
+  const int c = (threadIdx.x % TPR) * 4;
+  float m = kNone;
+  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, p.ws_ml[2 * (s * rows + at)]);
+  const float base = m == kNone ? 0.f : m;
+  float l = 0.f;
+  f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < p.splits; ++s) {
+    const int64_t w = s * rows + at;
+    const f32x2_t ml = *reinterpret_cast<const f32x2_t*>(p.ws_ml + 2 * w);
+    const float f = __builtin_amdgcn_exp2f(ml[0] - base);
+    l += ml[1] * f;
+    o += *reinterpret_cast<const f32x4_t*>(p.ws_o + w * D + c) * f;
+  }
+  const float g = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+  *reinterpret_cast<u32x2_t*>(p.out + at * D + c) =
+      u32x2_t{pack_bf16(o[0] * g, o[1] * g), pack_bf16(o[2] * g, o[3] * g)};
+  if (p.lse != nullptr && c == 0) p.lse[at] = l == 0.f ? kNone : (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+template <int D>
+hipError_t go(const AttnParams& p, const AttnSchedule& s, hipStream_t stream) {
+  int64_t slots = attn_slots(p.Tq_total, p.N, p.G, s.rows);
+  if (p.cu_q == nullptr) slots = p.N * ((p.Tq * p.G + s.rows - 1) / s.rows);
+  const dim3 grid((unsigned)(slots * p.Hk * p.splits));
+  if (s.tokens) {
+    if (s.tiles16 == 1) attn_token_kernel<D, 1><<<grid, kAttnThreads, 0, stream>>>(p);
+    else if (s.tiles16 == 2) attn_token_kernel<D, 2><<<grid, kAttnThreads, 0, stream>>>(p);
+    else attn_token_kernel<D, 4><<<grid, kAttnThreads, 0, stream>>>(p);
+  } else {
+    attn_tile_kernel<D, 2><<<grid, kAttnThreads, 0, stream>>>(p);
+  }
+  if (p.splits > 1) {
+    const int64_t rows = p.Tq_total * p.Hq, per = 256 / (D / 4);
+    attn_join_kernel<D><<<dim3((unsigned)((rows + per - 1) / per)), 256, 0, stream>>>(p);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+AttnSchedule attn_schedule(int64_t Tq_total, int64_t N, int64_t G, int D) {
+  (void)D;
+  const int64_t mean = (Tq_total * G + N - 1) / N;  // rows of a sequence and key/value head
+  if (mean <= 64) {
+    const int tiles = mean <= 16 ? 1 : mean <= 32 ? 2 : 4;
+    return AttnSchedule{1, tiles, 16 * tiles};
+  }
+  return AttnSchedule{0, 2, 128};
+}
+
+hipError_t launch_attn(const AttnParams& p, const AttnSchedule& s, int D, hipStream_t stream) {
+  return D == 64 ? go<64>(p, s, stream) : go<128>(p, s, stream);
+}
+
+}  // namespace kda

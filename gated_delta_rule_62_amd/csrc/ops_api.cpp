@@ -210,6 +210,86 @@ int la_check(const void* q, int64_t q_row, const void* k, int64_t k_row, const v
   return KDA_OK;
 }
 
+// Parts of each row's keys when the caller leaves the choice: as many as give each compute
+// unit kWant workgroups, with at least kLeast keys a part (of a sequence of mean length).
+int64_t attn_auto_splits(const kda::AttnSchedule& s, int64_t slots, int64_t Hk, int64_t mean_k) {
+  const int64_t want = (s.tokens ? 4 : 2) * (int64_t)kda::device_cus();
+  const int64_t least = s.tokens ? 256 : 512;
+  int64_t n = want / (slots * Hk);
+  if (n > mean_k / least) n = mean_k / least;
+  return n < 1 ? 1 : n > 64 ? 64 : n;
+}
+
+// Sizes of a kda_attn_fwd call to its schedule and splits.  Keys are packed when one row of
+// keys serves several sequences (Bk == 1).
+int attn_sizes(int64_t N, int64_t Bq, int64_t Tq, int64_t Bk, int64_t Tk, int64_t Hq, int64_t Hk,
+               int64_t D, int64_t splits, kda::AttnSchedule* sched, int64_t* splits_out) {
+  if (D != 64 && D != 128) return KDA_ERR_BAD_SHAPE;
+  if (Hk < 1 || Hq < 1 || Hq % Hk != 0 || Hq >= (1 << 24)) return KDA_ERR_BAD_SHAPE;
+  if (N < 1 || N >= ((int64_t)1 << 31) || Bq < 1 || Bk < 1 || Tq < 0 || Tk < 0)
+    return KDA_ERR_BAD_SHAPE;
+  if ((Bq != 1 && Bq != N) || (Bk != 1 && Bk != N)) return KDA_ERR_BAD_VARLEN;
+  // rows and keys of a sequence are 32-bit numbers
+  if (Tk > ((int64_t)1 << 30) || Tq > ((int64_t)1 << 30) / (Hq / Hk)) return KDA_ERR_BAD_SHAPE;
+  if (Tq > ((int64_t)1 << 40) / Bq || Tk > ((int64_t)1 << 40) / Bk) return KDA_ERR_BAD_SHAPE;
+  if (splits < 0 || splits > 64) return KDA_ERR_BAD_SCHEDULE;
+  const int64_t G = Hq / Hk, total = Bq * Tq;
+  *sched = kda::attn_schedule(total, N, G, static_cast<int>(D));
+  const int64_t slots = kda::attn_slots(total, N, G, sched->rows);  // at least the batched count
+  const int64_t mean_k = Bk == 1 ? Tk / N : Tk;
+  int64_t sp = splits ? splits : attn_auto_splits(*sched, slots, Hk, mean_k);
+  // every launch below 2^32 work-items
+  const int64_t most = (((int64_t)1 << 32) - 1) / kda::kAttnThreads;
+  if (slots > most / Hk || total > most / Hq) return KDA_ERR_BAD_SHAPE;
+  if (slots * Hk > most / sp) {
+    if (splits) return KDA_ERR_BAD_SHAPE;
+    sp = 1;
+  }
+  *splits_out = sp;
+  return KDA_OK;
+}
+
+int64_t attn_ws_bytes(int64_t total, int64_t Hq, int64_t D, int64_t splits) {
+  return splits > 1 ? splits * total * Hq * (D + 2) * 4 : 0;
+}
+
+int attn_check(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
+               int64_t v_row, float scale, const void* out, const float* lse, const int64_t* cu_q,
+               const int64_t* cu_k, const int64_t* k_lens, int64_t N, int64_t Bq, int64_t Tq,
+               int64_t Bk, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D, int64_t splits,
+               const void* workspace, int64_t workspace_bytes, kda::AttnSchedule* sched,
+               int64_t* splits_out) {
+  int64_t sp = 1;
+  const int st = attn_sizes(N, Bq, Tq, Bk, Tk, Hq, Hk, D, splits, sched, &sp);
+  if (st != KDA_OK) return st;
+  if ((cu_q ? Bq != 1 : Bq != N) || (cu_k ? Bk != 1 : Bk != N) || (cu_k && k_lens))
+    return KDA_ERR_BAD_VARLEN;
+  if (!std::isfinite(scale) || scale < 0.f) return KDA_ERR_BAD_SCALE;
+  const int64_t nq = Bq * Tq, nk = Bk * Tk;
+  if ((nq > 0 && (!q || !out)) || (nq > 0 && nk > 0 && (!k || !v))) return KDA_ERR_NULL_ARG;
+  if (q_row >= (1 << 24) || k_row >= (1 << 24) || v_row >= (1 << 24)) return KDA_ERR_BAD_SHAPE;
+  if (!row_ok(q_row, Hq, D) || !row_ok(k_row, Hk, D) || !row_ok(v_row, Hk, D) || !aligned16(q) ||
+      !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(workspace))
+    return KDA_ERR_BAD_LAYOUT;
+  if (splits == 0 && !workspace) sp = 1;  // left to the library: without one, no splits
+  const int64_t need = attn_ws_bytes(nq, Hq, D, sp);
+  if (need > 0 && !workspace) return KDA_ERR_NULL_ARG;
+  if (need > workspace_bytes) return KDA_ERR_BAD_WORKSPACE;
+  const Range ro = make_range(out, nq * Hq * D * 2), rl = make_range(lse, lse ? nq * Hq * 4 : 0),
+              rw = make_range(workspace, need);
+  const Range ins[] = {make_range(q, span_bytes(nq, q_row, Hq, D)),
+                       make_range(k, span_bytes(nk, k_row, Hk, D)),
+                       make_range(v, span_bytes(nk, v_row, Hk, D)),
+                       make_range(cu_q, cu_q ? (N + 1) * 8 : 0),
+                       make_range(cu_k, cu_k ? (N + 1) * 8 : 0),
+                       make_range(k_lens, k_lens ? N * 8 : 0)};
+  if (any_overlap(ro, ins, 6) || any_overlap(rl, ins, 6) || any_overlap(rw, ins, 6) ||
+      overlaps(ro, rl) || overlaps(ro, rw) || overlaps(rl, rw))
+    return KDA_ERR_BAD_ALIAS;
+  *splits_out = sp;
+  return KDA_OK;
+}
+
 int status(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_HIP; }
 
 }  // namespace
@@ -355,6 +435,65 @@ int kda_la_fwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const
     p.ws_decay = p.ws + p.slots * H * D * D;
   }
   return status(kda::launch_la(p, static_cast<int>(D), static_cast<hipStream_t>(stream)));
+}
+
+int64_t kda_attn_workspace_bytes(int64_t num_seqs, int64_t Bq, int64_t Tq, int64_t Bk, int64_t Tk,
+                                 int64_t Hq, int64_t Hk, int64_t D, int64_t splits) {
+  kda::AttnSchedule sched;
+  int64_t sp = 1;
+  const int st = attn_sizes(num_seqs, Bq, Tq, Bk, Tk, Hq, Hk, D, splits, &sched, &sp);
+  return st != KDA_OK ? st : attn_ws_bytes(Bq * Tq, Hq, D, sp);
+}
+
+int kda_attn_fwd_check(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
+                       int64_t v_row, float scale, const void* out, const float* lse,
+                       const int64_t* cu_seqlens_q, const int64_t* cu_seqlens_k,
+                       const int64_t* k_lens, int64_t num_seqs, int64_t Bq, int64_t Tq, int64_t Bk,
+                       int64_t Tk, int64_t Hq, int64_t Hk, int64_t D, int64_t splits,
+                       const void* workspace, int64_t workspace_bytes) {
+  kda::AttnSchedule sched;
+  int64_t sp = 1;
+  return attn_check(q, q_row, k, k_row, v, v_row, scale, out, lse, cu_seqlens_q, cu_seqlens_k,
+                    k_lens, num_seqs, Bq, Tq, Bk, Tk, Hq, Hk, D, splits, workspace,
+                    workspace_bytes, &sched, &sp);
+}
+
+int kda_attn_fwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
+                 int64_t v_row, float scale, void* out, float* lse, const int64_t* cu_seqlens_q,
+                 const int64_t* cu_seqlens_k, const int64_t* k_lens, int64_t num_seqs, int64_t Bq,
+                 int64_t Tq, int64_t Bk, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D,
+                 int64_t splits, void* workspace, int64_t workspace_bytes, void* stream) {
+  kda::AttnSchedule sched;
+  int64_t sp = 1;
+  const int st = attn_check(q, q_row, k, k_row, v, v_row, scale, out, lse, cu_seqlens_q,
+                            cu_seqlens_k, k_lens, num_seqs, Bq, Tq, Bk, Tk, Hq, Hk, D, splits,
+                            workspace, workspace_bytes, &sched, &sp);
+  if (st != KDA_OK || Bq * Tq == 0) return st;
+  kda::AttnParams p = {};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.cu_q = cu_seqlens_q;
+  p.cu_k = cu_seqlens_k;
+  p.k_lens = k_lens;
+  p.q_row = q_row;
+  p.k_row = k_row;
+  p.v_row = v_row;
+  p.Tq = Tq;
+  p.Tk = Tk;
+  p.Tq_total = Bq * Tq;
+  p.N = static_cast<int32_t>(num_seqs);
+  p.Hq = static_cast<int32_t>(Hq);
+  p.Hk = static_cast<int32_t>(Hk);
+  p.G = static_cast<int32_t>(Hq / Hk);
+  p.c = static_cast<float>(scale * 1.4426950408889634);
+  p.splits = static_cast<int32_t>(sp);
+  p.ws_o = static_cast<float*>(workspace);
+  p.ws_ml = sp > 1 ? p.ws_o + sp * p.Tq_total * Hq * D : nullptr;
+  return status(
+      kda::launch_attn(p, sched, static_cast<int>(D), static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

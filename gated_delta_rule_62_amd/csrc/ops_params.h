@@ -72,6 +72,44 @@ constexpr int64_t la_ws_floats(int64_t slots, int64_t H, int64_t D) {
 
 hipError_t launch_la(const LaParams& p, int D, hipStream_t stream);
 
+// Causal softmax attention with grouped heads: kda_attn_fwd.
+struct AttnParams {
+  const uint16_t* q;       // bf16 [query tokens, Hq, D], rows q_row elements apart
+  const uint16_t* k;       // bf16 [key tokens, Hk, D], rows k_row apart
+  const uint16_t* v;       // bf16 [key tokens, Hk, D], rows v_row apart
+  uint16_t* out;           // bf16 [query tokens, Hq, D]
+  float* lse;              // fp32 [query tokens, Hq] or nullptr
+  const int64_t* cu_q;     // [N + 1] or nullptr (every sequence has Tq queries)
+  const int64_t* cu_k;     // [N + 1] or nullptr (sequence n has row n of Tk keys)
+  const int64_t* k_lens;   // [N] keys in use of each row, or nullptr (all)
+  int64_t q_row, k_row, v_row;
+  int64_t Tq, Tk;          // query and key tokens of one batch row
+  int64_t Tq_total;
+  int32_t N, Hq, Hk, G;    // G = Hq / Hk query heads share a key/value head
+  float c;                 // scale * log2(e)
+  int32_t splits;          // parts of a row's keys, joined by a second kernel when above 1
+  float* ws_o;             // [splits, query tokens, Hq, D] unnormalised outputs
+  float* ws_ml;            // [splits, query tokens, Hq, 2] running maximum (base 2) and sum
+};
+
+// The schedule of a call: rows are (query token, head of the group) pairs of one key/value
+// head; a workgroup owns a tile of them.
+struct AttnSchedule {
+  int tokens;              // 1: the kernel whose waves split the keys; 0: the tile kernel
+  int tiles16;             // 16-row tiles per wave (tile kernel) or workgroup (token kernel)
+  int rows;                // rows per workgroup
+};
+
+AttnSchedule attn_schedule(int64_t Tq_total, int64_t N, int64_t G, int D);
+// Tiles of one key/value head: a sequence's tiles never share a slot with another's.
+constexpr int64_t attn_slots(int64_t Tq_total, int64_t N, int64_t G, int64_t rows) {
+  return Tq_total * G / rows + N;
+}
+constexpr int kAttnThreads = 256;
+constexpr int kAttnKeys = 64;  // keys per step of the tile kernel
+
+hipError_t launch_attn(const AttnParams& p, const AttnSchedule& s, int D, hipStream_t stream);
+
 }  // namespace kda
 
 #endif  // KDA_OPS_PARAMS_H_

@@ -1,4 +1,5 @@
-"""Bindings of the serving operators: the single-token recurrences on pooled states.
+"""Bindings of the serving operators: the single-token recurrences on pooled states, linear
+attention with one decay per head, and causal softmax attention with grouped heads.
 
 Like the package's other bindings they check dtypes, shapes, devices and strides, pass raw
 pointers, sizes and torch's current stream to the C ABI declared in ``include/kda.h``, and
@@ -14,18 +15,21 @@ _STEP = [_VP] * 5 + [_F32] + [_VP] * 3 + [_F32, _VP, _I32, _I64, _VP, _VP] + [_I
 _LA_STEP = ([_VP, _I64] * 3 + [_VP, _VP, _F32, _VP, _VP, _I32, _I64, _VP, _VP] + [_I64] * 4)
 _LA_FWD = ([_VP, _I64] * 3 + [_VP, _VP, _F32, _VP, _VP, _I32, _VP, _I32, _VP] + [_I64] * 7
            + [_VP, _I64])
+_ATTN_FWD = ([_VP, _I64] * 3 + [_F32] + [_VP] * 5 + [_I64] * 9 + [_VP, _I64])
 
 
 def declare(lib) -> None:
     """Sets the argument types of the serving operators' C functions."""
     for name, args in (("kda_step", _STEP), ("kda_la_step", _LA_STEP),
-                       ("kda_la_fwd", _LA_FWD)):
+                       ("kda_la_fwd", _LA_FWD), ("kda_attn_fwd", _ATTN_FWD)):
         getattr(lib, name).argtypes = args + [_VP]
         getattr(lib, name).restype = _I32
         getattr(lib, name + "_check").argtypes = args
         getattr(lib, name + "_check").restype = _I32
     lib.kda_la_workspace_bytes.argtypes = [_I64] * 5
     lib.kda_la_workspace_bytes.restype = _I64
+    lib.kda_attn_workspace_bytes.argtypes = [_I64] * 9
+    lib.kda_attn_workspace_bytes.restype = _I64
 
 
 def _lib():
@@ -233,3 +237,53 @@ def kda_la_fwd(q, k, v, g, scale, out, decay=None, initial_state=None, final_sta
             *_state("final_state", final_state, N, H, D, dev), cu, N, B, T, H, Hk, D,
             int(segment), ws, ws_bytes, _stream_ptr(stream, dev))
     _launch(lib.kda_la_fwd, dev, args)
+
+
+def kda_attn_workspace_bytes(num_seqs: int, Bq: int, Tq: int, Bk: int, Tk: int, Hq: int, Hk: int,
+                             D: int, splits: int = 0) -> int:
+    """Bytes of the workspace of ``kda_attn_fwd`` (0: this call needs none)."""
+    n = _lib().kda_attn_workspace_bytes(int(num_seqs), int(Bq), int(Tq), int(Bk), int(Tk), int(Hq),
+                                        int(Hk), int(D), int(splits))
+    if n < 0:
+        _raise(int(n))
+    return int(n)
+
+
+def kda_attn_fwd(q, k, v, scale, out, lse=None, cu_seqlens_q=None, cu_seqlens_k=None, k_lens=None,
+                 splits: int = 0, workspace=None, stream=None) -> None:
+    """Causal softmax attention with grouped heads (asynchronous on ``stream``).  Query i of a
+    sequence of Lq queries and Lk keys sees keys ``j <= i + Lk - Lq``; one that sees none
+    gets out 0 and lse minus infinity.
+
+    q: bf16 ``[Bq,Tq,Hq,D]``, k, v: bf16 ``[Bk,Tk,Hk,D]`` with Hq a multiple of Hk (views with
+    one row stride are taken as they are); out: bf16 ``[Bq,Tq,Hq,D]``; lse: fp32
+    ``[Bq,Tq,Hq]`` or None.  Queries are packed (``cu_seqlens_q`` int64 ``[N+1]``, Bq == 1) or
+    batch rows; keys are packed (``cu_seqlens_k``, Bk == 1) or batch rows of a cache of which
+    the first ``k_lens[n]`` (int64 ``[N]``; None: all) are in use.  ``splits``: 0 (automatic)
+    or parts of each row's keys; ``workspace``: a uint8 tensor of at least
+    ``kda_attn_workspace_bytes(...)`` bytes for this call alone; None takes one from torch's
+    allocator where the call needs it.
+    """
+    import torch
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k must be [B,T,heads,D]")
+    Bq, Tq, Hq, D = q.shape
+    Bk, Tk, Hk, _ = k.shape
+    dev = _device(q)
+    if torch.cuda.current_device() != dev.index:  # schedules go by the current device
+        with torch.cuda.device(dev):
+            return kda_attn_fwd(q, k, v, scale, out, lse, cu_seqlens_q, cu_seqlens_k, k_lens,
+                                splits, workspace, stream)
+    N = cu_seqlens_q.numel() - 1 if cu_seqlens_q is not None else Bq
+    lib = _lib()
+    need = lib.kda_attn_workspace_bytes(N, Bq, Tq, Bk, Tk, Hq, Hk, D, int(splits))
+    ws, ws_bytes, _keep = _workspace(workspace, max(need, 0), dev, stream)
+    args = (*_rows("q", q, (Bq, Tq, Hq, D), dev), *_rows("k", k, (Bk, Tk, Hk, D), dev),
+            *_rows("v", v, (Bk, Tk, Hk, D), dev), float(scale),
+            _tensor("out", out, torch.bfloat16, (Bq, Tq, Hq, D), dev),
+            _optional("lse", lse, torch.float32, (Bq, Tq, Hq), dev),
+            _optional("cu_seqlens_q", cu_seqlens_q, torch.int64, (N + 1,), dev),
+            _optional("cu_seqlens_k", cu_seqlens_k, torch.int64, (N + 1,), dev),
+            _optional("k_lens", k_lens, torch.int64, (N,), dev), N, Bq, Tq, Bk, Tk, Hq, Hk, D,
+            int(splits), ws, ws_bytes, _stream_ptr(stream, dev))
+    _launch(lib.kda_attn_fwd, dev, args)

@@ -463,6 +463,65 @@ int kda_la_fwd_check(const void* q, int64_t q_row, const void* k, int64_t k_row,
 int64_t kda_la_workspace_bytes(int64_t T_total, int64_t num_seqs, int64_t H, int64_t D,
                                int64_t segment);
 
+/*
+ * kda_attn_fwd -- causal softmax attention with grouped heads, for the layers of a model
+ * that are not recurrent: whole prompts, prompts that continue earlier keys, and single
+ * (or a few drafted) tokens over key/value caches.  Query i of a sequence with Lq queries
+ * and Lk keys sees keys j <= i + Lk - Lq, its queries being the last Lq of its positions:
+ *
+ *     out_i = sum_j softmax_j(scale q_i . k_j) v_j,    lse_i = log sum_j exp(scale q_i . k_j)
+ *
+ * and a query that sees no key (Lk < Lq, or no keys) gets out 0 and lse minus infinity.
+ *   q              bf16 [Bq, Tq, Hq, D], row stride q_row (below 2^24).
+ *   k, v           bf16 [Bk, Tk, Hk, D], row strides k_row, v_row (below 2^24); query head h
+ *                  uses key/value head h / (Hq / Hk).  Batch rows follow each other: token t
+ *                  of batch row b is row b * T + t.
+ *   scale          finite and not negative (KDA_ERR_BAD_SCALE).
+ *   out            bf16 [Bq, Tq, Hq, D], contiguous.
+ *   lse            fp32 [Bq, Tq, Hq], or NULL.
+ *   cu_seqlens_q   int64 [num_seqs + 1] device array (Bq == 1): sequence n's queries are
+ *                  tokens [cu[n], cu[n+1]); or NULL (Bq == num_seqs): batch row n, Tq each.
+ *   cu_seqlens_k   the same for keys (Bk == 1); or NULL (Bk == num_seqs): batch row n, of
+ *                  which the first k_lens[n] keys are in use.
+ *   k_lens         int64 [num_seqs] device array, clamped into [0, Tk]; NULL: all Tk.  Not
+ *                  with cu_seqlens_k (KDA_ERR_BAD_VARLEN).  Keys behind a sequence's last
+ *                  are never used, whatever they hold.
+ *                  Offsets as for kda_fwd's cu_seqlens: not checked on the host, clamped on
+ *                  the device.  Query tokens outside every sequence keep their out and lse
+ *                  rows as they were.
+ *   Hq, Hk, D      Hq % Hk == 0, D in {64, 128}.  Tk <= 2^30, Tq * Hq / Hk <= 2^30.
+ *   splits         0 (automatic), or 1 .. 64 parts of each row's keys
+ *                  (KDA_ERR_BAD_SCHEDULE): few rows over long keys fill the device only
+ *                  when several workgroups share a row.  Each writes a partial result and a
+ *                  second kernel joins them.
+ *   workspace      caller-owned device memory, 16-byte aligned, of at least
+ *                  kda_attn_workspace_bytes(num_seqs, Bq, Tq, Bk, Tk, Hq, Hk, D, splits)
+ *                  bytes (KDA_ERR_BAD_WORKSPACE), scratch on return: calls that may overlap
+ *                  in time need one each.  With splits 0 it may be NULL: one part then.
+ * Scores and sums are fp32; probabilities are rounded to bf16 for their product with v.  A
+ * non-finite v of one key may reach the outputs of earlier queries of its sequence and
+ * head whose tile of keys it shares (zero probability times it).
+ */
+int kda_attn_fwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
+                 int64_t v_row, float scale, void* out, float* lse, const int64_t* cu_seqlens_q,
+                 const int64_t* cu_seqlens_k, const int64_t* k_lens, int64_t num_seqs, int64_t Bq,
+                 int64_t Tq, int64_t Bk, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D,
+                 int64_t splits, void* workspace, int64_t workspace_bytes, void* stream);
+int kda_attn_fwd_check(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
+                       int64_t v_row, float scale, const void* out, const float* lse,
+                       const int64_t* cu_seqlens_q, const int64_t* cu_seqlens_k,
+                       const int64_t* k_lens, int64_t num_seqs, int64_t Bq, int64_t Tq, int64_t Bk,
+                       int64_t Tk, int64_t Hq, int64_t Hk, int64_t D, int64_t splits,
+                       const void* workspace, int64_t workspace_bytes);
+
+/*
+ * kda_attn_workspace_bytes -- bytes of kda_attn_fwd's workspace: zero when the (automatic)
+ * schedule does not split the keys, else splits * Bq * Tq * Hq * (D + 2) floats.  Returns
+ * the size or a negative status.
+ */
+int64_t kda_attn_workspace_bytes(int64_t num_seqs, int64_t Bq, int64_t Tq, int64_t Bk, int64_t Tk,
+                                 int64_t Hq, int64_t Hk, int64_t D, int64_t splits);
+
 /* kda_status_string -- a static, human-readable name for a status code. */
 const char* kda_status_string(int status);
 

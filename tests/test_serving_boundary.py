@@ -143,3 +143,54 @@ def test_la_fwd_refusals(lib):
     for bad in ((-1, 1, 4, 128, 0), (1, 0, 4, 128, 0), (1, 1, 0, 128, 0), (1, 1, 4, 100, 0),
                 (1 << 40, 1, 1 << 10, 128, 64), (1 << 62, 1, 4, 128, 0)):
         assert lib.kda_la_workspace_bytes(*bad) == kda.KDA_ERR_BAD_SHAPE, bad
+
+
+ATTN = ("q q_row k k_row v v_row scale out lse cu_q cu_k k_lens N Bq Tq Bk Tk Hq Hk D splits ws "
+        "ws_bytes").split()
+ATTN_BASE = dict(q=1 * GB, q_row=1024, k=2 * GB, k_row=256, v=3 * GB, v_row=256, scale=0.1,
+                 out=4 * GB, lse=5 * GB, cu_q=None, cu_k=None, k_lens=None, N=3, Bq=3, Tq=20, Bk=3,
+                 Tk=50, Hq=8, Hk=2, D=128, splits=0, ws=None, ws_bytes=0)
+
+
+def test_attn_refusals(lib):
+    st = lambda **o: _call(lib.kda_attn_fwd_check, ATTN, ATTN_BASE, **o)
+    packed = dict(cu_q=6 * GB, cu_k=7 * GB, Bq=1, Bk=1)
+    assert st() == st(**packed) == st(lse=None) == kda.KDA_OK
+    assert st(k_lens=8 * GB) == kda.KDA_OK
+    assert st(cu_q=6 * GB, Bq=1, k_lens=8 * GB) == kda.KDA_OK  # packed queries, cache rows
+    assert st(cu_k=7 * GB, Bk=1) == kda.KDA_OK
+    assert st(Tq=0, q=None, out=None, lse=None) == kda.KDA_OK
+    assert st(Tk=0, k=None, v=None) == kda.KDA_OK
+    for name in ("q", "k", "v", "out"):
+        assert st(**{name: None}) == kda.KDA_ERR_NULL_ARG, name
+    for bad in (dict(D=32), dict(D=96), dict(Hk=3), dict(Hk=0), dict(Hq=0), dict(N=0), dict(Tq=-1),
+                dict(Tk=(1 << 30) + 1), dict(Tq=(1 << 28) + 1), dict(q_row=1 << 24),
+                dict(k_row=1 << 33), dict(Hq=1 << 30), dict(N=1 << 40, Bq=1 << 40, Bk=1 << 40),
+                dict(Tq=1 << 28, N=1 << 20, Bq=1 << 20, Bk=1 << 20)):
+        assert st(**bad) == kda.KDA_ERR_BAD_SHAPE, bad
+    for bad in (dict(N=4), dict(Bq=2), dict(Bk=2), dict(cu_q=6 * GB), dict(cu_k=7 * GB),
+                dict(Bq=1), dict(Bk=1), dict(packed, k_lens=8 * GB)):
+        assert st(**bad) == kda.KDA_ERR_BAD_VARLEN, bad
+    for s in (float("inf"), float("nan"), -0.1):
+        assert st(scale=s) == kda.KDA_ERR_BAD_SCALE
+    for bad in (dict(q_row=1016), dict(k_row=255), dict(v_row=260), dict(k=2 * GB + 2),
+                dict(out=4 * GB + 8), dict(ws=9 * GB + 4)):
+        assert st(**bad) == kda.KDA_ERR_BAD_LAYOUT, bad
+    for bad in (-1, 65):
+        assert st(splits=bad) == kda.KDA_ERR_BAD_SCHEDULE
+    for bad in (dict(out=1 * GB), dict(lse=4 * GB), dict(out=3 * GB - 16), dict(lse=2 * GB),
+                dict(k_lens=4 * GB)):
+        assert st(**bad) == kda.KDA_ERR_BAD_ALIAS, bad
+    sizes = (3, 3, 20, 3, 50, 8, 2, 128)
+    need = lib.kda_attn_workspace_bytes(*sizes, 4)
+    assert need == 4 * 60 * 8 * 130 * 4
+    assert st(splits=4) == kda.KDA_ERR_NULL_ARG
+    assert st(splits=4, ws=9 * GB, ws_bytes=need - 1) == kda.KDA_ERR_BAD_WORKSPACE
+    assert st(splits=4, ws=9 * GB, ws_bytes=need) == kda.KDA_OK
+    for at in (1 * GB, 4 * GB, 5 * GB):
+        assert st(splits=4, ws=at, ws_bytes=need) == kda.KDA_ERR_BAD_ALIAS
+    assert lib.kda_attn_workspace_bytes(*sizes, 1) == 0
+    assert lib.kda_attn_workspace_bytes(1, 1, 1, 1, 8192, 32, 8, 128, 0) > 0
+    assert lib.kda_attn_workspace_bytes(1, 1, 8192, 1, 8192, 32, 8, 128, 0) == 0
+    for bad in ((0,) + sizes[1:], sizes[:7] + (80,)):
+        assert lib.kda_attn_workspace_bytes(*bad, 0) == kda.KDA_ERR_BAD_SHAPE
