@@ -11,10 +11,9 @@ from __future__ import annotations
 import ctypes
 import os
 
-from . import serving
+from . import _abi
 from ._build import LIB_PATH, build  # noqa: F401  (build() is the in-tree compile step)
-from .serving import (kda_attn_fwd, kda_attn_workspace_bytes, kda_la_fwd, kda_la_step,
-                      kda_la_workspace_bytes, kda_step)
+
 
 __all__ = ["kda_fwd", "kda_fwd_sched", "kda_fwd_ordered", "kda_fwd_transposed_state",
            "kda_fwd_bf16_state",
@@ -41,6 +40,19 @@ KDA_DTYPE_BF16 = 0
 KDA_DTYPE_FP32 = 1
 
 _lib = None
+
+# The serving operators live in a module that imports torch at once (their checks run for
+# every token), so it is loaded with the first of them that is used.
+_SERVING = ("kda_step", "kda_la_step", "kda_la_fwd", "kda_la_workspace_bytes", "kda_attn_fwd",
+            "kda_attn_workspace_bytes")
+
+
+def __getattr__(name):
+    if name not in _SERVING:
+        raise AttributeError("module %r has no attribute %r" % (__name__, name))
+    from . import serving
+    globals().update((n, getattr(serving, n)) for n in _SERVING)
+    return globals()[name]
 
 
 class KdaError(RuntimeError):
@@ -93,7 +105,7 @@ def load_library():
     lib.kda_chunk_anchor.restype = f32
     lib.kda_status_string.argtypes = [i32]
     lib.kda_status_string.restype = ctypes.c_char_p
-    serving.declare(lib)
+    _abi.declare(lib)
     _lib = lib
     return lib
 

@@ -7,69 +7,39 @@ turn status codes into exceptions; every computation runs in the library's kerne
 """
 from __future__ import annotations
 
-import ctypes
+import torch
+from torch import bfloat16 as bf16, float32 as fp32
 
-_VP, _I64, _F32, _I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_int
-
-_STEP = [_VP] * 5 + [_F32] + [_VP] * 3 + [_F32, _VP, _I32, _I64, _VP, _VP] + [_I64] * 3
-_LA_STEP = ([_VP, _I64] * 3 + [_VP, _VP, _F32, _VP, _VP, _I32, _I64, _VP, _VP] + [_I64] * 4)
-_LA_FWD = ([_VP, _I64] * 3 + [_VP, _VP, _F32, _VP, _VP, _I32, _VP, _I32, _VP] + [_I64] * 7
-           + [_VP, _I64])
-_ATTN_FWD = ([_VP, _I64] * 3 + [_F32] + [_VP] * 5 + [_I64] * 9 + [_VP, _I64])
-
-
-def declare(lib) -> None:
-    """Sets the argument types of the serving operators' C functions."""
-    for name, args in (("kda_step", _STEP), ("kda_la_step", _LA_STEP),
-                       ("kda_la_fwd", _LA_FWD), ("kda_attn_fwd", _ATTN_FWD)):
-        getattr(lib, name).argtypes = args + [_VP]
-        getattr(lib, name).restype = _I32
-        getattr(lib, name + "_check").argtypes = args
-        getattr(lib, name + "_check").restype = _I32
-    lib.kda_la_workspace_bytes.argtypes = [_I64] * 5
-    lib.kda_la_workspace_bytes.restype = _I64
-    lib.kda_attn_workspace_bytes.argtypes = [_I64] * 9
-    lib.kda_attn_workspace_bytes.restype = _I64
-
-
-def _lib():
-    from . import load_library
-    return load_library()
-
-
-def _raise(status: int) -> None:
-    from . import KdaError
-    raise KdaError(status)
+from . import KdaError, load_library
 
 
 def _tensor(name, t, dtype, shape, dev):
-    """A contiguous tensor of this dtype, shape and device; its address."""
+    """Address of a contiguous tensor of this dtype, shape and device."""
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype or tuple(t.shape) != shape:
         raise ValueError("%s must be %s %s, got %s %s" % (name, dtype, list(shape), t.dtype,
                                                           list(t.shape)))
     if t.device != dev:
         raise ValueError("every tensor must live on the same GPU")
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+    raise ValueError("%s must be contiguous" % name)
 
 
 def _optional(name, t, dtype, shape, dev):
     return None if t is None else _tensor(name, t, dtype, shape, dev)
 
 
-def _rows(name, t, shape, dev):
-    """A bf16 tensor [..., heads, D] whose tokens lie one fixed row stride apart: its
-    address and that stride in elements."""
-    import torch
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != shape:
-        raise ValueError("%s must be bfloat16 %s, got %s %s" % (name, list(shape), t.dtype,
-                                                                list(t.shape)))
+def _rows(name, t, dtype, shape, dev):
+    """Address and row stride (in elements) of a bf16 tensor [..., heads, D] whose tokens lie
+    one fixed row stride apart."""
+    heads, D = shape[-2:]
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr(), heads * D
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError("%s must be %s %s, got %s %s" % (name, dtype, list(shape), t.dtype,
+                                                          list(t.shape)))
     if t.device != dev:
         raise ValueError("every tensor must live on the same GPU")
-    heads, D = shape[-2:]
-    if t.is_contiguous():
-        return t.data_ptr(), heads * D
     st = t.stride()
     if (st[-1] == 1 or D == 1) and (st[-2] == D or heads == 1):
         if len(shape) == 3:
@@ -82,38 +52,42 @@ def _rows(name, t, shape, dev):
 
 
 def _device(q):
-    if q.device.type != "cuda":
+    if not q.is_cuda:
         raise ValueError("every tensor must live on the same GPU")
     return q.device
 
 
 def _stream_ptr(stream, dev):
-    import torch
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(dev.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _launch(fn, dev, args) -> None:
     """Calls a C operator with dev current (the library launches on the current device)."""
-    import torch
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         st = fn(*args)
     else:
         with torch.cuda.device(dev):
             st = fn(*args)
     if st != 0:
-        _raise(st)
+        raise KdaError(st)
+
+
+def _dtype_code(t):
+    if t.dtype is bf16:
+        return 0
+    if t.dtype is fp32:
+        return 1
+    raise TypeError("state tensors must be bfloat16 or float32, got %s" % t.dtype)
 
 
 def _pool(state, slot_in, slot_out, N, H, D, dev):
-    import torch
-    from . import _state_dtype_code
     if state.dim() != 4:
         raise ValueError("state must be [slots,H,D,D]")
     slots = state.shape[0]
-    return (_tensor("state", state, state.dtype, (slots, H, D, D), dev), _state_dtype_code(state),
-            slots, _optional("slot_in", slot_in, torch.int64, (N,), dev),
+    return (_tensor("state", state, state.dtype, (slots, H, D, D), dev), _dtype_code(state), slots,
+            _optional("slot_in", slot_in, torch.int64, (N,), dev),
             _optional("slot_out", slot_out, torch.int64, (N,), dev))
 
 
@@ -128,18 +102,17 @@ def kda_step(q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound, state, s
     and writes slot ``slot_out[n]`` (None: slot_in); an index outside the pool reads zeros
     or writes nothing.  A slot that one request writes must not be named by another.
     """
-    import torch
     if q.dim() != 3:
         raise ValueError("q must be [N,H,D]")
     N, H, D = shape = tuple(q.shape)
     dev = _device(q)
-    args = (_tensor("q", q, torch.bfloat16, shape, dev), _tensor("k", k, torch.bfloat16, shape, dev),
-            _tensor("v", v, torch.bfloat16, shape, dev), _tensor("g", g, torch.bfloat16, shape, dev),
-            _tensor("beta", beta, torch.bfloat16, (N, H), dev), float(scale),
-            _tensor("out", out, torch.bfloat16, shape, dev), _tensor("A_log", A_log, torch.float32, (H,), dev),
-            _tensor("dt_bias", dt_bias, torch.float32, (H, D), dev), float(lower_bound),
+    args = (_tensor("q", q, bf16, shape, dev), _tensor("k", k, bf16, shape, dev),
+            _tensor("v", v, bf16, shape, dev), _tensor("g", g, bf16, shape, dev),
+            _tensor("beta", beta, bf16, (N, H), dev), float(scale),
+            _tensor("out", out, bf16, shape, dev), _tensor("A_log", A_log, fp32, (H,), dev),
+            _tensor("dt_bias", dt_bias, fp32, (H, D), dev), float(lower_bound),
             *_pool(state, slot_in, slot_out, N, H, D, dev), N, H, D, _stream_ptr(stream, dev))
-    _launch(_lib().kda_step, dev, args)
+    _launch(load_library().kda_step, dev, args)
 
 
 def kda_la_step(q, k, v, g, scale, out, state, decay=None, slot_in=None, slot_out=None,
@@ -151,32 +124,29 @@ def kda_la_step(q, k, v, g, scale, out, state, decay=None, slot_in=None, slot_ou
     views with a row stride); g: fp32 ``[N,H]`` log decays or None; decay: fp32 ``[H]`` log
     decays or None; state and slots as for ``kda_step``.
     """
-    import torch
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q and v must be [N,heads,D]")
     N, H, D = v.shape
     Hk = q.shape[1]
     dev = _device(q)
-    args = (*_rows("q", q, (N, Hk, D), dev), *_rows("k", k, (N, Hk, D), dev),
-            *_rows("v", v, (N, H, D), dev), _optional("g", g, torch.float32, (N, H), dev),
-            _optional("decay", decay, torch.float32, (H,), dev), float(scale),
-            _tensor("out", out, torch.bfloat16, (N, H, D), dev),
+    args = (*_rows("q", q, bf16, (N, Hk, D), dev), *_rows("k", k, bf16, (N, Hk, D), dev),
+            *_rows("v", v, bf16, (N, H, D), dev), _optional("g", g, fp32, (N, H), dev),
+            _optional("decay", decay, fp32, (H,), dev), float(scale),
+            _tensor("out", out, bf16, (N, H, D), dev),
             *_pool(state, slot_in, slot_out, N, H, D, dev), N, H, Hk, D,
             _stream_ptr(stream, dev))
-    _launch(_lib().kda_la_step, dev, args)
+    _launch(load_library().kda_la_step, dev, args)
 
 
 def _state(name, t, N, H, D, dev):
     """Address and dtype code of a prompt's initial or final states, or nothing."""
-    from . import _state_dtype_code
     if t is None:
         return None, 0
-    return _tensor(name, t, t.dtype, (N, H, D, D), dev), _state_dtype_code(t)
+    return _tensor(name, t, t.dtype, (N, H, D, D), dev), _dtype_code(t)
 
 
 def _workspace(workspace, need, dev, stream):
     """The caller's workspace, or one from torch's allocator for this call."""
-    import torch
     if workspace is None:
         if need == 0:
             return None, 0, None
@@ -193,9 +163,9 @@ def _workspace(workspace, need, dev, stream):
 
 def kda_la_workspace_bytes(T_total: int, num_seqs: int, H: int, D: int, segment: int = 0) -> int:
     """Bytes of the workspace of ``kda_la_fwd`` (0: this call needs none)."""
-    n = _lib().kda_la_workspace_bytes(int(T_total), int(num_seqs), int(H), int(D), int(segment))
+    n = load_library().kda_la_workspace_bytes(int(T_total), int(num_seqs), int(H), int(D), int(segment))
     if n < 0:
-        _raise(int(n))
+        raise KdaError(int(n))
     return int(n)
 
 
@@ -212,13 +182,12 @@ def kda_la_fwd(q, k, v, g, scale, out, decay=None, initial_state=None, final_sta
     ``kda_la_workspace_bytes(B*T, N, H, D, segment)`` bytes for this call alone; None takes
     one from torch's allocator where the call needs it.
     """
-    import torch
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q and v must be [B,T,heads,D]")
     B, T, H, D = v.shape
     Hk = q.shape[2]
     dev = _device(q)
-    if torch.cuda.current_device() != dev.index:  # schedules go by the current device
+    if torch._C._cuda_getDevice() != dev.index:  # schedules go by the current device
         with torch.cuda.device(dev):
             return kda_la_fwd(q, k, v, g, scale, out, decay, initial_state, final_state,
                               cu_seqlens, segment, workspace, stream)
@@ -226,13 +195,13 @@ def kda_la_fwd(q, k, v, g, scale, out, decay=None, initial_state=None, final_sta
     if cu_seqlens is not None:
         N = cu_seqlens.numel() - 1
         cu = _tensor("cu_seqlens", cu_seqlens, torch.int64, (N + 1,), dev)
-    lib = _lib()
+    lib = load_library()
     need = lib.kda_la_workspace_bytes(B * T, N, H, D, int(segment))
     ws, ws_bytes, _keep = _workspace(workspace, max(need, 0), dev, stream)
-    args = (*_rows("q", q, (B, T, Hk, D), dev), *_rows("k", k, (B, T, Hk, D), dev),
-            *_rows("v", v, (B, T, H, D), dev), _optional("g", g, torch.float32, (B, T, H), dev),
-            _optional("decay", decay, torch.float32, (H,), dev), float(scale),
-            _tensor("out", out, torch.bfloat16, (B, T, H, D), dev),
+    args = (*_rows("q", q, bf16, (B, T, Hk, D), dev), *_rows("k", k, bf16, (B, T, Hk, D), dev),
+            *_rows("v", v, bf16, (B, T, H, D), dev), _optional("g", g, fp32, (B, T, H), dev),
+            _optional("decay", decay, fp32, (H,), dev), float(scale),
+            _tensor("out", out, bf16, (B, T, H, D), dev),
             *_state("initial_state", initial_state, N, H, D, dev),
             *_state("final_state", final_state, N, H, D, dev), cu, N, B, T, H, Hk, D,
             int(segment), ws, ws_bytes, _stream_ptr(stream, dev))
@@ -242,10 +211,10 @@ def kda_la_fwd(q, k, v, g, scale, out, decay=None, initial_state=None, final_sta
 def kda_attn_workspace_bytes(num_seqs: int, Bq: int, Tq: int, Bk: int, Tk: int, Hq: int, Hk: int,
                              D: int, splits: int = 0) -> int:
     """Bytes of the workspace of ``kda_attn_fwd`` (0: this call needs none)."""
-    n = _lib().kda_attn_workspace_bytes(int(num_seqs), int(Bq), int(Tq), int(Bk), int(Tk), int(Hq),
+    n = load_library().kda_attn_workspace_bytes(int(num_seqs), int(Bq), int(Tq), int(Bk), int(Tk), int(Hq),
                                         int(Hk), int(D), int(splits))
     if n < 0:
-        _raise(int(n))
+        raise KdaError(int(n))
     return int(n)
 
 
@@ -264,24 +233,23 @@ def kda_attn_fwd(q, k, v, scale, out, lse=None, cu_seqlens_q=None, cu_seqlens_k=
     ``kda_attn_workspace_bytes(...)`` bytes for this call alone; None takes one from torch's
     allocator where the call needs it.
     """
-    import torch
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q and k must be [B,T,heads,D]")
     Bq, Tq, Hq, D = q.shape
     Bk, Tk, Hk, _ = k.shape
     dev = _device(q)
-    if torch.cuda.current_device() != dev.index:  # schedules go by the current device
+    if torch._C._cuda_getDevice() != dev.index:  # schedules go by the current device
         with torch.cuda.device(dev):
             return kda_attn_fwd(q, k, v, scale, out, lse, cu_seqlens_q, cu_seqlens_k, k_lens,
                                 splits, workspace, stream)
     N = cu_seqlens_q.numel() - 1 if cu_seqlens_q is not None else Bq
-    lib = _lib()
+    lib = load_library()
     need = lib.kda_attn_workspace_bytes(N, Bq, Tq, Bk, Tk, Hq, Hk, D, int(splits))
     ws, ws_bytes, _keep = _workspace(workspace, max(need, 0), dev, stream)
-    args = (*_rows("q", q, (Bq, Tq, Hq, D), dev), *_rows("k", k, (Bk, Tk, Hk, D), dev),
-            *_rows("v", v, (Bk, Tk, Hk, D), dev), float(scale),
-            _tensor("out", out, torch.bfloat16, (Bq, Tq, Hq, D), dev),
-            _optional("lse", lse, torch.float32, (Bq, Tq, Hq), dev),
+    args = (*_rows("q", q, bf16, (Bq, Tq, Hq, D), dev), *_rows("k", k, bf16, (Bk, Tk, Hk, D), dev),
+            *_rows("v", v, bf16, (Bk, Tk, Hk, D), dev), float(scale),
+            _tensor("out", out, bf16, (Bq, Tq, Hq, D), dev),
+            _optional("lse", lse, fp32, (Bq, Tq, Hq), dev),
             _optional("cu_seqlens_q", cu_seqlens_q, torch.int64, (N + 1,), dev),
             _optional("cu_seqlens_k", cu_seqlens_k, torch.int64, (N + 1,), dev),
             _optional("k_lens", k_lens, torch.int64, (N,), dev), N, Bq, Tq, Bk, Tk, Hq, Hk, D,
