@@ -7,12 +7,12 @@
 //     out_i = scale (e^{G_i} S q_i + sum_{j<=i} e^{G_i - G_j} (q_i . k_j) v_j)
 //     S'    = e^{G_C} S + sum_j e^{G_C - G_j} v_j k_j^T.
 //
-// One workgroup of four waves (two for D = 32) owns one (sequence, head) and walks its
-// chunks.  The fp32 state stays in accumulators: a wave holds S^T, all D keys by its own
-// value columns, as 16x16 tiles (lane l: value l%16, four keys).  Its keys are ordered so
-// that two tiles of accumulators pack into a matrix operand whose reduction slots are
-// eight consecutive keys, a 16-byte read of a q row in LDS: row 4g + i of an even tile is
-// key 8g + i of its 32-key block, and of an odd tile key 8g + 4 + i.
+// One workgroup owns one (sequence, head) and walks its chunks; its D / 16 waves hold the
+// fp32 state in accumulators, S^T, all D keys by 16 values a wave (lane l: value l%16, four
+// keys of each 16-key tile).  The keys are ordered so that two tiles of accumulators pack
+// into a matrix operand whose reduction slots are eight consecutive keys, a 16-byte read of
+// a q row in LDS: row 4g + i of an even tile is key 8g + i of its 32-key block, and of an
+// odd tile key 8g + 4 + i.
 //
 // Decay weights never exceed one and never come from a difference of long sums.  Inside
 // each 16-token tile p is the inclusive prefix of lam and s the sum of what follows, each
@@ -24,13 +24,15 @@
 // Roundings.  Scores times weights, and the state as an operand of S q, are rounded to
 // bf16 once each: out is a bf16 sum of two such parts, so its error stays below 1.5 of
 // its own rounding.  The state itself must not lose bits at each of thousands of chunks:
-// its update multiplies k (exact in bf16) by the weighted v in three bf16 parts, whose
-// sum holds the fp32 product to 2^-25.
+// its update multiplies k (exact in bf16) by the weighted v in two or three bf16 parts,
+// whose sum holds the fp32 product to 2^-17 or 2^-25.
 //
 // Segments.  One workgroup per (sequence, head) leaves most of the device idle for a few
 // long sequences.  Then three launches split the tokens: a state-only pass sums every
 // segment's own contribution from a zero state (k and v only), an elementwise scan turns
 // these into the state before each segment, and the main pass runs all segments at once.
+// The state-only pass goes backwards from the segment's end and stops once the decay of
+// what it has passed is zero in fp32: all earlier weights are.
 #include "api_util.h"
 #include "gfx950.h"
 #include "ops_params.h"
@@ -45,9 +47,8 @@ constexpr int RT = C / 16;  // 16-token tiles of a chunk
 
 template <int D>
 struct LaCfg {
-  static constexpr int NW = D >= 64 ? 4 : 2;     // waves
+  static constexpr int NW = D / 16;              // waves, 16 values each
   static constexpr int THREADS = NW * 64;
-  static constexpr int NT = D / (16 * NW);       // value tiles per wave
   static constexpr int KT = D / 16;              // key tiles
   static constexpr int KS = D / 32;              // 32-key steps
   static constexpr int LD = D + 16;              // row stride of the token tiles (bf16)
@@ -133,7 +134,9 @@ __device__ __forceinline__ bool find_unit(const LaParams& p, unsigned block, Uni
 }
 
 // First of the four keys that row 4g + i of key tile kt holds for lane group g.
-__device__ __forceinline__ int key0(int kt, int g) { return 32 * (kt >> 1) + 8 * g + 4 * (kt & 1); }
+__device__ __forceinline__ constexpr int key0(int kt, int g) {
+  return 32 * (kt >> 1) + 8 * g + 4 * (kt & 1);
+}
 
 template <int CTRL>
 __device__ __forceinline__ float dpp0(float v) {  // lanes without a source read zero
@@ -141,7 +144,42 @@ __device__ __forceinline__ float dpp0(float v) {  // lanes without a source read
                                                                0xf, 0xf, true));
 }
 
-template <int D, bool STATE_ONLY>
+// Loads and stores of the state as accumulators: `at` is the element of the lane's value and
+// lane group in a [V, K] state.
+template <int KT>
+__device__ __forceinline__ void state_load(f32x4_t (&S)[KT], const void* src, int64_t at,
+                                           int fp32) {
+  if (fp32) {
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+      S[kt] = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(src) + at + key0(kt, 0));
+  } else {
+    u32x2_t w[KT];
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+      w[kt] = *reinterpret_cast<const u32x2_t*>(static_cast<const u16*>(src) + at + key0(kt, 0));
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+      S[kt] = f32x4_t{bf_lo(w[kt][0]), bf_hi(w[kt][0]), bf_lo(w[kt][1]), bf_hi(w[kt][1])};
+  }
+}
+template <int KT>
+__device__ __forceinline__ void state_store(const f32x4_t (&S)[KT], void* dst, int64_t at,
+                                            int fp32) {
+  if (fp32) {
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+      *reinterpret_cast<f32x4_t*>(static_cast<float*>(dst) + at + key0(kt, 0)) = S[kt];
+  } else {
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+      *reinterpret_cast<u32x2_t*>(static_cast<u16*>(dst) + at + key0(kt, 0)) =
+          u32x2_t{pack_bf16(S[kt][0], S[kt][1]), pack_bf16(S[kt][2], S[kt][3])};
+  }
+}
+
+// PARTS: bf16 parts of the weighted v in the state update.
+template <int D, bool STATE_ONLY, int PARTS>
 __global__ __launch_bounds__(LaCfg<D>::THREADS, 2) void la_kernel(LaParams p) {
   using F = LaCfg<D>;
   __shared__ LaSmem<D, STATE_ONLY> sm;
@@ -151,40 +189,22 @@ __global__ __launch_bounds__(LaCfg<D>::THREADS, 2) void la_kernel(LaParams p) {
 
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int vw = wave * 16 * F::NT;  // first value column of this wave
   const int64_t H = p.H;
 
-  // ---- the state before the segment: tile [kt][nt] holds keys key0(kt, lg) .. +3 of value
-  // vw + 16 nt + l16
-  f32x4_t S[F::KT][F::NT];
+  // ---- the state before the segment: tile kt holds keys key0(kt, lg) .. +3 of value
+  // 16 wave + l16
+  f32x4_t S[F::KT];
 #pragma unroll
-  for (int kt = 0; kt < F::KT; ++kt)
-#pragma unroll
-    for (int nt = 0; nt < F::NT; ++nt) S[kt][nt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  float* const wseg = p.ws + (u.slot * H + u.h) * (int64_t)(D * D);
-  const int64_t head = ((int64_t)u.n * H + u.h) * (D * D);
+  for (int kt = 0; kt < F::KT; ++kt) S[kt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  float* const wseg = p.ws + (u.slot * H + u.h) * (int64_t)(D * D) + tid * 4;
+  const int64_t head = ((int64_t)u.n * H + u.h) * (D * D) + (16 * wave + l16) * D + 8 * lg;
   if constexpr (!STATE_ONLY) {
     if (u.nseg > 1) {
 #pragma unroll
       for (int kt = 0; kt < F::KT; ++kt)
-#pragma unroll
-        for (int nt = 0; nt < F::NT; ++nt)
-          S[kt][nt] = *reinterpret_cast<const f32x4_t*>(
-              wseg + ((kt * F::NT + nt) * F::THREADS + tid) * 4);
+        S[kt] = *reinterpret_cast<const f32x4_t*>(wseg + kt * F::THREADS * 4);
     } else if (p.s_in != nullptr) {
-#pragma unroll
-      for (int kt = 0; kt < F::KT; ++kt)
-#pragma unroll
-        for (int nt = 0; nt < F::NT; ++nt) {
-          const int64_t at = head + (vw + 16 * nt + l16) * D + key0(kt, lg);
-          if (p.s_in_fp32) {
-            S[kt][nt] = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p.s_in) + at);
-          } else {
-            const u32x2_t w =
-                *reinterpret_cast<const u32x2_t*>(static_cast<const u16*>(p.s_in) + at);
-            S[kt][nt] = f32x4_t{bf_lo(w[0]), bf_hi(w[0]), bf_lo(w[1]), bf_hi(w[1])};
-          }
-        }
+      state_load(S, p.s_in, head, p.s_in_fp32);
     }
   }
 
@@ -212,9 +232,18 @@ __global__ __launch_bounds__(LaCfg<D>::THREADS, 2) void la_kernel(LaParams p) {
     if (wave == 0 && p.g != nullptr) rg = lane < valid ? p.g[(t + lane) * H + u.h] : 0.f;
   };
 
-  if (u.t0 < u.t1) load(u.t0);
-  float seg_decay = 1.f;
-  for (int64_t t = u.t0; t < u.t1; t += C) {
+  // the main pass goes forwards, the state-only pass backwards
+  constexpr int STEP = STATE_ONLY ? -C : C;
+  auto inside = [&](int64_t t) { return STATE_ONLY ? t >= u.t0 : t < u.t1; };
+  const int64_t first =
+      STATE_ONLY && u.t0 < u.t1 ? u.t0 + (u.t1 - u.t0 - 1) / C * C : u.t0;
+  if (u.t0 < u.t1) load(first);
+  // the state's loads end here: their first use inside the loop would make every chunk wait
+  // for all loads in flight
+#pragma unroll
+  for (int kt = 0; kt < F::KT; ++kt) asm volatile("" : "+v"(S[kt]));
+  float after = 1.f;  // state-only: decay of the chunks passed, which follow this one
+  for (int64_t t = first; u.t0 < u.t1 && inside(t); t += STEP) {
     const int valid = (int)(u.t1 - t < C ? u.t1 - t : C);
     lds_barrier();  // the previous chunk's reads are done
 #pragma unroll
@@ -252,11 +281,11 @@ __global__ __launch_bounds__(LaCfg<D>::THREADS, 2) void la_kernel(LaParams p) {
       sm.w[lane] = w;
     }
     lds_barrier();
-    if (t + C < u.t1) load(t + C);
+    if (inside(t + STEP)) load(t + STEP);
 
     const float d0 = sm.tile[0], d1 = sm.tile[1], d2 = sm.tile[2], d3 = sm.tile[3];
     const float d_all = d0 * d1 * d2 * d3;
-    f32x4_t O[RT][F::NT];
+    f32x4_t O[RT];
     if constexpr (!STATE_ONLY) {
       // ---- scores: ten 16x16 tiles (i, j <= i) over the waves, as K Q^T: lane holds token
       // i = l16 and four j
@@ -286,132 +315,112 @@ __global__ __launch_bounds__(LaCfg<D>::THREADS, 2) void la_kernel(LaParams p) {
             u32x2_t{pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])};
       }
       // ---- the state's part: O^T = S Q^T, lane holds token l16 and four values
-      u32x4_t s_op[F::KS][F::NT];
 #pragma unroll
-      for (int ks = 0; ks < F::KS; ++ks)
+      for (int i = 0; i < RT; ++i) O[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int nt = 0; nt < F::NT; ++nt) {
-          const f32x4_t x = S[2 * ks][nt], y = S[2 * ks + 1][nt];
-          s_op[ks][nt] = u32x4_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                                 pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
-        }
+      for (int ks = 0; ks < F::KS; ++ks) {
+        const f32x4_t x = S[2 * ks], y = S[2 * ks + 1];
+        const u32x4_t s_op = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                              pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+          O[i] = mfma(s_op,
+                      *reinterpret_cast<const u32x4_t*>(&sm.Q[16 * i + l16][32 * ks + 8 * lg]),
+                      O[i]);
+      }
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
-#pragma unroll
-        for (int nt = 0; nt < F::NT; ++nt) O[i][nt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int ks = 0; ks < F::KS; ++ks) {
-          const u32x4_t q = *reinterpret_cast<const u32x4_t*>(&sm.Q[16 * i + l16][32 * ks + 8 * lg]);
-#pragma unroll
-          for (int nt = 0; nt < F::NT; ++nt) O[i][nt] = mfma(s_op[ks][nt], q, O[i][nt]);
-        }
         float f = sm.ep[16 * i + l16];
         if (i > 0) f *= d0;
         if (i > 1) f *= d1;
         if (i > 2) f *= d2;
-#pragma unroll
-        for (int nt = 0; nt < F::NT; ++nt) O[i][nt] *= f;
+        O[i] *= f;
       }
       lds_barrier();  // the scores are written
     }
 
-    // ---- per 32 tokens: the chunk's own part of the output, and the state update
-#pragma unroll
-    for (int kt = 0; kt < F::KT; ++kt)
-#pragma unroll
-      for (int nt = 0; nt < F::NT; ++nt) S[kt][nt] *= d_all;
+    // ---- V^T, from transposed reads: rows are values, slots tokens 32 b + 4g + i and
+    // 32 b + 16 + 4g + i
+    const int tr = 4 * lg + (l16 >> 2);
+    u32x4_t vt[C / 32];
 #pragma unroll
     for (int b = 0; b < C / 32; ++b) {
-      // V^T: rows are values, slots tokens 32 b + 4g + i and 32 b + 16 + 4g + i
-      u32x4_t vt[F::NT], w1[F::NT], w2[F::NT], w3[F::NT];
-      const int tr = 32 * b + 4 * lg + (l16 >> 2);
-      const f32x4_t wa = *reinterpret_cast<const f32x4_t*>(&sm.w[32 * b + 4 * lg]);
-      const f32x4_t wb = *reinterpret_cast<const f32x4_t*>(&sm.w[32 * b + 16 + 4 * lg]);
+      const int c = 16 * wave + 4 * (l16 & 3);
+      const u32x2_t lo = ds_read_tr(&sm.V[32 * b + tr][c]),
+                    hi = ds_read_tr(&sm.V[32 * b + tr + 16][c]);
+      vt[b] = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+    }
+    if constexpr (!STATE_ONLY) {
+      // ---- the chunk's own part of the output; the columns behind the diagonal tile are not
+      // written in the first row tile of each 32: slots 4-7 zero
 #pragma unroll
-      for (int nt = 0; nt < F::NT; ++nt) {
-        const int c = vw + 16 * nt + 4 * (l16 & 3);
-        const u32x2_t lo = ds_read_tr(&sm.V[tr][c]), hi = ds_read_tr(&sm.V[tr + 16][c]);
-        vt[nt] = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
-        // weight times v in three bf16 parts
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = bf_lo(vt[nt][e]) * (e < 2 ? wa[2 * e] : wb[2 * e - 4]);
-          const float y = bf_hi(vt[nt][e]) * (e < 2 ? wa[2 * e + 1] : wb[2 * e - 3]);
-          const unsigned h = pack_bf16(x, y);
-          const float x1 = x - bf_lo(h), y1 = y - bf_hi(h);
-          const unsigned m = pack_bf16(x1, y1);
-          w1[nt][e] = h;
-          w2[nt][e] = m;
-          w3[nt][e] = pack_bf16(x1 - bf_lo(m), y1 - bf_hi(m));
-        }
-      }
-      if constexpr (!STATE_ONLY) {
+      for (int b = 0; b < C / 32; ++b)
 #pragma unroll
         for (int i = 2 * b; i < RT; ++i) {
-          // tile 2 b's columns past the diagonal tile are not written: slots 4-7 zero
-          u32x4_t a;
-          if (i == 2 * b) {
-            const u32x4_t w = *reinterpret_cast<const u32x4_t*>(&sm.A[16 * i + l16][32 * b + 8 * lg]);
-            a = u32x4_t{w[0], w[1], 0u, 0u};
-          } else {
-            a = *reinterpret_cast<const u32x4_t*>(&sm.A[16 * i + l16][32 * b + 8 * lg]);
-          }
-#pragma unroll
-          for (int nt = 0; nt < F::NT; ++nt) O[i][nt] = mfma(vt[nt], a, O[i][nt]);
+          u32x4_t a = *reinterpret_cast<const u32x4_t*>(&sm.A[16 * i + l16][32 * b + 8 * lg]);
+          if (i == 2 * b) a = u32x4_t{a[0], a[1], 0u, 0u};
+          O[i] = mfma(vt[b], a, O[i]);
         }
-      }
-#pragma unroll
-      for (int kt = 0; kt < F::KT; ++kt) {
-        const int c = 32 * (kt >> 1) + 8 * (l16 & 3) + 4 * (kt & 1);
-        const u32x2_t lo = ds_read_tr(&sm.K[tr][c]), hi = ds_read_tr(&sm.K[tr + 16][c]);
-        const u32x4_t kop = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
-#pragma unroll
-        for (int nt = 0; nt < F::NT; ++nt) {
-          S[kt][nt] = mfma(kop, w3[nt], S[kt][nt]);
-          S[kt][nt] = mfma(kop, w2[nt], S[kt][nt]);
-          S[kt][nt] = mfma(kop, w1[nt], S[kt][nt]);
-        }
-      }
-    }
-    if constexpr (STATE_ONLY) {
-      seg_decay *= d_all;
-    } else {
       const uint32_t out_row = (uint32_t)H * D * 2u;
       const __amdgpu_buffer_rsrc_t ro =
           make_rsrc(p.out + (t * H + u.h) * D, (uint32_t)(valid - 1) * out_row + D * 2u);
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
+      for (int i = 0; i < RT; ++i) {
+        const f32x4_t o = O[i] * p.scale;
+        const u32x2_t w = {pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+        __builtin_amdgcn_raw_buffer_store_b64(
+            w, ro, (uint32_t)(16 * i + l16) * out_row + (uint32_t)(16 * wave + 4 * lg) * 2u, 0, 0);
+      }
+      // the output's registers are free from here: the compiler does not mix the phases,
+      // which keeps two workgroups of eight waves on a compute unit (126 registers)
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int nt = 0; nt < F::NT; ++nt) {
-          const f32x4_t o = O[i][nt] * p.scale;
-          const u32x2_t w = {pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
-          __builtin_amdgcn_raw_buffer_store_b64(
-              w, ro, (uint32_t)(16 * i + l16) * out_row + (uint32_t)(vw + 16 * nt + 4 * lg) * 2u, 0, 0);
+      for (int kt = 0; kt < F::KT; ++kt) S[kt] *= d_all;
+    }
+    // ---- the state update
+#pragma unroll
+    for (int b = 0; b < C / 32; ++b) {
+      f32x4_t wa = *reinterpret_cast<const f32x4_t*>(&sm.w[32 * b + 4 * lg]);
+      f32x4_t wb = *reinterpret_cast<const f32x4_t*>(&sm.w[32 * b + 16 + 4 * lg]);
+      if constexpr (STATE_ONLY) {
+        wa *= after;
+        wb *= after;
+      }
+      u32x4_t w[PARTS];  // weight times v
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float x = bf_lo(vt[b][e]) * (e < 2 ? wa[2 * e] : wb[2 * e - 4]);
+        float y = bf_hi(vt[b][e]) * (e < 2 ? wa[2 * e + 1] : wb[2 * e - 3]);
+#pragma unroll
+        for (int m = 0; m < PARTS; ++m) {
+          w[m][e] = pack_bf16(x, y);
+          x -= bf_lo(w[m][e]);
+          y -= bf_hi(w[m][e]);
         }
+      }
+#pragma unroll
+      for (int kt = 0; kt < F::KT; ++kt) {
+        const int c = key0(kt, l16 & 3);
+        const u32x2_t lo = ds_read_tr(&sm.K[32 * b + tr][c]),
+                      hi = ds_read_tr(&sm.K[32 * b + tr + 16][c]);
+        const u32x4_t kop = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+#pragma unroll
+        for (int m = PARTS - 1; m >= 0; --m) S[kt] = mfma(kop, w[m], S[kt]);
+      }
+    }
+    if constexpr (STATE_ONLY) {
+      after *= d_all;
+      if (__builtin_amdgcn_readfirstlane(after == 0.f)) break;  // the same in every lane
     }
   }
 
   if constexpr (STATE_ONLY) {
 #pragma unroll
     for (int kt = 0; kt < F::KT; ++kt)
-#pragma unroll
-      for (int nt = 0; nt < F::NT; ++nt)
-        *reinterpret_cast<f32x4_t*>(wseg + ((kt * F::NT + nt) * F::THREADS + tid) * 4) = S[kt][nt];
-    if (tid == 0) p.ws_decay[u.slot * H + u.h] = seg_decay;
+      *reinterpret_cast<f32x4_t*>(wseg + kt * F::THREADS * 4) = S[kt];
+    if (tid == 0) p.ws_decay[u.slot * H + u.h] = after;
   } else if (p.s_out != nullptr && u.s == u.nseg - 1) {
-#pragma unroll
-    for (int kt = 0; kt < F::KT; ++kt)
-#pragma unroll
-      for (int nt = 0; nt < F::NT; ++nt) {
-        const int64_t at = head + (vw + 16 * nt + l16) * D + key0(kt, lg);
-        const f32x4_t x = S[kt][nt];
-        if (p.s_out_fp32) {
-          *reinterpret_cast<f32x4_t*>(static_cast<float*>(p.s_out) + at) = x;
-        } else {
-          *reinterpret_cast<u32x2_t*>(static_cast<u16*>(p.s_out) + at) =
-              u32x2_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
-        }
-      }
+    state_store(S, p.s_out, head, p.s_out_fp32);
   }
 }
 
@@ -433,15 +442,13 @@ __global__ __launch_bounds__(256) void la_scan_kernel(LaParams p) {
   const int64_t slot = a / p.seg + n;
   f32x4_t S = {0.f, 0.f, 0.f, 0.f};
   if (p.s_in != nullptr) {
-    const int tid = e % F::THREADS, tile = e / F::THREADS, kt = tile / F::NT, nt = tile % F::NT;
-    const int v = (tid >> 6) * 16 * F::NT + 16 * nt + (tid & 15);
-    const int64_t at = ((int64_t)n * p.H + h) * (D * D) + v * D + key0(kt, (tid & 63) >> 4);
-    if (p.s_in_fp32) {
-      S = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p.s_in) + at);
-    } else {
-      const u32x2_t w = *reinterpret_cast<const u32x2_t*>(static_cast<const u16*>(p.s_in) + at);
-      S = f32x4_t{bf_lo(w[0]), bf_hi(w[0]), bf_lo(w[1]), bf_hi(w[1])};
-    }
+    const int tid = e % F::THREADS, kt = e / F::THREADS;
+    f32x4_t one[1];
+    state_load(one, p.s_in,
+               ((int64_t)n * p.H + h) * (D * D) + (16 * (tid >> 6) + (tid & 15)) * D +
+                   key0(kt, (tid & 63) >> 4),
+               p.s_in_fp32);
+    S = one[0];
   }
   const int64_t step = (int64_t)p.H * (D * D);
   float* w = p.ws + (slot * p.H + h) * (int64_t)(D * D) + e * 4;
@@ -455,25 +462,34 @@ __global__ __launch_bounds__(256) void la_scan_kernel(LaParams p) {
   *reinterpret_cast<f32x4_t*>(w) = S;
 }
 
-template <int D>
+template <int D, int PARTS>
 hipError_t go(const LaParams& p, hipStream_t stream) {
   using F = LaCfg<D>;
   const int64_t run = 8 * (int64_t)p.group;
   const int64_t items = p.seg ? p.slots : p.N;
   const int64_t blocks = (items * (p.H / p.group) + 7) / 8 * run;
   if (p.seg) {
-    la_kernel<D, true><<<dim3((unsigned)blocks), F::THREADS, 0, stream>>>(p);
+    la_kernel<D, true, PARTS><<<dim3((unsigned)blocks), F::THREADS, 0, stream>>>(p);
     constexpr int BLOCKS = (D * D / 4 + 255) / 256;
     la_scan_kernel<D><<<dim3((unsigned)((int64_t)p.N * p.H * BLOCKS)), 256, 0, stream>>>(p);
   }
-  la_kernel<D, false><<<dim3((unsigned)blocks), F::THREADS, 0, stream>>>(p);
+  la_kernel<D, false, PARTS><<<dim3((unsigned)blocks), F::THREADS, 0, stream>>>(p);
   return hipGetLastError();
+}
+
+// An fp32 final state keeps three parts; where none leaves, or one rounded to bf16, two
+// parts hold it to 2^-17 and save a third of the update's products.
+template <int D>
+hipError_t by_parts(const LaParams& p, hipStream_t stream) {
+  return p.s_out != nullptr && p.s_out_fp32 ? go<D, 3>(p, stream) : go<D, 2>(p, stream);
 }
 
 }  // namespace
 
 hipError_t launch_la(const LaParams& p, int D, hipStream_t stream) {
-  return D == 32 ? go<32>(p, stream) : D == 64 ? go<64>(p, stream) : go<128>(p, stream);
+  return D == 32   ? by_parts<32>(p, stream)
+         : D == 64 ? by_parts<64>(p, stream)
+                   : by_parts<128>(p, stream);
 }
 
 }  // namespace kda
