@@ -180,7 +180,7 @@ __device__ __forceinline__ void state_store(const f32x4_t (&S)[KT], void* dst, i
 
 // PARTS: bf16 parts of the weighted v in the state update.
 template <int D, bool STATE_ONLY, int PARTS>
-__global__ __launch_bounds__(LaCfg<D>::THREADS, 2) void la_kernel(LaParams p) {
+__global__ __launch_bounds__(LaCfg<D>::THREADS, STATE_ONLY ? 4 : 2) void la_kernel(LaParams p) {
   using F = LaCfg<D>;
   __shared__ LaSmem<D, STATE_ONLY> sm;
   Unit u;
