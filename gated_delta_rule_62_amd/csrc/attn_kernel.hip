@@ -118,6 +118,39 @@ __device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t off
   return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
+// Waits for the loads of a tile of rows before the loop over the keys: their first use inside
+// it would make every step wait for all loads in flight.
+template <int KS, int NI>
+__device__ __forceinline__ void end_loads(u32x4_t (&q)[KS][NI]) {
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+    for (int i = 0; i < NI; ++i) asm volatile("" : "+v"(q[ks][i]));
+}
+
+// The same descriptor as four words, for load_lds.
+__device__ __forceinline__ u32x4_t rows_words(const u16* base, int64_t row, int tokens, int D) {
+  const uint64_t at = reinterpret_cast<uint64_t>(base);
+  const uint32_t bytes = tokens > 0 ? (uint32_t)(tokens - 1) * (uint32_t)(row * 2) + D * 2u : 0u;
+  return u32x4_t{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32) & 0xffffu),
+                 (uint32_t)__builtin_amdgcn_readfirstlane(bytes), 0x00020000u};
+}
+
+// 16 bytes per lane from memory to LDS: lane l's land 16 l bytes behind `to` (uniform);
+// zeros where `off` is behind the descriptor's end.  It has no result the compiler could
+// track: kWaitLoads ends it, and a barrier shows it to the other waves.  (Nothing else in
+// these kernels uses m0.)
+__device__ __forceinline__ void load_lds(u32x4_t rsrc, const u16* to, uint32_t off) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const u16*)to;
+  asm volatile(
+      "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+      :
+      : "s"((uint32_t)__builtin_amdgcn_readfirstlane(at)), "v"(off), "s"(rsrc)
+      : "memory");
+}
+constexpr int kWaitLoads = 0x0f70;  // s_waitcnt: no vector memory access in flight
+
 // Row state and output tiles of NI 16-row tiles: lane = row l16, d = 16 dt + 4 lg + i.
 template <int D, int NI>
 struct Acc {
@@ -135,22 +168,24 @@ struct Acc {
     }
   }
 
-  // Scores x (scaled, masked ones minus infinity) of JT 16-key tiles to probabilities.
+  // Raises the running maximum where a row of x (scores, masked ones minus infinity) outgrows
+  // it.
   template <int JT>
-  __device__ __forceinline__ void softmax(f32x4_t (&x)[JT][NI]) {
+  __device__ __forceinline__ void raise(const f32x4_t (&x)[JT][NI], float c) {
     float top[NI];
-    bool raise = false;
+    bool any = false;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       float t = kNone;
 #pragma unroll
-      for (int j = 0; j < JT; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) t = fmaxf(t, x[j][i][r]);
-      top[i] = max_over_groups(t);
-      raise |= top[i] > m[i] + kRaise;  // minus infinity plus kRaise: any score raises it
+      for (int j = 0; j < JT; ++j) {
+        t = fmaxf(t, fmaxf(x[j][i][0], x[j][i][1]));
+        t = fmaxf(t, fmaxf(x[j][i][2], x[j][i][3]));
+      }
+      top[i] = max_over_groups(t) * c;
+      any |= top[i] > m[i] + kRaise;  // minus infinity plus kRaise: any score raises it
     }
-    if (__any(raise)) {  // uniform
+    if (__any(any)) {  // uniform
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const float now = fmaxf(m[i], top[i]);
@@ -161,18 +196,19 @@ struct Acc {
         for (int d = 0; d < DT; ++d) o[d][i] *= f;
       }
     }
+  }
+
+  // One 16-key tile of scores to probabilities, in place.
+  __device__ __forceinline__ void exps(f32x4_t (&x)[NI], float c) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const float base = m[i] == kNone ? 0.f : m[i];
+      const float base = m[i] == kNone ? 0.f : -m[i];
       float s = 0.f;
 #pragma unroll
-      for (int j = 0; j < JT; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float e = __builtin_amdgcn_exp2f(x[j][i][r] - base);
-          x[j][i][r] = e;
-          s += e;
-        }
+      for (int r = 0; r < 4; ++r) {
+        x[i][r] = __builtin_amdgcn_exp2f(fmaf(x[i][r], c, base));
+        s += x[i][r];
+      }
       l[i] += s;
     }
   }
@@ -208,13 +244,11 @@ __device__ __forceinline__ void store_row(const AttnParams& p, int64_t token, in
 
 // ---- prompts: four waves share the keys' tiles in LDS, each owns NI 16-row tiles.
 template <int D, int NI>
-__global__ __launch_bounds__(kAttnThreads, NI <= 2 ? 2 : 1) void attn_tile_kernel(AttnParams p) {
+__global__ __launch_bounds__(kAttnThreads, 2) void attn_tile_kernel(AttnParams p) {
   constexpr int BN = kAttnKeys, JT = BN / 16, KS = D / 32, DT = D / 16;
   constexpr int ROWS = 4 * 16 * NI;
-  constexpr int LD = D + 16;
-  constexpr int TPR = D / 8, RPP = kAttnThreads / TPR, PASSES = BN / RPP;
-  __shared__ alignas(16) u16 sk[2][BN][LD];
-  __shared__ alignas(16) u16 sv[2][BN][LD];
+  __shared__ alignas(1024) u16 sk[2][BN][D];
+  __shared__ alignas(1024) u16 sv[2][BN][D];
 
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -249,6 +283,7 @@ __global__ __launch_bounds__(kAttnThreads, NI <= 2 ? 2 : 1) void attn_tile_kerne
       for (int ks = 0; ks < KS; ++ks) q[ks][i] = *reinterpret_cast<const u32x4_t*>(src + 32 * ks);
     }
   }
+  end_loads(q);
   // keys some row of the tile, of this wave sees; keys every row of this wave sees
   const int tile_end = min(t.rows, t.row0 + ROWS) - 1;
   const int keys = max(0, min(t.Lk, tile_end / p.G + off + 1));
@@ -259,40 +294,45 @@ __global__ __launch_bounds__(kAttnThreads, NI <= 2 ? 2 : 1) void attn_tile_kerne
   const int steps = (keys + BN - 1) / BN, per = (steps + p.splits - 1) / p.splits;
   const int first = min(steps, split * per), end = min(steps, first + per);
 
-  const int lrow = tid / TPR, lcol = (tid % TPR) * 8;
+  // ---- K and V tiles go from memory straight into LDS, 1 KB (512 / D rows) per wave
+  // instruction: through registers and back the copies cost an eighth of the time.  The
+  // 16-byte pieces of a row are permuted, by exclusive or with the row, so that operand
+  // reads of 16 rows fall in distinct banks without padding.
+  constexpr int RPI = 512 / D;         // rows per instruction
+  constexpr int IPW = BN / RPI / 4;    // instructions per wave and tile
+  constexpr int PPR = D / 8;           // pieces per row
+  auto swz = [](int row) { return D == 128 ? row & 15 : (row >> 1) & 7; };
+  uint32_t koff[IPW], voff[IPW];
+#pragma unroll
+  for (int i = 0; i < IPW; ++i) {
+    const int r = (wave * IPW + i) * RPI + lane / PPR;
+    const uint32_t col = (uint32_t)((lane % PPR) ^ swz(r)) * 16u;
+    koff[i] = (uint32_t)r * (uint32_t)(p.k_row * 2) + col;
+    voff[i] = (uint32_t)r * (uint32_t)(p.v_row * 2) + col;
+  }
   const u16* kb = p.k + t.k0 * p.k_row + hk * D;
   const u16* vb = p.v + t.k0 * p.v_row + hk * D;
-  u32x4_t rk[PASSES], rv[PASSES];
   auto load = [&](int s) {
     const int valid = min(BN, t.Lk - s * BN);
-    const __amdgpu_buffer_rsrc_t dk = rows_rsrc(kb + (int64_t)s * BN * p.k_row, p.k_row, valid, D),
-                                 dv = rows_rsrc(vb + (int64_t)s * BN * p.v_row, p.v_row, valid, D);
+    const u32x4_t dk = rows_words(kb + (int64_t)s * BN * p.k_row, p.k_row, valid, D),
+                  dv = rows_words(vb + (int64_t)s * BN * p.v_row, p.v_row, valid, D);
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      rk[i] = load16(dk, (uint32_t)(lrow + i * RPP) * (uint32_t)(p.k_row * 2) + lcol * 2u);
-      rv[i] = load16(dv, (uint32_t)(lrow + i * RPP) * (uint32_t)(p.v_row * 2) + lcol * 2u);
-    }
-  };
-  auto stage = [&](int b) {
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      *reinterpret_cast<u32x4_t*>(&sk[b][lrow + i * RPP][lcol]) = rk[i];
-      *reinterpret_cast<u32x4_t*>(&sv[b][lrow + i * RPP][lcol]) = rv[i];
+    for (int i = 0; i < IPW; ++i) {
+      load_lds(dk, &sk[s & 1][(wave * IPW + i) * RPI][0], koff[i]);
+      load_lds(dv, &sv[s & 1][(wave * IPW + i) * RPI][0], voff[i]);
     }
   };
 
   Acc<D, NI> acc;
   acc.init();
-  if (first < end) {
-    load(first);
-    stage(0);
-    if (first + 1 < end) load(first + 1);
-  }
-  lds_barrier();
+  if (first < end) load(first);
   for (int s = first; s < end; ++s) {
-    const int b = (s - first) & 1;
-    if (s + 1 < end) stage(b ^ 1);
-    if (s + 2 < end) load(s + 2);
+    const int b = s & 1;
+    // this wave's part of tile s is in LDS; behind the barrier every wave's is, and all have
+    // read tile s - 1, whose buffer takes tile s + 1
+    __builtin_amdgcn_s_waitcnt(kWaitLoads);
+    lds_barrier();
+    if (s + 1 < end) load(s + 1);
     if (s * BN < wave_keys) {  // uniform per wave
       f32x4_t x[JT][NI];
 #pragma unroll
@@ -301,26 +341,26 @@ __global__ __launch_bounds__(kAttnThreads, NI <= 2 ? 2 : 1) void attn_tile_kerne
         for (int i = 0; i < NI; ++i) x[j][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          const u32x4_t k = *reinterpret_cast<const u32x4_t*>(&sk[b][16 * j + l16][32 * ks + 8 * lg]);
+          const u32x4_t k = *reinterpret_cast<const u32x4_t*>(
+              &sk[b][16 * j + l16][((4 * ks + lg) ^ swz(l16)) * 8]);
 #pragma unroll
           for (int i = 0; i < NI; ++i) x[j][i] = mfma(k, q[ks][i], x[j][i]);
         }
       }
+      __builtin_amdgcn_iglp_opt(1);  // operand reads ahead of the products: 2% of the time
       if ((s + 1) * BN > all_keys) {  // uniform: some row does not see all of these keys
+        asm volatile("");  // keeps this a branch
 #pragma unroll
         for (int j = 0; j < JT; ++j)
 #pragma unroll
           for (int i = 0; i < NI; ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              x[j][i][r] = s * BN + 16 * j + 4 * lg + r <= last[i] ? x[j][i][r] * p.c : kNone;
-      } else {
-#pragma unroll
-        for (int j = 0; j < JT; ++j)
-#pragma unroll
-          for (int i = 0; i < NI; ++i) x[j][i] *= p.c;
+              if (s * BN + 16 * j + 4 * lg + r > last[i]) x[j][i][r] = kNone;
       }
-      acc.softmax(x);
+      acc.raise(x, p.c);
+#pragma unroll
+      for (int j = 0; j < JT; ++j) acc.exps(x[j], p.c);
 #pragma unroll
       for (int js = 0; js < JT / 2; ++js) {
         u32x4_t pr[NI];
@@ -329,7 +369,7 @@ __global__ __launch_bounds__(kAttnThreads, NI <= 2 ? 2 : 1) void attn_tile_kerne
         const int row = 32 * js + 4 * lg + (l16 >> 2);
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          const int c = 16 * d + 4 * (l16 & 3);
+          const int c = ((2 * d + ((l16 & 3) >> 1)) ^ swz(row)) * 8 + 4 * (l16 & 1);
           const u32x2_t lo = ds_read_tr(&sv[b][row][c]), hi = ds_read_tr(&sv[b][row + 16][c]);
           const u32x4_t vt = {lo[0], lo[1], hi[0], hi[1]};
 #pragma unroll
@@ -337,7 +377,6 @@ __global__ __launch_bounds__(kAttnThreads, NI <= 2 ? 2 : 1) void attn_tile_kerne
         }
       }
     }
-    lds_barrier();
   }
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
@@ -393,6 +432,7 @@ __global__ __launch_bounds__(kAttnThreads, NI <= 2 ? 2 : 1) void attn_token_kern
       for (int ks = 0; ks < KS; ++ks) q[ks][i] = *reinterpret_cast<const u32x4_t*>(src + 32 * ks);
     }
   }
+  end_loads(q);
   const int keys = max(0, min(t.Lk, (min(t.rows, t.row0 + ROWS) - 1) / p.G + off + 1));
   const int all_keys = t.row0 / p.G + off + 1;
   const int steps = (keys + KEYS - 1) / KEYS, per = (steps + p.splits - 1) / p.splits;
@@ -439,20 +479,18 @@ __global__ __launch_bounds__(kAttnThreads, NI <= 2 ? 2 : 1) void attn_token_kern
       *reinterpret_cast<u32x4_t*>(&sm.v[wave][lrow + i * RPP][lcol]) = rv[i];
     if (s + 4 < end) load(s + 4);
     if ((s + 1) * KEYS > all_keys) {
+      asm volatile("");  // keeps this a branch
 #pragma unroll
       for (int j = 0; j < JT; ++j)
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            x[j][i][r] = s * KEYS + 16 * j + 4 * lg + r <= last[i] ? x[j][i][r] * p.c : kNone;
-    } else {
-#pragma unroll
-      for (int j = 0; j < JT; ++j)
-#pragma unroll
-        for (int i = 0; i < NI; ++i) x[j][i] *= p.c;
+            if (s * KEYS + 16 * j + 4 * lg + r > last[i]) x[j][i][r] = kNone;
     }
-    acc.softmax(x);
+    acc.raise(x, p.c);
+#pragma unroll
+    for (int j = 0; j < JT; ++j) acc.exps(x[j], p.c);
     wave_lds_sync();
     u32x4_t pr[NI];
 #pragma unroll

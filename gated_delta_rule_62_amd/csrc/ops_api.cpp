@@ -488,7 +488,9 @@ int kda_attn_fwd(const void* q, int64_t q_row, const void* k, int64_t k_row, con
   p.Hq = static_cast<int32_t>(Hq);
   p.Hk = static_cast<int32_t>(Hk);
   p.G = static_cast<int32_t>(Hq / Hk);
-  p.c = static_cast<float>(scale * 1.4426950408889634);
+  // never zero: minus infinity times it stands for a masked score (below 1e-30 every finite
+  // score times it is zero to the exponential anyway)
+  p.c = static_cast<float>(std::fmax(scale * 1.4426950408889634, 1e-30));
   p.splits = static_cast<int32_t>(sp);
   p.ws_o = static_cast<float*>(workspace);
   p.ws_ml = sp > 1 ? p.ws_o + sp * p.Tq_total * Hq * D : nullptr;
