@@ -140,16 +140,25 @@ __device__ __forceinline__ u32x4_t rows_words(const u16* base, int64_t row, int 
 // 16 bytes per lane from memory to LDS: lane l's land 16 l bytes behind `to` (uniform);
 // zeros where `off` is behind the descriptor's end.  It has no result the compiler could
 // track: kWaitLoads ends it, and a barrier shows it to the other waves.  (Nothing else in
-// these kernels uses m0.)
+// these kernels uses m0.)  ONCE marks what no other workgroup reads, so that it does not
+// displace what others do.
+template <bool ONCE>
 __device__ __forceinline__ void load_lds(u32x4_t rsrc, const u16* to, uint32_t off) {
   const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const u16*)to;
-  asm volatile(
-      "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-      :
-      : "s"((uint32_t)__builtin_amdgcn_readfirstlane(at)), "v"(off), "s"(rsrc)
-      : "memory");
+  const uint32_t m0 = (uint32_t)__builtin_amdgcn_readfirstlane(at);
+  if constexpr (ONCE)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
+                 :
+                 : "s"(m0), "v"(off), "s"(rsrc)
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(m0), "v"(off), "s"(rsrc)
+                 : "memory");
 }
-constexpr int kWaitLoads = 0x0f70;  // s_waitcnt: no vector memory access in flight
+constexpr int kWaitLoads = 0x0f70;  // s_waitcnt: no vector memory access in flight (or n: | n)
+constexpr int kWaitLds = 0xc07f;    // s_waitcnt: no LDS access in flight
 
 // Row state and output tiles of NI 16-row tiles: lane = row l16, d = 16 dt + 4 lg + i.
 template <int D, int NI>
@@ -318,8 +327,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_tile_kernel(AttnParams p
                   dv = rows_words(vb + (int64_t)s * BN * p.v_row, p.v_row, valid, D);
 #pragma unroll
     for (int i = 0; i < IPW; ++i) {
-      load_lds(dk, &sk[s & 1][(wave * IPW + i) * RPI][0], koff[i]);
-      load_lds(dv, &sv[s & 1][(wave * IPW + i) * RPI][0], voff[i]);
+      load_lds<false>(dk, &sk[s & 1][(wave * IPW + i) * RPI][0], koff[i]);
+      load_lds<false>(dv, &sv[s & 1][(wave * IPW + i) * RPI][0], voff[i]);
     }
   };
 
@@ -391,21 +400,24 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_tile_kernel(AttnParams p
 }
 
 // ---- single tokens: the four waves share NI 16-row tiles and take 32 keys each in turn.
-// A key is read by one wave only, so k goes from memory into operand registers and v
-// through a piece of LDS of the wave's own (for its transposed reads); no barrier until
-// the waves join their results.
+// Bound by HBM.  A key is read by one wave only, so each wave brings its keys and values
+// into a piece of LDS of its own, two steps deep, and waits for nobody until the waves join
+// their results; one workgroup of a compute unit keeps up to 128 KB in flight.
 template <int D, int NI>
-__global__ __launch_bounds__(kAttnThreads, NI <= 2 ? 2 : 1) void attn_token_kernel(AttnParams p) {
+__global__ __launch_bounds__(kAttnThreads, 1) void attn_token_kernel(AttnParams p) {
   constexpr int KEYS = 32, JT = 2, KS = D / 32, DT = D / 16;
   constexpr int ROWS = 16 * NI;
-  constexpr int LD = D + 16;
-  constexpr int TPR = D / 8, RPP = 64 / TPR, PASSES = KEYS / RPP;
+  constexpr int RPI = 512 / D, IPT = KEYS / RPI;  // rows per load instruction, of them per tile
+  constexpr int PPR = D / 8;
   constexpr int LO = D + 4;  // row stride of the join buffer (floats)
+  struct Keys {
+    u16 k[4][2][KEYS][D], v[4][2][KEYS][D];
+  };
   union Smem {
-    u16 v[4][KEYS][LD];
+    Keys s;
     float o[4][16][LO];
   };
-  __shared__ alignas(16) Smem sm;
+  __shared__ alignas(1024) Smem sm;
   __shared__ float sml[4][ROWS][2];
 
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lg = lane >> 4;
@@ -438,46 +450,50 @@ __global__ __launch_bounds__(kAttnThreads, NI <= 2 ? 2 : 1) void attn_token_kern
   const int steps = (keys + KEYS - 1) / KEYS, per = (steps + p.splits - 1) / p.splits;
   const int first = min(steps, split * per), end = min(steps, first + per);
 
-  const int lrow = lane / TPR, lcol = (lane % TPR) * 8;
+  auto swz = [](int row) { return D == 128 ? row & 15 : (row >> 1) & 7; };
+  uint32_t koff[IPT], voff[IPT];
+#pragma unroll
+  for (int i = 0; i < IPT; ++i) {
+    const int r = i * RPI + lane / PPR;
+    const uint32_t col = (uint32_t)((lane % PPR) ^ swz(r)) * 16u;
+    koff[i] = (uint32_t)r * (uint32_t)(p.k_row * 2) + col;
+    voff[i] = (uint32_t)r * (uint32_t)(p.v_row * 2) + col;
+  }
   const u16* kb = p.k + t.k0 * p.k_row + hk * D;
   const u16* vb = p.v + t.k0 * p.v_row + hk * D;
-  const uint32_t k_row = (uint32_t)(p.k_row * 2), v_row = (uint32_t)(p.v_row * 2);
-  u32x4_t rk[JT][KS], rv[PASSES];
-  auto load = [&](int s) {
+  auto load = [&](int s, int buf) {
     const int valid = min(KEYS, t.Lk - s * KEYS);
-    const __amdgpu_buffer_rsrc_t dk =
-                                     rows_rsrc(kb + (int64_t)s * KEYS * p.k_row, p.k_row, valid, D),
-                                 dv =
-                                     rows_rsrc(vb + (int64_t)s * KEYS * p.v_row, p.v_row, valid, D);
+    const u32x4_t dk = rows_words(kb + (int64_t)s * KEYS * p.k_row, p.k_row, valid, D),
+                  dv = rows_words(vb + (int64_t)s * KEYS * p.v_row, p.v_row, valid, D);
 #pragma unroll
-    for (int j = 0; j < JT; ++j)
+    for (int i = 0; i < IPT; ++i) load_lds<true>(dk, &sm.s.k[wave][buf][i * RPI][0], koff[i]);
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-        rk[j][ks] = load16(dk, (uint32_t)(16 * j + l16) * k_row + 64u * ks + 16u * lg);
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i)
-      rv[i] = load16(dv, (uint32_t)(lrow + i * RPP) * v_row + lcol * 2u);
+    for (int i = 0; i < IPT; ++i) load_lds<true>(dv, &sm.s.v[wave][buf][i * RPI][0], voff[i]);
   };
 
   Acc<D, NI> acc;
   acc.init();
-  int s = first + wave;
-  if (s < end) load(s);
-  for (; s < end; s += 4) {
+  if (first + wave < end) load(first + wave, 0);
+  if (first + wave + 4 < end) load(first + wave + 4, 1);
+  int buf = 0;
+  for (int s = first + wave; s < end; s += 4, buf ^= 1) {
+    // the oldest step is in place when only the next one's loads are in flight
+    if (s + 4 < end) __builtin_amdgcn_s_waitcnt(kWaitLoads | (2 * IPT & 15) | (2 * IPT >> 4 << 14));
+    else __builtin_amdgcn_s_waitcnt(kWaitLoads);
+    asm volatile("" ::: "memory");
     f32x4_t x[JT][NI];
 #pragma unroll
     for (int j = 0; j < JT; ++j) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) x[j][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
+      for (int ks = 0; ks < KS; ++ks) {
+        const u32x4_t k = *reinterpret_cast<const u32x4_t*>(
+            &sm.s.k[wave][buf][16 * j + l16][((4 * ks + lg) ^ swz(l16)) * 8]);
 #pragma unroll
-        for (int i = 0; i < NI; ++i) x[j][i] = mfma(rk[j][ks], q[ks][i], x[j][i]);
+        for (int i = 0; i < NI; ++i) x[j][i] = mfma(k, q[ks][i], x[j][i]);
+      }
     }
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i)
-      *reinterpret_cast<u32x4_t*>(&sm.v[wave][lrow + i * RPP][lcol]) = rv[i];
-    if (s + 4 < end) load(s + 4);
     if ((s + 1) * KEYS > all_keys) {
       asm volatile("");  // keeps this a branch
 #pragma unroll
@@ -491,20 +507,23 @@ __global__ __launch_bounds__(kAttnThreads, NI <= 2 ? 2 : 1) void attn_token_kern
     acc.raise(x, p.c);
 #pragma unroll
     for (int j = 0; j < JT; ++j) acc.exps(x[j], p.c);
-    wave_lds_sync();
     u32x4_t pr[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) pr[i] = p_op(x[0][i], x[1][i]);
     const int row = 4 * lg + (l16 >> 2);
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
-      const int c = 16 * d + 4 * (l16 & 3);
-      const u32x2_t lo = ds_read_tr(&sm.v[wave][row][c]), hi = ds_read_tr(&sm.v[wave][row + 16][c]);
+      const int c = ((2 * d + ((l16 & 3) >> 1)) ^ swz(row)) * 8 + 4 * (l16 & 1);
+      const u32x2_t lo = ds_read_tr(&sm.s.v[wave][buf][row][c]),
+                    hi = ds_read_tr(&sm.s.v[wave][buf][row + 16][c]);
       const u32x4_t vt = {lo[0], lo[1], hi[0], hi[1]};
 #pragma unroll
       for (int i = 0; i < NI; ++i) acc.o[d][i] = mfma(vt, pr[i], acc.o[d][i]);
     }
-    wave_lds_sync();
+    // this step's reads are done before its place is written again
+    __builtin_amdgcn_s_waitcnt(kWaitLds);
+    asm volatile("" ::: "memory");
+    if (s + 8 < end) load(s + 8, buf);
   }
 
   // ---- join the waves: maxima and sums first, then the outputs, one 16-row tile at a time

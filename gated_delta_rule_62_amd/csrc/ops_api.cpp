@@ -215,7 +215,7 @@ int la_check(const void* q, int64_t q_row, const void* k, int64_t k_row, const v
 int64_t attn_auto_splits(const kda::AttnSchedule& s, int64_t slots, int64_t Hk, int64_t mean_k) {
   const int64_t want = (s.tokens ? 4 : 2) * (int64_t)kda::device_cus();
   const int64_t least = s.tokens ? 256 : 512;
-  int64_t n = want / (slots * Hk);
+  int64_t n = want / (slots > 0 ? slots * Hk : 1);
   if (n > mean_k / least) n = mean_k / least;
   return n < 1 ? 1 : n > 64 ? 64 : n;
 }
@@ -235,12 +235,14 @@ int attn_sizes(int64_t N, int64_t Bq, int64_t Tq, int64_t Bk, int64_t Tk, int64_
   if (splits < 0 || splits > 64) return KDA_ERR_BAD_SCHEDULE;
   const int64_t G = Hq / Hk, total = Bq * Tq;
   *sched = kda::attn_schedule(total, N, G, static_cast<int>(D));
-  const int64_t slots = kda::attn_slots(total, N, G, sched->rows);  // at least the batched count
+  // tiles of rows: for batch rows as many as each has, for packed ones a bound
+  const int64_t slots = Bq == N ? N * ((Tq * G + sched->rows - 1) / sched->rows)
+                                : kda::attn_slots(total, N, G, sched->rows);
   const int64_t mean_k = Bk == 1 ? Tk / N : Tk;
   int64_t sp = splits ? splits : attn_auto_splits(*sched, slots, Hk, mean_k);
   // every launch below 2^32 work-items
   const int64_t most = (((int64_t)1 << 32) - 1) / kda::kAttnThreads;
-  if (slots > most / Hk || total > most / Hq) return KDA_ERR_BAD_SHAPE;
+  if (N > most / Hk || slots > most / Hk || total > most / Hq) return KDA_ERR_BAD_SHAPE;
   if (slots * Hk > most / sp) {
     if (splits) return KDA_ERR_BAD_SHAPE;
     sp = 1;

@@ -14,7 +14,9 @@
 // computed, so their latency covers it.  The two row sums a lane group needs,
 // p = (S diag(a)) kh and o = (S diag(a)) qh, are formed together: out's second term is
 // u (kh . qh), a scalar of the head, which leaves one reduction latency per row and not
-// two dependent ones.  State arithmetic is fp32 for either storage type; out is
+// two dependent ones.  A state is read once and written once, long before its next use:
+// both accesses are marked non-temporal (96 requests, 96 heads, fp32: 231 to 215 us, 5.6
+// TB/s read and written; 256 requests, 32 heads, bf16: 109 to 102 us).  State arithmetic is fp32 for either storage type; out is
 // computed from the fp32 state before a bf16 state is rounded.
 #include "api_util.h"
 #include "gfx950.h"
@@ -105,7 +107,7 @@ __global__ __launch_bounds__((Cfg<D, FP32>::THREADS)) void step_kernel(StepParam
     const char* s = pool + ((src * p.H + h) * (int64_t)(D * D) + at) * R::BYTES;
 #pragma unroll
     for (int i = 0; i < PASSES; ++i)
-      raw[i] = *reinterpret_cast<const u32x4_t*>(s + i * D * R::BYTES);
+      raw[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(s + i * D * R::BYTES));
   } else {
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) raw[i] = u32x4_t{0u, 0u, 0u, 0u};
@@ -183,7 +185,7 @@ __global__ __launch_bounds__((Cfg<D, FP32>::THREADS)) void step_kernel(StepParam
     char* s = pool + ((dst * p.H + h) * (int64_t)(D * D) + at) * R::BYTES;
 #pragma unroll
     for (int i = 0; i < PASSES; ++i)
-      *reinterpret_cast<u32x4_t*>(s + i * D * R::BYTES) = raw[i];
+      __builtin_nontemporal_store(raw[i], reinterpret_cast<u32x4_t*>(s + i * D * R::BYTES));
   }
   if (k0 == 0) {
     u16* out = p.out + nh * D + row0;
