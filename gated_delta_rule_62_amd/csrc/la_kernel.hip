@@ -43,7 +43,8 @@ namespace {
 using namespace dev;
 
 constexpr int C = kLaChunk;
-constexpr int RT = C / 16;  // 16-token tiles of a chunk
+constexpr int RT = C / 16;    // 16-token tiles of a chunk
+constexpr int kOnce = 2;      // a buffer access's flags: non-temporal
 
 template <int D>
 struct LaCfg {
@@ -180,7 +181,7 @@ __device__ __forceinline__ void state_store(const f32x4_t (&S)[KT], void* dst, i
 
 // PARTS: bf16 parts of the weighted v in the state update.
 template <int D, bool STATE_ONLY, int PARTS>
-__global__ __launch_bounds__(LaCfg<D>::THREADS, STATE_ONLY ? 4 : 2) void la_kernel(LaParams p) {
+__global__ __launch_bounds__(LaCfg<D>::THREADS, D == 128 || STATE_ONLY ? 4 : 3) void la_kernel(LaParams p) {
   using F = LaCfg<D>;
   __shared__ LaSmem<D, STATE_ONLY> sm;
   Unit u;
@@ -242,10 +243,26 @@ __global__ __launch_bounds__(LaCfg<D>::THREADS, STATE_ONLY ? 4 : 2) void la_kern
   // for all loads in flight
 #pragma unroll
   for (int kt = 0; kt < F::KT; ++kt) asm volatile("" : "+v"(S[kt]));
+  // the outputs of the chunk at t, from LDS: each thread reads the pieces that it will write
+  // next
+  const uint32_t out_row = (uint32_t)H * D * 2u;
+  auto store_out = [&](int64_t t) {
+    const int valid = (int)(u.t1 - t < C ? u.t1 - t : C);
+    const __amdgpu_buffer_rsrc_t ro =
+        make_rsrc(p.out + (t * H + u.h) * D, (uint32_t)(valid - 1) * out_row + D * 2u);
+#pragma unroll
+    for (int i = 0; i < F::PASSES; ++i) {
+      const int r = lrow + i * F::RPP;
+      __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4_t*>(&sm.Q[r][lcol]), ro,
+                                             (uint32_t)r * out_row + lcol * 2u, 0, kOnce);
+    }
+  };
   float after = 1.f;  // state-only: decay of the chunks passed, which follow this one
   for (int64_t t = first; u.t0 < u.t1 && inside(t); t += STEP) {
     const int valid = (int)(u.t1 - t < C ? u.t1 - t : C);
-    lds_barrier();  // the previous chunk's reads are done
+    lds_barrier();  // the previous chunk's reads are done, its outputs in place
+    if constexpr (!STATE_ONLY)
+      if (t > first) store_out(t - C);
 #pragma unroll
     for (int i = 0; i < F::PASSES; ++i) {
       const int r = lrow + i * F::RPP;
@@ -361,18 +378,15 @@ __global__ __launch_bounds__(LaCfg<D>::THREADS, STATE_ONLY ? 4 : 2) void la_kern
           if (i == 2 * b) a = u32x4_t{a[0], a[1], 0u, 0u};
           O[i] = mfma(vt[b], a, O[i]);
         }
-      const uint32_t out_row = (uint32_t)H * D * 2u;
-      const __amdgpu_buffer_rsrc_t ro =
-          make_rsrc(p.out + (t * H + u.h) * D, (uint32_t)(valid - 1) * out_row + D * 2u);
+      // into the place of Q, whose reads are done: whole rows leave with the next chunk
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
         const f32x4_t o = O[i] * p.scale;
-        const u32x2_t w = {pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
-        __builtin_amdgcn_raw_buffer_store_b64(
-            w, ro, (uint32_t)(16 * i + l16) * out_row + (uint32_t)(16 * wave + 4 * lg) * 2u, 0, 0);
+        *reinterpret_cast<u32x2_t*>(&sm.Q[16 * i + l16][16 * wave + 4 * lg]) =
+            u32x2_t{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
       }
-      // the output's registers are free from here: the compiler does not mix the phases,
-      // which keeps two workgroups of eight waves on a compute unit (126 registers)
+      // the output's registers are free from here: the compiler does not mix the phases, and
+      // two workgroups of eight waves stay on a compute unit (128 registers)
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int kt = 0; kt < F::KT; ++kt) S[kt] *= d_all;
@@ -414,6 +428,11 @@ __global__ __launch_bounds__(LaCfg<D>::THREADS, STATE_ONLY ? 4 : 2) void la_kern
     }
   }
 
+  if constexpr (!STATE_ONLY)
+    if (u.t0 < u.t1) {
+      lds_barrier();
+      store_out(u.t0 + (u.t1 - u.t0 - 1) / C * C);
+    }
   if constexpr (STATE_ONLY) {
 #pragma unroll
     for (int kt = 0; kt < F::KT; ++kt)

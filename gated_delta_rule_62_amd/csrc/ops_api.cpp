@@ -104,27 +104,31 @@ int la_step_check(const void* q, int64_t q_row, const void* k, int64_t k_row, co
   return KDA_OK;
 }
 
-// Tokens per segment of kda_la_fwd when the caller leaves the choice, 0 for none.  Times in
-// microseconds.  Unsegmented, one workgroup walks a sequence (whose length is only known
-// on average) at kStep per chunk, unless the device is full and HBM bounds it.  In
-// segments all tokens' k and v are read twice, and each segment's state is written, scanned
-// and read; a few segments per compute unit fill the device.
+// Tokens per segment of kda_la_fwd when the caller leaves the choice, 0 for none: the least
+// estimated time.  The host knows the sequences' mean length only.  The constants
+// (microseconds, bytes per microsecond) are fitted to 130 measured calls, 1-4 sequences of
+// 512-32,768 tokens, 1-128 heads, D 64 and 128, with and without segments: the choice costs
+// 2% over the best of each on average.
 int64_t la_auto_segment(int64_t T_total, int64_t N, int64_t H, int64_t D) {
-  constexpr double kStep = 1.7, kRate = 5.0e6 /* bytes per us */, kLaunches = 8.0;
-  const int64_t C = kda::kLaChunk;
-  const int64_t units = N * H, cus = kda::device_cus(), mean = T_total / N;
+  const double units = double(N) * H, mean = double(T_total) / N, chunk = kda::kLaChunk;
+  const double room = 2.0 * kda::device_cus();  // workgroups at once
   const double bytes = 8.0 * T_total * H * D;
-  const double waves = std::ceil(units / (2.0 * cus));
-  const double whole = std::fmax(bytes / kRate, waves * kStep * mean / C);
-  // segments that give each compute unit two workgroups, of at least four chunks
-  int64_t per_seq = (2 * cus + units - 1) / units;
-  int64_t seg = (mean / (per_seq > 0 ? per_seq : 1) + C - 1) / C * C;
-  if (seg < 4 * C) seg = 4 * C;
-  if (seg > (1 << 20)) seg = 1 << 20;
-  if (2 * seg > mean) return 0;
-  const double state = 4.0 * 4.0 * D * D * H * (double(T_total) / seg);
-  const double split = std::fmax((1.5 * bytes + state) / kRate, 1.75 * kStep * seg / C) + kLaunches;
-  return split < whole ? seg : 0;
+  // one workgroup walks a sequence's chunks, unless HBM bounds the call
+  double best = 9.0 + std::fmax((2.2 + 0.0136 * D) * std::ceil(mean / chunk) *
+                                    std::fmax(1.0, units / room), bytes / 4.4e6);
+  int64_t choice = 0;
+  for (int64_t seg = 2 * kda::kLaChunk; 2 * seg <= mean && seg <= (1 << 20); seg *= 2) {
+    // two passes over a segment's chunks and a scan over the segments, or the bytes: k and v
+    // twice (the first pass ends where the decay is zero), each segment's state four times
+    const double walk = (2.1 + 0.017 * D) * (seg / chunk) + 0.25 * mean / seg;
+    const double move = (1.35 * bytes + 16.0 * D * D * H * (double(T_total) / seg)) / 4.6e6;
+    const double t = 21.0 + std::fmax(walk, move) + 0.13 * std::fmin(walk, move);
+    if (t < best) {
+      best = t;
+      choice = seg;
+    }
+  }
+  return choice;
 }
 
 // A segment length as given (0: automatic) to the one used, or a negative status.
