@@ -36,7 +36,6 @@ constexpr float kNone = -__builtin_inff();
 
 // A tile of rows: its sequence's queries and keys, its rows.
 struct Tile {
-  int n;
   int64_t q0, k0;   // first query and key token
   int Lq, Lk;       // lengths
   int row0, rows;   // first row of the tile, rows of the sequence (Lq * G)
@@ -56,43 +55,87 @@ __device__ __forceinline__ void query_bounds(const AttnParams& p, int n, int64_t
   }
 }
 
-// Slot `slot` of a key/value head's tiles of ROWS rows; false if no tile has it.
-__device__ __forceinline__ bool find_tile(const AttnParams& p, int64_t slot, int tile_rows,
-                                          Tile& t) {
-  int lo = 0, hi = p.N - 1;
-  int64_t a, b;
-  if (p.cu_q == nullptr) {
-    const int64_t per = (p.Tq * p.G + tile_rows - 1) / tile_rows;
-    lo = (int)(slot / per);
-    if (lo >= p.N) return false;
-    t.row0 = (int)(slot % per) * tile_rows;
-    query_bounds(p, lo, a, b);
+__device__ __forceinline__ void key_bounds(const AttnParams& p, int n, int64_t& a, int64_t& b) {
+  if (p.cu_k != nullptr) {
+    a = clamp64(p.cu_k[n], 0, p.Tk);
+    b = clamp64(p.cu_k[n + 1], a, p.Tk);
   } else {
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      query_bounds(p, mid, a, b);
-      if (a * p.G / tile_rows + mid <= slot) lo = mid;
-      else hi = mid - 1;
-    }
-    query_bounds(p, lo, a, b);
-    const int64_t at = (slot - (a * p.G / tile_rows + lo)) * tile_rows;
-    if (at < 0 || at >= (b - a) * p.G) return false;
-    t.row0 = (int)at;
+    a = (int64_t)n * p.Tk;
+    b = a + (p.k_lens != nullptr ? clamp64(p.k_lens[n], 0, p.Tk) : p.Tk);
   }
-  t.n = lo;
+}
+
+// The tile of `tile_rows` rows that starts at row row0 of sequence n; false if there is none.
+__device__ __forceinline__ bool set_tile(const AttnParams& p, int n, int64_t row0, Tile& t) {
+  int64_t a, b;
+  query_bounds(p, n, a, b);
+  if (row0 < 0 || row0 >= (b - a) * p.G) return false;
+  t.row0 = (int)row0;
   t.q0 = a;
   t.Lq = (int)(b - a);
   t.rows = t.Lq * p.G;
-  int64_t len;
-  if (p.cu_k != nullptr) {
-    t.k0 = clamp64(p.cu_k[lo], 0, p.Tk);
-    len = clamp64(p.cu_k[lo + 1], t.k0, p.Tk) - t.k0;
-  } else {
-    t.k0 = (int64_t)lo * p.Tk;
-    len = p.k_lens != nullptr ? clamp64(p.k_lens[lo], 0, p.Tk) : p.Tk;
-  }
-  t.Lk = (int)len;
+  key_bounds(p, n, a, b);
+  t.k0 = a;
+  t.Lk = (int)(b - a);
   return true;
+}
+
+// Tile number `slot` of a key/value head, in any order; false if it has none.
+__device__ __forceinline__ bool find_tile(const AttnParams& p, int64_t slot, int tile_rows,
+                                          Tile& t) {
+  if (p.cu_q == nullptr) {
+    const int64_t per = (p.Tq * p.G + tile_rows - 1) / tile_rows;
+    return slot / per < p.N && set_tile(p, (int)(slot / per), slot % per * tile_rows, t);
+  }
+  // the last sequence whose first slot is not behind this one (first slots grow strictly)
+  int lo = 0, hi = p.N - 1;
+  int64_t a, b;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    query_bounds(p, mid, a, b);
+    if (a * p.G / tile_rows + mid <= slot) lo = mid;
+    else hi = mid - 1;
+  }
+  query_bounds(p, lo, a, b);
+  return set_tile(p, lo, (slot - (a * p.G / tile_rows + lo)) * tile_rows, t);
+}
+
+// The same with the tiles that see the most keys first, as workgroups start in order and a
+// long one that starts last would set the time: batch rows by their tile, packed sequences
+// (of up to 16: the ranking costs a short workgroup more than it gains with many) longest
+// keys first, each from its last tile.  Whole waves call it.
+__device__ __forceinline__ bool find_tile_longest_first(const AttnParams& p, int64_t slot,
+                                                        int64_t slots, int tile_rows, Tile& t) {
+  int n;
+  int64_t row0;
+  if (p.cu_q == nullptr) {
+    const int64_t per = (p.Tq * p.G + tile_rows - 1) / tile_rows;
+    n = (int)(slot % p.N);
+    row0 = (per - 1 - slot / p.N) * tile_rows;
+  } else if (p.N > 16) {
+    return find_tile(p, slots - 1 - slot, tile_rows, t);
+  } else {
+    // lane l: keys and tiles of sequence l, and the tiles of all that come before it
+    const int lane = threadIdx.x & 63;
+    int64_t a = 0, b = 0, c = 0, d = 0;
+    if (lane < p.N) {
+      query_bounds(p, lane, a, b);
+      key_bounds(p, lane, c, d);
+    }
+    const int keys = (int)(d - c), tiles = (int)(((b - a) * p.G + tile_rows - 1) / tile_rows);
+    int before = 0;
+    for (int m = 0; m < p.N; ++m) {
+      const int k = __builtin_amdgcn_readlane(keys, m), x = __builtin_amdgcn_readlane(tiles, m);
+      if (k > keys || (k == keys && m < lane)) before += x;
+    }
+    const int mine = (int)slot - before;
+    const uint64_t has = __ballot(lane < p.N && mine >= 0 && mine < tiles);
+    if (has == 0) return false;
+    n = __builtin_ctzll(has);
+    row0 = (int64_t)(__builtin_amdgcn_readlane(tiles, n) - 1 -
+                     __builtin_amdgcn_readlane(mine, n)) * tile_rows;
+  }
+  return set_tile(p, __builtin_amdgcn_readfirstlane(n), row0, t);
 }
 
 __device__ __forceinline__ float max_over_groups(float x) {
@@ -261,14 +304,13 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_tile_kernel(AttnParams p
 
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // a key/value head's tiles share an XCD and its L2 (blocks go to the XCDs round robin);
-  // the last tiles of a sequence see the most keys and start first
+  // a key/value head's tiles share an XCD and its L2 (blocks go to the XCDs round robin)
   const unsigned units = gridDim.x / (unsigned)p.splits;
   const int split = (int)(blockIdx.x / units);
   const unsigned unit = blockIdx.x % units;
   const int hk = (int)(unit % (unsigned)p.Hk);
   Tile t;
-  if (!find_tile(p, units / (unsigned)p.Hk - 1 - unit / (unsigned)p.Hk, ROWS, t)) return;
+  if (!find_tile_longest_first(p, unit / (unsigned)p.Hk, units / (unsigned)p.Hk, ROWS, t)) return;
 
   // ---- this wave's rows: their operand of the first product, their last visible key
   const int off = t.Lk - t.Lq;
