@@ -628,34 +628,46 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_token_kernel(AttnParams 
   }
 }
 
-// Joins the splits of a row: D / 4 threads per (query token, head).
+// Joins the splits of a row, one wave per (query token, head): lane s weighs split s (there
+// are at most 64), then the lanes share the row's D values.
 template <int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
-  constexpr int TPR = D / 4;
-  const int64_t at = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
+  constexpr int V = D / 64;  // values per lane
+  typedef float vec __attribute__((ext_vector_type(V)));
+  const int lane = threadIdx.x & 63;
+  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int64_t rows = p.Tq_total * p.Hq;
   if (at >= rows) return;
   if (p.cu_q != nullptr) {  // a query outside every sequence keeps its rows
     const int64_t token = at / p.Hq;
     if (token < p.cu_q[0] || token >= p.cu_q[p.N]) return;
   }
-  const int c = (threadIdx.x % TPR) * 4;
-  float m = kNone;
-  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, p.ws_ml[2 * (s * rows + at)]);
-  const float base = m == kNone ? 0.f : m;
-  float l = 0.f;
-  f32x4_t o = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < p.splits; ++s) {
-    const int64_t w = s * rows + at;
-    const f32x2_t ml = *reinterpret_cast<const f32x2_t*>(p.ws_ml + 2 * w);
-    const float f = __builtin_amdgcn_exp2f(ml[0] - base);
-    l += ml[1] * f;
-    o += *reinterpret_cast<const f32x4_t*>(p.ws_o + w * D + c) * f;
+  f32x2_t ml = {kNone, 0.f};
+  if (lane < p.splits) ml = *reinterpret_cast<const f32x2_t*>(p.ws_ml + 2 * (lane * rows + at));
+  float m = ml[0];
+#pragma unroll
+  for (int x = 1; x < 64; x *= 2) m = fmaxf(m, __shfl_xor(m, x));
+  const float f = __builtin_amdgcn_exp2f(ml[0] - (m == kNone ? 0.f : m));
+  float l = ml[1] * f;
+#pragma unroll
+  for (int x = 1; x < 64; x *= 2) l += __shfl_xor(l, x);
+  const float* o = p.ws_o + at * D + lane * V;
+  vec sum = {};
+  for (int s0 = 0; s0 < p.splits; s0 += 8) {  // eight loads in flight
+    vec x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x[i] = s0 + i < p.splits ? *reinterpret_cast<const vec*>(o + (s0 + i) * rows * D) : vec{};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      sum += x[i] * __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), (s0 + i) & 63));
   }
   const float g = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-  *reinterpret_cast<u32x2_t*>(p.out + at * D + c) =
-      u32x2_t{pack_bf16(o[0] * g, o[1] * g), pack_bf16(o[2] * g, o[3] * g)};
-  if (p.lse != nullptr && c == 0) p.lse[at] = l == 0.f ? kNone : (m + __builtin_amdgcn_logf(l)) * kLn2;
+  u16* out = p.out + at * D + lane * V;
+  if constexpr (V == 2) *reinterpret_cast<unsigned*>(out) = pack_bf16(sum[0] * g, sum[1] * g);
+  else out[0] = (u16)pack_bf16(sum[0] * g, 0.f);
+  if (p.lse != nullptr && lane == 0)
+    p.lse[at] = l == 0.f ? kNone : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 template <int D>
@@ -671,8 +683,8 @@ hipError_t go(const AttnParams& p, const AttnSchedule& s, hipStream_t stream) {
     attn_tile_kernel<D, 2><<<grid, kAttnThreads, 0, stream>>>(p);
   }
   if (p.splits > 1) {
-    const int64_t rows = p.Tq_total * p.Hq, per = 256 / (D / 4);
-    attn_join_kernel<D><<<dim3((unsigned)((rows + per - 1) / per)), 256, 0, stream>>>(p);
+    const int64_t rows = p.Tq_total * p.Hq;
+    attn_join_kernel<D><<<dim3((unsigned)((rows + 3) / 4)), 256, 0, stream>>>(p);
   }
   return hipGetLastError();
 }

@@ -214,12 +214,18 @@ int la_check(const void* q, int64_t q_row, const void* k, int64_t k_row, const v
   return KDA_OK;
 }
 
-// Parts of each row's keys when the caller leaves the choice: as many as give each compute
-// unit kWant workgroups, with at least kLeast keys a part (of a sequence of mean length).
+// Parts of each row's keys when the caller leaves the choice, from a sequence's mean number
+// of keys.  Single tokens: one workgroup per compute unit, from 1024 keys on and at least 256
+// a part (8192 keys, 8 key/value heads: 80 us in one part, 14 in 32; 4 such sequences of 4096
+// keys: 48 and 16 in 8; 32 sequences: more parts only cost).  Tiles of rows: two workgroups
+// per compute unit and at least 512 keys a part, or 1024 when every second unit has a tile
+// anyway (256 queries, 8192 keys, 32/8 heads: 161 us in one part, 51 in 8; 1024 queries and
+// keys: 27 in one, 38 in two, whose partial results cost more than they save).
 int64_t attn_auto_splits(const kda::AttnSchedule& s, int64_t slots, int64_t Hk, int64_t mean_k) {
-  const int64_t want = (s.tokens ? 4 : 2) * (int64_t)kda::device_cus();
-  const int64_t least = s.tokens ? 256 : 512;
-  int64_t n = want / (slots > 0 ? slots * Hk : 1);
+  const int64_t units = slots * Hk, cus = kda::device_cus();
+  if (units < 1 || (s.tokens && mean_k < 1024)) return 1;
+  int64_t n = (s.tokens ? cus : 2 * cus) / units;
+  const int64_t least = s.tokens ? 256 : 2 * units < cus ? 512 : 1024;
   if (n > mean_k / least) n = mean_k / least;
   return n < 1 ? 1 : n > 64 ? 64 : n;
 }
