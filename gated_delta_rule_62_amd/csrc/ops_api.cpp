@@ -140,7 +140,7 @@ int64_t la_segment(int64_t T_total, int64_t N, int64_t H, int64_t D, int64_t seg
 
 // Whether every launch of a la call stays below 2^32 work-items and its slots in range.
 bool la_grid_ok(int64_t T_total, int64_t N, int64_t H, int64_t seg) {
-  const int64_t most = (((int64_t)1 << 32) - 1) / 256 / 8;  // in units of eight workgroups
+  const int64_t most = (((int64_t)1 << 32) - 1) / 512 / 8;  // eight workgroups of 512 threads
   const int64_t items = seg ? kda::la_slots(T_total, N, seg) : N;
   if (items > most * 8 / H - 8) return false;
   return !seg || N <= most / H / 2;  // the scan: up to 16 workgroups per (sequence, head)
@@ -252,8 +252,10 @@ int attn_sizes(int64_t N, int64_t Bq, int64_t Tq, int64_t Bk, int64_t Tk, int64_
   int64_t sp = splits ? splits : attn_auto_splits(*sched, slots, Hk, mean_k);
   // every launch below 2^32 work-items
   const int64_t most = (((int64_t)1 << 32) - 1) / kda::kAttnThreads;
-  if (N > most / Hk || slots > most / Hk || total > most / Hq) return KDA_ERR_BAD_SHAPE;
-  if (slots * Hk > most / sp) {
+  const int64_t tiles = kda::attn_slots(total, N, G, sched->rows) + (Bq == N ? N : 0);
+  if (tiles > most / Hk) return KDA_ERR_BAD_SHAPE;
+  // ... the join's of four rows a workgroup among them
+  if (sp > 1 && (tiles * Hk > most / sp || total > 4 * most / Hq)) {
     if (splits) return KDA_ERR_BAD_SHAPE;
     sp = 1;
   }

@@ -146,14 +146,17 @@ def _state(name, t, N, H, D, dev):
 
 
 def _workspace(workspace, need, dev, stream):
-    """The caller's workspace, or one from torch's allocator for this call."""
+    """Address, size and owner of the caller's workspace, or of one from torch's allocator
+    for this call (taken for the stream it runs on, so that nothing else uses it meanwhile)."""
     if workspace is None:
         if need == 0:
             return None, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        if stream is not None:  # the allocator knows only the current stream
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
             s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream, dev)
-            workspace.record_stream(s)
+            with torch.cuda.stream(s):
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     elif workspace.dtype != torch.uint8 or workspace.dim() != 1:
         raise ValueError("workspace must be a 1-d uint8 tensor")
     elif workspace.device != dev or not workspace.is_contiguous():

@@ -165,6 +165,13 @@ def test_caches_beyond_32_bit_offsets():
         _check_seq(out[n], lse[n], q[n], k[n, :L], v[n, :L], 0.1, "row %d" % n)
 
 
+def test_long_caches_in_the_automatic_parts():
+    """Lengths that the library splits by itself, odd ones, packed and as cache rows."""
+    assert kda.kda_attn_workspace_bytes(1, 1, 3, 1, 20001, 6, 2, 128) > 0
+    _packed(61, [3], [20001], 6, 2, 128)
+    _packed(62, [150], [5003], 4, 1, 64)
+
+
 def test_nan_stays_in_its_head():
     g = _gen(7)
     q, k, v = (_normal(g, 1, 90, 4, 64) for _ in range(3))

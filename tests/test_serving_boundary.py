@@ -192,5 +192,10 @@ def test_attn_refusals(lib):
     assert lib.kda_attn_workspace_bytes(*sizes, 1) == 0
     assert lib.kda_attn_workspace_bytes(1, 1, 1, 1, 8192, 32, 8, 128, 0) > 0
     assert lib.kda_attn_workspace_bytes(1, 1, 8192, 1, 8192, 32, 8, 128, 0) == 0
+    # a million query tokens of 96 heads is one launch; parts of them would be too many rows
+    big = dict(N=1, Bq=1, Bk=1, Tq=1 << 20, Tk=1 << 20, Hq=96, Hk=8, q_row=96 * 128, k_row=8 * 128,
+               v_row=8 * 128, q=100 * GB, k=200 * GB, v=300 * GB, out=400 * GB, lse=500 * GB)
+    assert st(**big) == kda.KDA_OK
+    assert st(**big, splits=2, ws=600 * GB, ws_bytes=1 << 50) == kda.KDA_ERR_BAD_SHAPE
     for bad in ((0,) + sizes[1:], sizes[:7] + (80,)):
         assert lib.kda_attn_workspace_bytes(*bad, 0) == kda.KDA_ERR_BAD_SHAPE
