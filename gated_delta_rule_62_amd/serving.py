@@ -8,64 +8,34 @@ turn status codes into exceptions; every computation runs in the library's kerne
 from __future__ import annotations
 
 import torch
-from torch import bfloat16 as bf16, float32 as fp32
 
 from . import KdaError, load_library
 
+try:
+    from ._tensor_args import optional as _optional, rows as _rows, tensor as _tensor
+except ImportError as e:
+    raise ImportError("the bindings' argument checks (_tensor_args.so) are not built; run "
+                      "gated_delta_rule_62_amd.build() (or __graft_entry__.build())") from e
 
-def _tensor(name, t, dtype, shape, dev):
-    """Address of a contiguous tensor of this dtype, shape and device."""
-    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
-        return t.data_ptr()
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise ValueError("%s must be %s %s, got %s %s" % (name, dtype, list(shape), t.dtype,
-                                                          list(t.shape)))
-    if t.device != dev:
-        raise ValueError("every tensor must live on the same GPU")
-    raise ValueError("%s must be contiguous" % name)
+# dtype codes of _tensor_args (the first two are the C ABI's state dtypes)
+bf16, fp32, int64 = 0, 1, 2
 
 
-def _optional(name, t, dtype, shape, dev):
-    return None if t is None else _tensor(name, t, dtype, shape, dev)
-
-
-def _rows(name, t, dtype, shape, dev):
-    """Address and row stride (in elements) of a bf16 tensor [..., heads, D] whose tokens lie
-    one fixed row stride apart."""
-    heads, D = shape[-2:]
-    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
-        return t.data_ptr(), heads * D
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise ValueError("%s must be %s %s, got %s %s" % (name, dtype, list(shape), t.dtype,
-                                                          list(t.shape)))
-    if t.device != dev:
-        raise ValueError("every tensor must live on the same GPU")
-    st = t.stride()
-    if (st[-1] == 1 or D == 1) and (st[-2] == D or heads == 1):
-        if len(shape) == 3:
-            return t.data_ptr(), st[0] if shape[0] > 1 else heads * D
-        B, T = shape[:2]
-        row = st[1] if T > 1 else st[0] if B > 1 else heads * D
-        if B == 1 or T == 1 or st[0] == T * row:
-            return t.data_ptr(), row
-    raise ValueError("%s must have contiguous heads, its tokens one row stride apart" % name)
-
-
-def _device(q):
+def _device(q) -> int:
     if not q.is_cuda:
         raise ValueError("every tensor must live on the same GPU")
-    return q.device
+    return q.get_device()
 
 
 def _stream_ptr(stream, dev):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev.index)
+        return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _launch(fn, dev, args) -> None:
     """Calls a C operator with dev current (the library launches on the current device)."""
-    if torch._C._cuda_getDevice() == dev.index:
+    if torch._C._cuda_getDevice() == dev:
         st = fn(*args)
     else:
         with torch.cuda.device(dev):
@@ -75,10 +45,10 @@ def _launch(fn, dev, args) -> None:
 
 
 def _dtype_code(t):
-    if t.dtype is bf16:
-        return 0
-    if t.dtype is fp32:
-        return 1
+    if t.dtype is torch.bfloat16:
+        return bf16
+    if t.dtype is torch.float32:
+        return fp32
     raise TypeError("state tensors must be bfloat16 or float32, got %s" % t.dtype)
 
 
@@ -86,9 +56,10 @@ def _pool(state, slot_in, slot_out, N, H, D, dev):
     if state.dim() != 4:
         raise ValueError("state must be [slots,H,D,D]")
     slots = state.shape[0]
-    return (_tensor("state", state, state.dtype, (slots, H, D, D), dev), _dtype_code(state), slots,
-            _optional("slot_in", slot_in, torch.int64, (N,), dev),
-            _optional("slot_out", slot_out, torch.int64, (N,), dev))
+    code = _dtype_code(state)
+    return (_tensor("state", state, code, (slots, H, D, D), dev), code, slots,
+            _optional("slot_in", slot_in, int64, (N,), dev),
+            _optional("slot_out", slot_out, int64, (N,), dev))
 
 
 def kda_step(q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound, state, slot_in=None,
@@ -142,7 +113,8 @@ def _state(name, t, N, H, D, dev):
     """Address and dtype code of a prompt's initial or final states, or nothing."""
     if t is None:
         return None, 0
-    return _tensor(name, t, t.dtype, (N, H, D, D), dev), _dtype_code(t)
+    code = _dtype_code(t)
+    return _tensor(name, t, code, (N, H, D, D), dev), code
 
 
 def _workspace(workspace, need, dev, stream):
@@ -152,14 +124,14 @@ def _workspace(workspace, need, dev, stream):
         if need == 0:
             return None, 0, None
         if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(need, dtype=torch.uint8, device="cuda:%d" % dev)
         else:
             s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream, dev)
             with torch.cuda.stream(s):
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+                workspace = torch.empty(need, dtype=torch.uint8, device="cuda:%d" % dev)
     elif workspace.dtype != torch.uint8 or workspace.dim() != 1:
         raise ValueError("workspace must be a 1-d uint8 tensor")
-    elif workspace.device != dev or not workspace.is_contiguous():
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and live on the same GPU")
     return workspace.data_ptr(), workspace.numel(), workspace
 
@@ -190,14 +162,14 @@ def kda_la_fwd(q, k, v, g, scale, out, decay=None, initial_state=None, final_sta
     B, T, H, D = v.shape
     Hk = q.shape[2]
     dev = _device(q)
-    if torch._C._cuda_getDevice() != dev.index:  # schedules go by the current device
+    if torch._C._cuda_getDevice() != dev:  # schedules go by the current device
         with torch.cuda.device(dev):
             return kda_la_fwd(q, k, v, g, scale, out, decay, initial_state, final_state,
                               cu_seqlens, segment, workspace, stream)
     cu, N = None, B
     if cu_seqlens is not None:
         N = cu_seqlens.numel() - 1
-        cu = _tensor("cu_seqlens", cu_seqlens, torch.int64, (N + 1,), dev)
+        cu = _tensor("cu_seqlens", cu_seqlens, int64, (N + 1,), dev)
     lib = load_library()
     need = lib.kda_la_workspace_bytes(B * T, N, H, D, int(segment))
     ws, ws_bytes, _keep = _workspace(workspace, max(need, 0), dev, stream)
@@ -241,7 +213,7 @@ def kda_attn_fwd(q, k, v, scale, out, lse=None, cu_seqlens_q=None, cu_seqlens_k=
     Bq, Tq, Hq, D = q.shape
     Bk, Tk, Hk, _ = k.shape
     dev = _device(q)
-    if torch._C._cuda_getDevice() != dev.index:  # schedules go by the current device
+    if torch._C._cuda_getDevice() != dev:  # schedules go by the current device
         with torch.cuda.device(dev):
             return kda_attn_fwd(q, k, v, scale, out, lse, cu_seqlens_q, cu_seqlens_k, k_lens,
                                 splits, workspace, stream)
@@ -253,8 +225,8 @@ def kda_attn_fwd(q, k, v, scale, out, lse=None, cu_seqlens_q=None, cu_seqlens_k=
             *_rows("v", v, bf16, (Bk, Tk, Hk, D), dev), float(scale),
             _tensor("out", out, bf16, (Bq, Tq, Hq, D), dev),
             _optional("lse", lse, fp32, (Bq, Tq, Hq), dev),
-            _optional("cu_seqlens_q", cu_seqlens_q, torch.int64, (N + 1,), dev),
-            _optional("cu_seqlens_k", cu_seqlens_k, torch.int64, (N + 1,), dev),
-            _optional("k_lens", k_lens, torch.int64, (N,), dev), N, Bq, Tq, Bk, Tk, Hq, Hk, D,
+            _optional("cu_seqlens_q", cu_seqlens_q, int64, (N + 1,), dev),
+            _optional("cu_seqlens_k", cu_seqlens_k, int64, (N + 1,), dev),
+            _optional("k_lens", k_lens, int64, (N,), dev), N, Bq, Tq, Bk, Tk, Hq, Hk, D,
             int(splits), ws, ws_bytes, _stream_ptr(stream, dev))
     _launch(lib.kda_attn_fwd, dev, args)
