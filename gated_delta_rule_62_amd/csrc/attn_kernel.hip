@@ -18,7 +18,7 @@
 // outgrows it by 2^8: p then reaches 256 at most, which costs no accuracy in a float, and
 // almost every step skips the rescaling of the output.  p is rounded to bf16 for the
 // product (the sum uses the unrounded p): with the output's own rounding that stays below
-// 1.5 roundings of out.
+// 1.5 roundings of out.  The kernel for few rows takes a second bf16 part of p.
 //
 // Few rows leave the device idle; then `splits` workgroups share a tile's keys, write
 // unnormalised fp32 outputs with their maximum and sum, and a second kernel joins them.
@@ -549,9 +549,16 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_token_kernel(AttnParams 
     acc.raise(x, p.c);
 #pragma unroll
     for (int j = 0; j < JT; ++j) acc.exps(x[j], p.c);
-    u32x4_t pr[NI];
+    // p in two bf16 parts: the products are free beside the loads
+    u32x4_t pr[NI], pr2[NI];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) pr[i] = p_op(x[0][i], x[1][i]);
+    for (int i = 0; i < NI; ++i) {
+      pr[i] = p_op(x[0][i], x[1][i]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        pr2[i][e] = pack_bf16(x[e >> 1][i][2 * (e & 1)] - bf_lo(pr[i][e]),
+                              x[e >> 1][i][2 * (e & 1) + 1] - bf_hi(pr[i][e]));
+    }
     const int row = 4 * lg + (l16 >> 2);
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
@@ -560,7 +567,10 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_token_kernel(AttnParams 
                     hi = ds_read_tr(&sm.s.v[wave][buf][row + 16][c]);
       const u32x4_t vt = {lo[0], lo[1], hi[0], hi[1]};
 #pragma unroll
-      for (int i = 0; i < NI; ++i) acc.o[d][i] = mfma(vt, pr[i], acc.o[d][i]);
+      for (int i = 0; i < NI; ++i) {
+        acc.o[d][i] = mfma(vt, pr2[i], acc.o[d][i]);
+        acc.o[d][i] = mfma(vt, pr[i], acc.o[d][i]);
+      }
     }
     // this step's reads are done before its place is written again
     __builtin_amdgcn_s_waitcnt(kWaitLds);
@@ -691,8 +701,7 @@ hipError_t go(const AttnParams& p, const AttnSchedule& s, hipStream_t stream) {
 
 }  // namespace
 
-AttnSchedule attn_schedule(int64_t Tq_total, int64_t N, int64_t G, int D) {
-  (void)D;
+AttnSchedule attn_schedule(int64_t Tq_total, int64_t N, int64_t G) {
   const int64_t mean = (Tq_total * G + N - 1) / N;  // rows of a sequence and key/value head
   if (mean <= 64) {
     const int tiles = mean <= 16 ? 1 : mean <= 32 ? 2 : 4;

@@ -90,14 +90,6 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// Makes one wave's LDS writes visible to its other lanes, and keeps its later writes
-// behind its reads.
-__device__ __forceinline__ void wave_lds_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
-}
-
 // Four 16-bit values of one column from four rows: inside each 16-lane group, lane i
 // receives element i%4 of the 8-byte pieces that lanes i/4, 4 + i/4, 8 + i/4 and
 // 12 + i/4 address.

@@ -23,7 +23,7 @@
 //
 // Roundings.  Scores times weights, and the state as an operand of S q, are rounded to
 // bf16 once each: out is a bf16 sum of two such parts, so its error stays below 1.5 of
-// its own rounding.  The state itself must not lose bits at each of thousands of chunks:
+// its own rounding (second parts of both cost 5-13% of a large call; small ones have them).  The state itself must not lose bits at each of thousands of chunks:
 // its update multiplies k (exact in bf16) by the weighted v in two or three bf16 parts,
 // whose sum holds the fp32 product to 2^-17 or 2^-25.
 //
@@ -59,13 +59,14 @@ struct LaCfg {
   static constexpr int PASSES = C / RPP;
 };
 
-template <int D, bool STATE_ONLY>
+template <int D, bool STATE_ONLY, bool FINE>
 struct alignas(16) LaSmem {
   using F = LaCfg<D>;
   u16 Q[STATE_ONLY ? 1 : C][F::LD];
   u16 K[C][F::LD];
   u16 V[C][F::LD];
   u16 A[STATE_ONLY ? 1 : C][F::LDA];  // scores; columns in the order of a reduction's slots
+  u16 A2[FINE ? C : 1][F::LDA];       // their second parts
   float p[C];       // inclusive prefix of the base-2 log decay inside its 16-token tile
   float ep[C];      // 2^p
   float es[C];      // 2^(sum of what follows in the tile)
@@ -179,11 +180,18 @@ __device__ __forceinline__ void state_store(const f32x4_t (&S)[KT], void* dst, i
   }
 }
 
-// PARTS: bf16 parts of the weighted v in the state update.
-template <int D, bool STATE_ONLY, int PARTS>
-__global__ __launch_bounds__(LaCfg<D>::THREADS, D == 128 || STATE_ONLY ? 4 : 3) void la_kernel(LaParams p) {
+// The part of a pair that its bf16 rounding w leaves, as another bf16 pair.
+__device__ __forceinline__ unsigned rest(float lo, float hi, unsigned w) {
+  return pack_bf16(lo - bf_lo(w), hi - bf_hi(w));
+}
+
+// PARTS: bf16 parts of the weighted v in the state update.  FINE: second parts of the scores
+// and of the state operand.
+template <int D, bool STATE_ONLY, int PARTS, bool FINE>
+__global__ __launch_bounds__(LaCfg<D>::THREADS,
+                             (D == 128 || STATE_ONLY ? 4 : D == 64 ? 3 : 2)) void la_kernel(LaParams p) {
   using F = LaCfg<D>;
-  __shared__ LaSmem<D, STATE_ONLY> sm;
+  __shared__ LaSmem<D, STATE_ONLY, FINE> sm;
   Unit u;
   if (!find_unit(p, blockIdx.x, u)) return;  // uniform per workgroup
   if (STATE_ONLY && u.s == u.nseg - 1) return;  // no segment starts from this one's end
@@ -328,8 +336,12 @@ __global__ __launch_bounds__(LaCfg<D>::THREADS, D == 128 || STATE_ONLY ? 4 : 3) 
 #pragma unroll
           for (int r = 0; r < 4; ++r) a[r] *= f * ej[r];
         }
-        *reinterpret_cast<u32x2_t*>(&sm.A[ti][32 * (j >> 1) + 8 * lg + 4 * (j & 1)]) =
-            u32x2_t{pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])};
+        const u32x2_t w = {pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])};
+        const int col = 32 * (j >> 1) + 8 * lg + 4 * (j & 1);
+        *reinterpret_cast<u32x2_t*>(&sm.A[ti][col]) = w;
+        if constexpr (FINE)
+          *reinterpret_cast<u32x2_t*>(&sm.A2[ti][col]) =
+              u32x2_t{rest(a[0], a[1], w[0]), rest(a[2], a[3], w[1])};
       }
       // ---- the state's part: O^T = S Q^T, lane holds token l16 and four values
 #pragma unroll
@@ -339,11 +351,16 @@ __global__ __launch_bounds__(LaCfg<D>::THREADS, D == 128 || STATE_ONLY ? 4 : 3) 
         const f32x4_t x = S[2 * ks], y = S[2 * ks + 1];
         const u32x4_t s_op = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
                               pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+        u32x4_t s2;
+        if constexpr (FINE)
+          s2 = u32x4_t{rest(x[0], x[1], s_op[0]), rest(x[2], x[3], s_op[1]),
+                       rest(y[0], y[1], s_op[2]), rest(y[2], y[3], s_op[3])};
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-          O[i] = mfma(s_op,
-                      *reinterpret_cast<const u32x4_t*>(&sm.Q[16 * i + l16][32 * ks + 8 * lg]),
-                      O[i]);
+        for (int i = 0; i < RT; ++i) {
+          const u32x4_t q = *reinterpret_cast<const u32x4_t*>(&sm.Q[16 * i + l16][32 * ks + 8 * lg]);
+          if constexpr (FINE) O[i] = mfma(s2, q, O[i]);
+          O[i] = mfma(s_op, q, O[i]);
+        }
       }
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
@@ -376,6 +393,11 @@ __global__ __launch_bounds__(LaCfg<D>::THREADS, D == 128 || STATE_ONLY ? 4 : 3) 
         for (int i = 2 * b; i < RT; ++i) {
           u32x4_t a = *reinterpret_cast<const u32x4_t*>(&sm.A[16 * i + l16][32 * b + 8 * lg]);
           if (i == 2 * b) a = u32x4_t{a[0], a[1], 0u, 0u};
+          if constexpr (FINE) {
+            u32x4_t a2 = *reinterpret_cast<const u32x4_t*>(&sm.A2[16 * i + l16][32 * b + 8 * lg]);
+            if (i == 2 * b) a2 = u32x4_t{a2[0], a2[1], 0u, 0u};
+            O[i] = mfma(vt[b], a2, O[i]);
+          }
           O[i] = mfma(vt[b], a, O[i]);
         }
       // into the place of Q, whose reads are done: whole rows leave with the next chunk
@@ -481,26 +503,31 @@ __global__ __launch_bounds__(256) void la_scan_kernel(LaParams p) {
   *reinterpret_cast<f32x4_t*>(w) = S;
 }
 
-template <int D, int PARTS>
+template <int D, int PARTS, bool FINE>
 hipError_t go(const LaParams& p, hipStream_t stream) {
   using F = LaCfg<D>;
   const int64_t run = 8 * (int64_t)p.group;
   const int64_t items = p.seg ? p.slots : p.N;
   const int64_t blocks = (items * (p.H / p.group) + 7) / 8 * run;
   if (p.seg) {
-    la_kernel<D, true, PARTS><<<dim3((unsigned)blocks), F::THREADS, 0, stream>>>(p);
+    la_kernel<D, true, PARTS, false><<<dim3((unsigned)blocks), F::THREADS, 0, stream>>>(p);
     constexpr int BLOCKS = (D * D / 4 + 255) / 256;
     la_scan_kernel<D><<<dim3((unsigned)((int64_t)p.N * p.H * BLOCKS)), 256, 0, stream>>>(p);
   }
-  la_kernel<D, false, PARTS><<<dim3((unsigned)blocks), F::THREADS, 0, stream>>>(p);
+  la_kernel<D, false, PARTS, FINE><<<dim3((unsigned)blocks), F::THREADS, 0, stream>>>(p);
   return hipGetLastError();
 }
 
 // An fp32 final state keeps three parts; where none leaves, or one rounded to bf16, two
 // parts hold it to 2^-17 and save a third of the update's products.
+// Few outputs take every second part: their call is bounded by its latency, not by products
+// (128 tokens of 2 heads: 7.8 us either way; 512 tokens of 8 heads 23 and 24), and the fewer
+// roundings a result has, the less they average out.
 template <int D>
 hipError_t by_parts(const LaParams& p, hipStream_t stream) {
-  return p.s_out != nullptr && p.s_out_fp32 ? go<D, 3>(p, stream) : go<D, 2>(p, stream);
+  if (p.T_total * p.H <= 2048) return go<D, 3, true>(p, stream);
+  return p.s_out != nullptr && p.s_out_fp32 ? go<D, 3, false>(p, stream)
+                                             : go<D, 2, false>(p, stream);
 }
 
 }  // namespace

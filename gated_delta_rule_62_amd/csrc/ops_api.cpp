@@ -244,7 +244,7 @@ int attn_sizes(int64_t N, int64_t Bq, int64_t Tq, int64_t Bk, int64_t Tk, int64_
   if (Tq > ((int64_t)1 << 40) / Bq || Tk > ((int64_t)1 << 40) / Bk) return KDA_ERR_BAD_SHAPE;
   if (splits < 0 || splits > 64) return KDA_ERR_BAD_SCHEDULE;
   const int64_t G = Hq / Hk, total = Bq * Tq;
-  *sched = kda::attn_schedule(total, N, G, static_cast<int>(D));
+  *sched = kda::attn_schedule(total, N, G);
   // tiles of rows: for batch rows as many as each has, for packed ones a bound
   const int64_t slots = Bq == N ? N * ((Tq * G + sched->rows - 1) / sched->rows)
                                 : kda::attn_slots(total, N, G, sched->rows);

@@ -100,7 +100,7 @@ struct AttnSchedule {
   int rows;                // rows per workgroup
 };
 
-AttnSchedule attn_schedule(int64_t Tq_total, int64_t N, int64_t G, int D);
+AttnSchedule attn_schedule(int64_t Tq_total, int64_t N, int64_t G);
 // Tiles of one key/value head: a sequence's tiles never share a slot with another's.
 constexpr int64_t attn_slots(int64_t Tq_total, int64_t N, int64_t G, int64_t rows) {
   return Tq_total * G / rows + N;
