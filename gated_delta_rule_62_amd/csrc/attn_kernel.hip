@@ -20,6 +20,10 @@
 // product (the sum uses the unrounded p): with the output's own rounding that stays below
 // 1.5 roundings of out.  The kernel for few rows takes a second bf16 part of p.
 //
+// Infinities and NaN of v behind a row's last key would reach it through the product, as zero
+// times them.  On the diagonal's tiles they are dropped from LDS, and what they mean for the
+// rows that do see them is added after the loop (looking for them: under 1% of a prompt).
+//
 // Few rows leave the device idle; then `splits` workgroups share a tile's keys, write
 // unnormalised fp32 outputs with their maximum and sum, and a second kernel joins them.
 #include "api_util.h"
@@ -272,6 +276,55 @@ __device__ __forceinline__ u32x4_t p_op(f32x4_t a, f32x4_t b) {
                  pack_bf16(b[2], b[3])};
 }
 
+// What infinities and NaN of v add to the rows that see them, 32 keys: `key` is the first of
+// this lane's (key .. + 3 and key + 16 .. + 19), vt(d) the operand of v's 16-column tile d.
+template <int D, int NI, class V>
+__device__ __forceinline__ void add_odd(Acc<D, NI>& acc, int key, const int (&last)[NI], V vt) {
+  u32x4_t sees[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int k = key + 16 * (e >> 1) + 2 * (e & 1);
+      sees[i][e] = (k <= last[i] ? 0x3f80u : 0u) | (k + 1 <= last[i] ? 0x3f800000u : 0u);
+    }
+#pragma unroll
+  for (int d = 0; d < D / 16; ++d) {
+    u32x4_t code = vt(d);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) code[e] = odd_split(code[e]).code;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const f32x4_t n = mfma(code, sees[i], f32x4_t{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        acc.o[d][i][r] += odd_value(n[r]);
+    }
+  }
+}
+
+// Lane `lane` of a group of `lanes` looks at its part of n bf16 in LDS; whether its wave found
+// any that is not finite.
+__device__ __forceinline__ bool any_odd(const u16* v, int n, int lane, int lanes) {
+  unsigned marks = 0;
+#pragma unroll 4
+  for (int e = lane * 8; e < n; e += lanes * 8) {
+    const u32x4_t w = *reinterpret_cast<const u32x4_t*>(v + e);
+    marks |= odd_marks(w[0]) | odd_marks(w[1]) | odd_marks(w[2]) | odd_marks(w[3]);
+  }
+  return __any((marks & 0x80008000u) != 0u);
+}
+// The same part with zeros in their place.
+__device__ __forceinline__ void drop_odd(u16* v, int n, int lane, int lanes) {
+#pragma unroll 1
+  for (int e = lane * 8; e < n; e += lanes * 8) {
+    u32x4_t w = *reinterpret_cast<const u32x4_t*>(v + e);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = odd_split(w[i]).finite;
+    *reinterpret_cast<u32x4_t*>(v + e) = w;
+  }
+}
+
 // One row's outputs, or with several splits its partial ones.  l is the whole sum.
 template <int D>
 __device__ __forceinline__ void store_row(const AttnParams& p, int64_t token, int head, int split,
@@ -301,6 +354,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_tile_kernel(AttnParams p
   constexpr int ROWS = 4 * 16 * NI;
   __shared__ alignas(1024) u16 sk[2][BN][D];
   __shared__ alignas(1024) u16 sv[2][BN][D];
+  __shared__ unsigned sodd[2][4];  // per wave: its quarter of a v tile is not all finite
 
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -340,7 +394,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_tile_kernel(AttnParams p
   const int keys = max(0, min(t.Lk, tile_end / p.G + off + 1));
   const int wave_keys =
       wrow < t.rows ? max(0, min(t.Lk, (min(t.rows, wrow + 16 * NI) - 1) / p.G + off + 1)) : 0;
-  const int all_keys = wrow / p.G + off + 1;
+  const int all_keys = wrow / p.G + off + 1, tile_all_keys = t.row0 / p.G + off + 1;
   // this split's steps
   const int steps = (keys + BN - 1) / BN, per = (steps + p.splits - 1) / p.splits;
   const int first = min(steps, split * per), end = min(steps, first + per);
@@ -376,14 +430,31 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_tile_kernel(AttnParams p
 
   Acc<D, NI> acc;
   acc.init();
+  auto v_op = [&](int b, int row, int d) {
+    const int c = ((2 * d + ((l16 & 3) >> 1)) ^ swz(row)) * 8 + 4 * (l16 & 1);
+    const u32x2_t lo = ds_read_tr(&sv[b][row][c]), hi = ds_read_tr(&sv[b][row + 16][c]);
+    return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+  };
+  bool odd = false;  // some step dropped infinities or NaN of v
   if (first < end) load(first);
   for (int s = first; s < end; ++s) {
     const int b = s & 1;
     // this wave's part of tile s is in LDS; behind the barrier every wave's is, and all have
     // read tile s - 1, whose buffer takes tile s + 1
     __builtin_amdgcn_s_waitcnt(kWaitLoads);
+    const bool diagonal = (s + 1) * BN > tile_all_keys;  // some row does not see all these keys
+    if (diagonal) {
+      const bool any = any_odd(&sv[b][BN / 4 * wave][0], BN / 4 * D, lane, 64);
+      if (lane == 0) sodd[b][wave] = any;
+    }
     lds_barrier();
     if (s + 1 < end) load(s + 1);
+    if (diagonal && __builtin_amdgcn_readfirstlane(sodd[b][0] | sodd[b][1] | sodd[b][2] |
+                                                   sodd[b][3])) {
+      odd = true;
+      drop_odd(&sv[b][0][0], BN * D, tid, kAttnThreads);
+      lds_barrier();
+    }
     if (s * BN < wave_keys) {  // uniform per wave
       f32x4_t x[JT][NI];
 #pragma unroll
@@ -420,14 +491,23 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_tile_kernel(AttnParams p
         const int row = 32 * js + 4 * lg + (l16 >> 2);
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          const int c = ((2 * d + ((l16 & 3) >> 1)) ^ swz(row)) * 8 + 4 * (l16 & 1);
-          const u32x2_t lo = ds_read_tr(&sv[b][row][c]), hi = ds_read_tr(&sv[b][row + 16][c]);
-          const u32x4_t vt = {lo[0], lo[1], hi[0], hi[1]};
+          const u32x4_t vt = v_op(b, row, d);
 #pragma unroll
           for (int i = 0; i < NI; ++i) acc.o[d][i] = mfma(vt, pr[i], acc.o[d][i]);
         }
       }
     }
+  }
+  // what was dropped, after the loop, where it takes no registers from it
+  for (int s = max(first, tile_all_keys / BN); odd && s < end; ++s) {
+    lds_barrier();  // reads of the tiles before are done
+    load(s);
+    __builtin_amdgcn_s_waitcnt(kWaitLoads);
+    lds_barrier();
+#pragma unroll
+    for (int js = 0; js < JT / 2; ++js)
+      add_odd(acc, s * BN + 32 * js + 4 * lg, last,
+              [&](int d) { return v_op(s & 1, 32 * js + 4 * lg + (l16 >> 2), d); });
   }
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
@@ -517,12 +597,26 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_token_kernel(AttnParams 
   acc.init();
   if (first + wave < end) load(first + wave, 0);
   if (first + wave + 4 < end) load(first + wave + 4, 1);
+  auto v_op = [&](int buf, int d) {
+    const int row = 4 * lg + (l16 >> 2);
+    const int c = ((2 * d + ((l16 & 3) >> 1)) ^ swz(row)) * 8 + 4 * (l16 & 1);
+    const u32x2_t lo = ds_read_tr(&sm.s.v[wave][buf][row][c]),
+                  hi = ds_read_tr(&sm.s.v[wave][buf][row + 16][c]);
+    return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+  };
+  bool odd = false;  // some step dropped infinities or NaN of v
   int buf = 0;
   for (int s = first + wave; s < end; s += 4, buf ^= 1) {
     // the oldest step is in place when only the next one's loads are in flight
     if (s + 4 < end) __builtin_amdgcn_s_waitcnt(kWaitLoads | (2 * IPT & 15) | (2 * IPT >> 4 << 14));
     else __builtin_amdgcn_s_waitcnt(kWaitLoads);
     asm volatile("" ::: "memory");
+    // some row does not see all of these keys
+    if ((s + 1) * KEYS > all_keys && any_odd(&sm.s.v[wave][buf][0][0], KEYS * D, lane, 64)) {
+      odd = true;
+      drop_odd(&sm.s.v[wave][buf][0][0], KEYS * D, lane, 64);
+      asm volatile("" ::: "memory");  // a wave's LDS accesses stay in order
+    }
     f32x4_t x[JT][NI];
 #pragma unroll
     for (int j = 0; j < JT; ++j) {
@@ -549,33 +643,42 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_token_kernel(AttnParams 
     acc.raise(x, p.c);
 #pragma unroll
     for (int j = 0; j < JT; ++j) acc.exps(x[j], p.c);
-    // p in two bf16 parts: the products are free beside the loads
+    // p in two bf16 parts, its upper half and the rest: the products are free beside the
+    // loads.  No part of a positive p is zero, so an infinity of v stays one.
     u32x4_t pr[NI], pr2[NI];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      pr[i] = p_op(x[0][i], x[1][i]);
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        pr2[i][e] = pack_bf16(x[e >> 1][i][2 * (e & 1)] - bf_lo(pr[i][e]),
-                              x[e >> 1][i][2 * (e & 1) + 1] - bf_hi(pr[i][e]));
-    }
-    const int row = 4 * lg + (l16 >> 2);
+      for (int e = 0; e < 4; ++e) {
+        const float lo = x[e >> 1][i][2 * (e & 1)], hi = x[e >> 1][i][2 * (e & 1) + 1];
+        pr[i][e] = __float_as_uint(lo) >> 16 | (__float_as_uint(hi) & 0xffff0000u);
+        pr2[i][e] = pack_bf16(__builtin_amdgcn_fmed3f(lo - bf_lo(pr[i][e]), 1.2e-38f, lo),
+                              __builtin_amdgcn_fmed3f(hi - bf_hi(pr[i][e]), 1.2e-38f, hi));
+      }
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
-      const int c = ((2 * d + ((l16 & 3) >> 1)) ^ swz(row)) * 8 + 4 * (l16 & 1);
-      const u32x2_t lo = ds_read_tr(&sm.s.v[wave][buf][row][c]),
-                    hi = ds_read_tr(&sm.s.v[wave][buf][row + 16][c]);
-      const u32x4_t vt = {lo[0], lo[1], hi[0], hi[1]};
+      const u32x4_t v = v_op(buf, d);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        acc.o[d][i] = mfma(vt, pr2[i], acc.o[d][i]);
-        acc.o[d][i] = mfma(vt, pr[i], acc.o[d][i]);
+        acc.o[d][i] = mfma(v, pr2[i], acc.o[d][i]);
+        acc.o[d][i] = mfma(v, pr[i], acc.o[d][i]);
       }
     }
     // this step's reads are done before its place is written again
     __builtin_amdgcn_s_waitcnt(kWaitLds);
     asm volatile("" ::: "memory");
     if (s + 8 < end) load(s + 8, buf);
+  }
+
+  // what was dropped, after the loop, where it takes no registers from it
+  for (int s = first + wave; odd && s < end; s += 4) {
+    if ((s + 1) * KEYS <= all_keys) continue;
+    load(s, 0);
+    __builtin_amdgcn_s_waitcnt(kWaitLoads);
+    asm volatile("" ::: "memory");
+    add_odd(acc, s * KEYS + 4 * lg, last, [&](int d) { return v_op(0, d); });
+    __builtin_amdgcn_s_waitcnt(kWaitLds);
+    asm volatile("" ::: "memory");
   }
 
   // ---- join the waves: maxima and sums first, then the outputs, one 16-row tile at a time

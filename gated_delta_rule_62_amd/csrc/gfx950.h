@@ -99,6 +99,31 @@ __device__ __forceinline__ u32x2_t ds_read_tr(const u16* p) {
       __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(p)));
 }
 
+// Infinities and NaN in v at tokens that a row does not see: a matrix product would make a NaN
+// of them and their zero weight.  odd_marks sets bits 15 and 31 where the bf16 halves of w are
+// not finite.  Where any is, products take odd_split's `finite` (zeros in their place), and one
+// of `code` with ones for the visible tokens counts the +inf, -inf and NaN of 32 tokens in
+// steps of 1, 2^8 and 2^16, exact in fp32; odd_value is what a count adds to the row.
+__device__ __forceinline__ unsigned odd_marks(unsigned w) {
+  return (w & 0x7f807f80u) + 0x00800080u;
+}
+struct OddSplit {
+  unsigned finite, code;
+};
+__device__ __forceinline__ OddSplit odd_split(unsigned w) {
+  auto code = [](unsigned h) {  // one half
+    const unsigned kind = (h & 0x7fu) != 0u ? 0x4780u : (h & 0x8000u) != 0u ? 0x4380u : 0x3f80u;
+    return (h & 0x7f80u) == 0x7f80u ? kind : 0u;
+  };
+  const unsigned lo = code(w & 0xffffu), hi = code(w >> 16);
+  return OddSplit{(lo ? 0u : w & 0xffffu) | (hi ? 0u : w & 0xffff0000u), lo | hi << 16};
+}
+__device__ __forceinline__ float odd_value(float count) {
+  const unsigned n = (unsigned)count;
+  const float inf = __builtin_inff(), plus = n & 0xff00ffu ? inf : 0.f;
+  return n & 0xffff00u ? plus - inf : plus;
+}
+
 }  // namespace dev
 }  // namespace kda
 

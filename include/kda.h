@@ -498,9 +498,8 @@ int64_t kda_la_workspace_bytes(int64_t T_total, int64_t num_seqs, int64_t H, int
  *                  kda_attn_workspace_bytes(num_seqs, Bq, Tq, Bk, Tk, Hq, Hk, D, splits)
  *                  bytes (KDA_ERR_BAD_WORKSPACE), scratch on return: calls that may overlap
  *                  in time need one each.  With splits 0 it may be NULL: one part then.
- * Scores and sums are fp32; probabilities are rounded to bf16 for their product with v.  A
- * non-finite v of one key may reach the outputs of earlier queries of its sequence and
- * head whose tile of keys it shares (zero probability times it).
+ * Scores and sums are fp32; probabilities are rounded to bf16 for their product with v.
+ * Infinities and NaN reach the outputs of the queries that see them and no others.
  */
 int kda_attn_fwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
                  int64_t v_row, float scale, void* out, float* lse, const int64_t* cu_seqlens_q,

@@ -185,6 +185,36 @@ def test_nan_stays_in_its_head():
     assert torch.equal(torch.isnan(out[0]).any(-1), want)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Lq,Lk,Hq,Hk,splits", [
+    (1, 700, 8, 2, 0), (4, 100, 8, 2, 0), (4, 100, 8, 2, 3), (40, 500, 2, 1, 1), (200, 200, 2, 2, 0),
+    (300, 333, 4, 2, 3), (150, 130, 12, 1, 0)])
+def test_infinities_and_nan_behind_the_last_visible_key(Lq, Lk, Hq, Hk, splits, D):
+    """Infinities and NaN in k and v reach the queries that see them, and nothing else."""
+    print("kda_attn_fwd odd v", Lq, Lk, Hq, Hk, splits, D, flush=True)
+    g = _gen(Lk + D)
+    q, k, v = _normal(g, 1, Lq, Hq, D), _normal(g, 1, Lk, Hk, D), _normal(g, 1, Lk, Hk, D)
+    inf, off = float("inf"), Lk - Lq
+    want, lse_w, bound, lse_b = _want(q[0], k[0], v[0], 0.1)
+    odd, bad = [(0, 1, inf), (1, 1, -inf), (2, 2, inf), (17, 3, -inf), (Lq // 2, D - 1, inf),
+                (Lq - 1, 40, float("nan")), (Lq - 1, 41, -inf)], v.clone()
+    for i, d, x in odd:  # as seen by query i and those behind it, in the last key/value head
+        if 0 <= i + off < Lk and i < Lq:
+            bad[0, i + off, Hk - 1, d] = x
+            want[i:, Hq - Hq // Hk:, d] += x
+    if Lk > Lq:
+        bad[0, 0, 0, 7] = inf  # a key that every query sees
+        want[:, :Hq // Hk, 7] += inf
+    kq, G = k.clone(), Hq // Hk
+    if off >= 0 and Lq > 20:  # a key nobody before its query sees
+        kq[0, 19 + off, 0] = float("nan")
+        want[19:, :G], lse_w[19:, :G] = float("nan"), float("nan")
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device=DEV)
+    kda.kda_attn_fwd(q, kq, bad, 0.1, out, lse=lse, splits=splits)
+    forms.check(out[0], want, bound, "out")
+    forms.check(lse[0], lse_w, lse_b, "lse")
+
+
 def test_prompt_then_tokens():
     """A prompt's attention, then tokens over the cache it filled: rows of one longer prompt."""
     g = _gen(8)
