@@ -306,13 +306,14 @@ __device__ __forceinline__ void add_odd(Acc<D, NI>& acc, int key, const int (&la
 // Lane `lane` of a group of `lanes` looks at its part of n bf16 in LDS; whether its wave found
 // any that is not finite.
 __device__ __forceinline__ bool any_odd(const u16* v, int n, int lane, int lanes) {
-  unsigned marks = 0;
+  float zero = 0.f;
 #pragma unroll 4
   for (int e = lane * 8; e < n; e += lanes * 8) {
     const u32x4_t w = *reinterpret_cast<const u32x4_t*>(v + e);
-    marks |= odd_marks(w[0]) | odd_marks(w[1]) | odd_marks(w[2]) | odd_marks(w[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) zero = dot_zero(w[i], zero);
   }
-  return __any((marks & 0x80008000u) != 0u);
+  return __any(zero != zero);
 }
 // The same part with zeros in their place.
 __device__ __forceinline__ void drop_odd(u16* v, int n, int lane, int lanes) {

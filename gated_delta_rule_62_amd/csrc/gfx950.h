@@ -99,14 +99,17 @@ __device__ __forceinline__ u32x2_t ds_read_tr(const u16* p) {
       __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(p)));
 }
 
-// Infinities and NaN in v at tokens that a row does not see: a matrix product would make a NaN
-// of them and their zero weight.  odd_marks sets bits 15 and 31 where the bf16 halves of w are
-// not finite.  Where any is, products take odd_split's `finite` (zeros in their place), and one
-// of `code` with ones for the visible tokens counts the +inf, -inf and NaN of 32 tokens in
-// steps of 1, 2^8 and 2^16, exact in fp32; odd_value is what a count adds to the row.
-__device__ __forceinline__ unsigned odd_marks(unsigned w) {
-  return (w & 0x7f807f80u) + 0x00800080u;
+// acc + 0 * (both bf16 of w): NaN from the first that is not finite.
+__device__ __forceinline__ float dot_zero(unsigned w, float acc) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, w), bf16x2_t{(__bf16)0.f, (__bf16)0.f}, acc,
+                                         false);
 }
+
+// Infinities and NaN in v at tokens that a row does not see: a matrix product would make a NaN
+// of them and their zero weight.  Where any is, products take odd_split's `finite` (zeros in
+// their place), and one of `code` with ones for the visible tokens counts the +inf, -inf and
+// NaN of 32 tokens in steps of 1, 2^8 and 2^16, exact in fp32; odd_value is what a count adds
+// to the row.
 struct OddSplit {
   unsigned finite, code;
 };

@@ -27,6 +27,11 @@
 // its update multiplies k (exact in bf16) by the weighted v in two or three bf16 parts,
 // whose sum holds the fp32 product to 2^-17 or 2^-25.
 //
+// Infinities and NaN of v would reach earlier tokens of their chunk, as zero times them in the
+// products.  A wave that finds any in its values of a chunk drops them and sets the outputs
+// from their tokens on, and the state, to NaN there.  Looking for them takes 1-2% of a large
+// call.
+//
 // Segments.  One workgroup per (sequence, head) leaves most of the device idle for a few
 // long sequences.  Then three launches split the tokens: a state-only pass sums every
 // segment's own contribution from a zero state (k and v only), an elementwise scan turns
@@ -62,16 +67,17 @@ struct LaCfg {
 template <int D, bool STATE_ONLY, bool FINE>
 struct alignas(16) LaSmem {
   using F = LaCfg<D>;
-  u16 Q[STATE_ONLY ? 1 : C][F::LD];
-  u16 K[C][F::LD];
-  u16 V[C][F::LD];
-  u16 A[STATE_ONLY ? 1 : C][F::LDA];  // scores; columns in the order of a reduction's slots
-  u16 A2[FINE ? C : 1][F::LDA];       // their second parts
   float p[C];       // inclusive prefix of the base-2 log decay inside its 16-token tile
   float ep[C];      // 2^p
   float es[C];      // 2^(sum of what follows in the tile)
   float w[C];       // 2^(sum of what follows in the chunk): weight of a token in the state
   float tile[RT];   // 2^(sum of the tile)
+  int from[D];      // first token of the chunk with an infinity or NaN of v, per value
+  u16 Q[STATE_ONLY ? 1 : C][F::LD];
+  u16 K[C][F::LD];
+  u16 V[C][F::LD];
+  u16 A[STATE_ONLY ? 1 : C][F::LDA];  // scores; columns in the order of a reduction's slots
+  u16 A2[FINE ? C : 1][F::LDA];       // their second parts
 };
 
 // One launch unit: which sequence and head, its tokens [t0, t1), its segment.
@@ -309,7 +315,7 @@ __global__ __launch_bounds__(LaCfg<D>::THREADS,
     if (inside(t + STEP)) load(t + STEP);
 
     const float d0 = sm.tile[0], d1 = sm.tile[1], d2 = sm.tile[2], d3 = sm.tile[3];
-    const float d_all = d0 * d1 * d2 * d3;
+    float d_all = d0 * d1 * d2 * d3;
     f32x4_t O[RT];
     if constexpr (!STATE_ONLY) {
       // ---- scores: ten 16x16 tiles (i, j <= i) over the waves, as K Q^T: lane holds token
@@ -377,12 +383,39 @@ __global__ __launch_bounds__(LaCfg<D>::THREADS,
     // 32 b + 16 + 4g + i
     const int tr = 4 * lg + (l16 >> 2);
     u32x4_t vt[C / 32];
+    auto read_v = [&]() {
 #pragma unroll
-    for (int b = 0; b < C / 32; ++b) {
-      const int c = 16 * wave + 4 * (l16 & 3);
-      const u32x2_t lo = ds_read_tr(&sm.V[32 * b + tr][c]),
-                    hi = ds_read_tr(&sm.V[32 * b + tr + 16][c]);
-      vt[b] = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+      for (int b = 0; b < C / 32; ++b) {
+        const int c = 16 * wave + 4 * (l16 & 3);
+        const u32x2_t lo = ds_read_tr(&sm.V[32 * b + tr][c]),
+                      hi = ds_read_tr(&sm.V[32 * b + tr + 16][c]);
+        vt[b] = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+      }
+    };
+    read_v();
+    bool odd = false;
+    if constexpr (!STATE_ONLY) {
+      float zero = 0.f;
+#pragma unroll
+      for (int b = 0; b < C / 32; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) zero = dot_zero(vt[b][e], zero);
+      odd = __any(zero != zero);
+      if (odd) {  // a wave's own values: nobody else reads them
+        const int c = 16 * wave + l16;
+        if (lg == 0) {
+          int from = C;
+#pragma unroll 1
+          for (int j = C - 1; j >= 0; --j)
+            if ((sm.V[j][c] & 0x7f80u) == 0x7f80u) {
+              sm.V[j][c] = 0;
+              from = j;
+            }
+          sm.from[c] = from;
+        }
+        asm volatile("" ::: "memory");  // a wave's LDS accesses stay in order
+        read_v();
+      }
     }
     if constexpr (!STATE_ONLY) {
       // ---- the chunk's own part of the output; the columns behind the diagonal tile are not
@@ -406,6 +439,16 @@ __global__ __launch_bounds__(LaCfg<D>::THREADS,
         const f32x4_t o = O[i] * p.scale;
         *reinterpret_cast<u32x2_t*>(&sm.Q[16 * i + l16][16 * wave + 4 * lg]) =
             u32x2_t{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+      }
+      if (odd) {
+#pragma unroll 1
+        for (int r = 0; r < 4; ++r) {
+          const int c = 16 * wave + 4 * lg + r, from = sm.from[c];
+#pragma unroll 1
+          for (int i = l16; i < C; i += 16)
+            if (i >= from) sm.Q[i][c] = 0x7fc0u;
+        }
+        if (sm.from[16 * wave + l16] < C) d_all = __builtin_nanf("");
       }
       // the output's registers are free from here: the compiler does not mix the phases, and
       // two workgroups of eight waves stay on a compute unit (128 registers)

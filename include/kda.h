@@ -438,8 +438,8 @@ int kda_la_step_check(const void* q, int64_t q_row, const void* k, int64_t k_row
  *                  kda_la_workspace_bytes(B * T, num_seqs, H, D, segment) bytes
  *                  (KDA_ERR_BAD_WORKSPACE), scratch on return: calls that may overlap in
  *                  time need one each.  With segment 0 it may be NULL: no segments then.
- * A non-finite q, k or v of one token may reach the outputs of earlier tokens of its
- * sequence and head inside the same 64-token chunk (zero weights times it).
+ * Infinities and NaN of one token reach outputs of that token and later ones of its sequence
+ * only: those of q its own, of k all of its heads', of v its value's (as infinities or NaN).
  */
 int kda_la_fwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
                int64_t v_row, const float* g, const float* decay, float scale, void* out,

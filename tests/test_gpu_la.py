@@ -169,6 +169,36 @@ def test_nan_gate_reaches_its_head_only():
     assert torch.isnan(final[0, 1]).all() and not torch.isnan(final[1]).any()
 
 
+@pytest.mark.parametrize("lens,H,Hk,D,segment", [([150, 90], 4, 2, 32, 0), ([150, 90], 4, 2, 64, 0),
+                                                 ([150, 90], 4, 2, 128, 0), ([700], 6, 3, 128, 0),
+                                                 ([700], 6, 3, 128, 128)])
+def test_infinities_and_nan_reach_later_tokens_only(lens, H, Hk, D, segment):
+    """Those of v: later outputs and the state in their value; of q: its token; of k: later
+    tokens of its heads.  Everything else is bit for bit what it is without them."""
+    print("kda_la_fwd odd", lens, H, Hk, D, segment, flush=True)
+    x = _inputs(21, lens, H, Hk, D)
+    want, want_final = _run(x, 0.5, segment=segment)
+    got = torch.zeros(want.shape, dtype=torch.bool, device=DEV)  # where one is seen
+    state = torch.zeros(want_final.shape, dtype=torch.bool, device=DEV)
+    y = dict(x, **{n: x[n].clone() for n in "qkv"})
+    for t, d, value in [(3, 5, float("inf")), (70, 0, float("nan")), (75, D - 1, -float("inf")),
+                        (lens[0] - 1, 17, float("nan"))]:
+        y["v"][0, t, 1, d] = value
+        got[0, t:lens[0], 1, d] = True
+        state[0, 1, d] = True
+    y["q"][0, 66, 0, 2] = float("nan")
+    got[0, 66, :H // Hk] = True
+    y["k"][0, 90, Hk - 1, 4] = float("nan")
+    got[0, 90:lens[0], H - H // Hk:] = True
+    state[0, H - H // Hk:, :, 4] = True
+    out, final = _run(y, 0.5, segment=segment)
+    assert torch.equal(out.isfinite(), ~got) and torch.equal(out[~got], want[~got])
+    # k reaches its column of the state, and what the products take along with it
+    rest = ~state
+    rest[0, H - H // Hk:] = False
+    assert not final[state].isfinite().any() and torch.equal(final[rest], want_final[rest])
+
+
 def test_capture_and_streams():
     """Captured and replayed beside eager work, on another stream, workspaces of their own."""
     x = _inputs(15, [700], 4, 4, 64)
