@@ -11,13 +11,17 @@ _ATTN_FWD = ([_VP, _I64] * 3 + [_F32] + [_VP] * 5 + [_I64] * 9 + [_VP, _I64])
 
 
 def declare(lib) -> None:
-    """Sets the argument types of the serving operators' C functions."""
+    """Sets the argument types of the serving operators' C functions, and their addresses
+    (``name_at``) for the compiled calls."""
     for name, args in (("kda_step", _STEP), ("kda_la_step", _LA_STEP),
                        ("kda_la_fwd", _LA_FWD), ("kda_attn_fwd", _ATTN_FWD)):
         getattr(lib, name).argtypes = args + [_VP]
         getattr(lib, name).restype = _I32
+        setattr(lib, name + "_at", ctypes.cast(getattr(lib, name), _VP).value)
         getattr(lib, name + "_check").argtypes = args
         getattr(lib, name + "_check").restype = _I32
+    for name in ("kda_la_workspace_bytes", "kda_attn_workspace_bytes"):
+        setattr(lib, name + "_at", ctypes.cast(getattr(lib, name), _VP).value)
     lib.kda_la_workspace_bytes.argtypes = [_I64] * 5
     lib.kda_la_workspace_bytes.restype = _I64
     lib.kda_attn_workspace_bytes.argtypes = [_I64] * 9

@@ -7,7 +7,7 @@ import subprocess
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_PATH = os.path.join(PKG_DIR, "libkda.so")
-ARGS_PATH = os.path.join(PKG_DIR, "_tensor_args.so")
+CALLS_PATH = os.path.join(PKG_DIR, "_serving_calls.so")
 SOURCES = ["kda_kernel.hip", "kda_api.cpp", "step_kernel.hip", "la_kernel.hip",
            "attn_kernel.hip", "ops_api.cpp"]
 
@@ -18,35 +18,40 @@ HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
              "-Wall", "-Wno-unused-function"]
 
 
+def rocm() -> str:
+    return os.environ.get("ROCM_PATH", "/opt/rocm")
+
+
 def hipcc() -> str:
-    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
-    return os.path.join(rocm, "bin", "hipcc")
+    return os.path.join(rocm(), "bin", "hipcc")
 
 
-def build_tensor_args(verbose: bool = False) -> str:
-    """Compile the bindings' argument checks (host code over torch's headers)."""
+def build_serving_calls(verbose: bool = False) -> str:
+    """Compile the serving bindings' calls (host code over torch's headers)."""
     import sysconfig
 
     import torch
     root = os.path.dirname(torch.__file__)
     inc, lib = os.path.join(root, "include"), os.path.join(root, "lib")
-    tmp = ARGS_PATH + ".tmp%d" % os.getpid()
+    tmp = CALLS_PATH + ".tmp%d" % os.getpid()
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
-           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
            "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
-           "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "tensor_args.cpp"),
-           "-o", tmp, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+           "-isystem", os.path.join(rocm(), "include"),
+           "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "serving_calls.cpp"),
+           "-o", tmp, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_hip"]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
-    os.replace(tmp, ARGS_PATH)
-    return ARGS_PATH
+    os.replace(tmp, CALLS_PATH)
+    return CALLS_PATH
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source and link ``libkda.so``, and the bindings' argument checks
+    """Compile every HIP source and link ``libkda.so``, and the serving bindings' calls
     (always recompiles)."""
-    build_tensor_args(verbose)
+    build_serving_calls(verbose)
     objs = []
     for src in SOURCES:
         obj = os.path.join(CSRC, os.path.splitext(src)[0] + ".o")

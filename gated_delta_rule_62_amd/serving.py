@@ -2,8 +2,9 @@
 attention with one decay per head, and causal softmax attention with grouped heads.
 
 Like the package's other bindings they check dtypes, shapes, devices and strides, pass raw
-pointers, sizes and torch's current stream to the C ABI declared in ``include/kda.h``, and
-turn status codes into exceptions; every computation runs in the library's kernels.
+pointers, sizes and torch's current stream to the C ABI declared in ``include/kda.h`` (both
+in a compiled module, ``csrc/serving_calls.cpp``), and turn status codes into exceptions;
+every computation runs in the library's kernels.
 """
 from __future__ import annotations
 
@@ -12,54 +13,10 @@ import torch
 from . import KdaError, load_library
 
 try:
-    from ._tensor_args import optional as _optional, rows as _rows, tensor as _tensor
+    from . import _serving_calls as _calls
 except ImportError as e:
-    raise ImportError("the bindings' argument checks (_tensor_args.so) are not built; run "
+    raise ImportError("the serving operators' calls (_serving_calls.so) are not built; run "
                       "gated_delta_rule_62_amd.build() (or __graft_entry__.build())") from e
-
-# dtype codes of _tensor_args (the first two are the C ABI's state dtypes)
-bf16, fp32, int64 = 0, 1, 2
-
-
-def _device(q) -> int:
-    if not q.is_cuda:
-        raise ValueError("every tensor must live on the same GPU")
-    return q.get_device()
-
-
-def _stream_ptr(stream, dev):
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _launch(fn, dev, args) -> None:
-    """Calls a C operator with dev current (the library launches on the current device)."""
-    if torch._C._cuda_getDevice() == dev:
-        st = fn(*args)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args)
-    if st != 0:
-        raise KdaError(st)
-
-
-def _dtype_code(t):
-    if t.dtype is torch.bfloat16:
-        return bf16
-    if t.dtype is torch.float32:
-        return fp32
-    raise TypeError("state tensors must be bfloat16 or float32, got %s" % t.dtype)
-
-
-def _pool(state, slot_in, slot_out, N, H, D, dev):
-    if state.dim() != 4:
-        raise ValueError("state must be [slots,H,D,D]")
-    slots = state.shape[0]
-    code = _dtype_code(state)
-    return (_tensor("state", state, code, (slots, H, D, D), dev), code, slots,
-            _optional("slot_in", slot_in, int64, (N,), dev),
-            _optional("slot_out", slot_out, int64, (N,), dev))
 
 
 def kda_step(q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound, state, slot_in=None,
@@ -73,17 +30,10 @@ def kda_step(q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound, state, s
     and writes slot ``slot_out[n]`` (None: slot_in); an index outside the pool reads zeros
     or writes nothing.  A slot that one request writes must not be named by another.
     """
-    if q.dim() != 3:
-        raise ValueError("q must be [N,H,D]")
-    N, H, D = shape = tuple(q.shape)
-    dev = _device(q)
-    args = (_tensor("q", q, bf16, shape, dev), _tensor("k", k, bf16, shape, dev),
-            _tensor("v", v, bf16, shape, dev), _tensor("g", g, bf16, shape, dev),
-            _tensor("beta", beta, bf16, (N, H), dev), float(scale),
-            _tensor("out", out, bf16, shape, dev), _tensor("A_log", A_log, fp32, (H,), dev),
-            _tensor("dt_bias", dt_bias, fp32, (H, D), dev), float(lower_bound),
-            *_pool(state, slot_in, slot_out, N, H, D, dev), N, H, D, _stream_ptr(stream, dev))
-    _launch(load_library().kda_step, dev, args)
+    st = _calls.step(load_library().kda_step_at, q, k, v, g, beta, scale, out, A_log, dt_bias,
+                     lower_bound, state, slot_in, slot_out, stream)
+    if st != 0:
+        raise KdaError(st)
 
 
 def kda_la_step(q, k, v, g, scale, out, state, decay=None, slot_in=None, slot_out=None,
@@ -95,45 +45,21 @@ def kda_la_step(q, k, v, g, scale, out, state, decay=None, slot_in=None, slot_ou
     views with a row stride); g: fp32 ``[N,H]`` log decays or None; decay: fp32 ``[H]`` log
     decays or None; state and slots as for ``kda_step``.
     """
-    if q.dim() != 3 or v.dim() != 3:
-        raise ValueError("q and v must be [N,heads,D]")
-    N, H, D = v.shape
-    Hk = q.shape[1]
-    dev = _device(q)
-    args = (*_rows("q", q, bf16, (N, Hk, D), dev), *_rows("k", k, bf16, (N, Hk, D), dev),
-            *_rows("v", v, bf16, (N, H, D), dev), _optional("g", g, fp32, (N, H), dev),
-            _optional("decay", decay, fp32, (H,), dev), float(scale),
-            _tensor("out", out, bf16, (N, H, D), dev),
-            *_pool(state, slot_in, slot_out, N, H, D, dev), N, H, Hk, D,
-            _stream_ptr(stream, dev))
-    _launch(load_library().kda_la_step, dev, args)
+    st = _calls.la_step(load_library().kda_la_step_at, q, k, v, g, scale, out, state, decay,
+                        slot_in, slot_out, stream)
+    if st != 0:
+        raise KdaError(st)
 
 
-def _state(name, t, N, H, D, dev):
-    """Address and dtype code of a prompt's initial or final states, or nothing."""
-    if t is None:
-        return None, 0
-    code = _dtype_code(t)
-    return _tensor(name, t, code, (N, H, D, D), dev), code
-
-
-def _workspace(workspace, need, dev, stream):
-    """Address, size and owner of the caller's workspace, or of one from torch's allocator
-    for this call (taken for the stream it runs on, so that nothing else uses it meanwhile)."""
-    if workspace is None:
-        if need == 0:
-            return None, 0, None
-        if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device="cuda:%d" % dev)
-        else:
-            s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream, dev)
-            with torch.cuda.stream(s):
-                workspace = torch.empty(need, dtype=torch.uint8, device="cuda:%d" % dev)
-    elif workspace.dtype != torch.uint8 or workspace.dim() != 1:
-        raise ValueError("workspace must be a 1-d uint8 tensor")
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous and live on the same GPU")
-    return workspace.data_ptr(), workspace.numel(), workspace
+def _workspace(need, q, stream):
+    """A workspace from torch's allocator for one call, taken for the stream it runs on, so
+    that nothing else uses it meanwhile."""
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=q.device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(stream, q.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device=q.device)
 
 
 def kda_la_workspace_bytes(T_total: int, num_seqs: int, H: int, D: int, segment: int = 0) -> int:
@@ -157,30 +83,14 @@ def kda_la_fwd(q, k, v, g, scale, out, decay=None, initial_state=None, final_sta
     ``kda_la_workspace_bytes(B*T, N, H, D, segment)`` bytes for this call alone; None takes
     one from torch's allocator where the call needs it.
     """
-    if q.dim() != 4 or v.dim() != 4:
-        raise ValueError("q and v must be [B,T,heads,D]")
-    B, T, H, D = v.shape
-    Hk = q.shape[2]
-    dev = _device(q)
-    if torch._C._cuda_getDevice() != dev:  # schedules go by the current device
-        with torch.cuda.device(dev):
-            return kda_la_fwd(q, k, v, g, scale, out, decay, initial_state, final_state,
-                              cu_seqlens, segment, workspace, stream)
-    cu, N = None, B
-    if cu_seqlens is not None:
-        N = cu_seqlens.numel() - 1
-        cu = _tensor("cu_seqlens", cu_seqlens, int64, (N + 1,), dev)
     lib = load_library()
-    need = lib.kda_la_workspace_bytes(B * T, N, H, D, int(segment))
-    ws, ws_bytes, _keep = _workspace(workspace, max(need, 0), dev, stream)
-    args = (*_rows("q", q, bf16, (B, T, Hk, D), dev), *_rows("k", k, bf16, (B, T, Hk, D), dev),
-            *_rows("v", v, bf16, (B, T, H, D), dev), _optional("g", g, fp32, (B, T, H), dev),
-            _optional("decay", decay, fp32, (H,), dev), float(scale),
-            _tensor("out", out, bf16, (B, T, H, D), dev),
-            *_state("initial_state", initial_state, N, H, D, dev),
-            *_state("final_state", final_state, N, H, D, dev), cu, N, B, T, H, Hk, D,
-            int(segment), ws, ws_bytes, _stream_ptr(stream, dev))
-    _launch(lib.kda_la_fwd, dev, args)
+    args = (lib.kda_la_fwd_at, lib.kda_la_workspace_bytes_at, q, k, v, g, scale, out, decay,
+            initial_state, final_state, cu_seqlens, segment)
+    st = _calls.la_fwd(*args, workspace, stream)
+    if st > 0:  # the bytes it wants
+        st = _calls.la_fwd(*args, _workspace(st, q, stream), stream)
+    if st != 0:
+        raise KdaError(st)
 
 
 def kda_attn_workspace_bytes(num_seqs: int, Bq: int, Tq: int, Bk: int, Tk: int, Hq: int, Hk: int,
@@ -208,25 +118,11 @@ def kda_attn_fwd(q, k, v, scale, out, lse=None, cu_seqlens_q=None, cu_seqlens_k=
     ``kda_attn_workspace_bytes(...)`` bytes for this call alone; None takes one from torch's
     allocator where the call needs it.
     """
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError("q and k must be [B,T,heads,D]")
-    Bq, Tq, Hq, D = q.shape
-    Bk, Tk, Hk, _ = k.shape
-    dev = _device(q)
-    if torch._C._cuda_getDevice() != dev:  # schedules go by the current device
-        with torch.cuda.device(dev):
-            return kda_attn_fwd(q, k, v, scale, out, lse, cu_seqlens_q, cu_seqlens_k, k_lens,
-                                splits, workspace, stream)
-    N = cu_seqlens_q.numel() - 1 if cu_seqlens_q is not None else Bq
     lib = load_library()
-    need = lib.kda_attn_workspace_bytes(N, Bq, Tq, Bk, Tk, Hq, Hk, D, int(splits))
-    ws, ws_bytes, _keep = _workspace(workspace, max(need, 0), dev, stream)
-    args = (*_rows("q", q, bf16, (Bq, Tq, Hq, D), dev), *_rows("k", k, bf16, (Bk, Tk, Hk, D), dev),
-            *_rows("v", v, bf16, (Bk, Tk, Hk, D), dev), float(scale),
-            _tensor("out", out, bf16, (Bq, Tq, Hq, D), dev),
-            _optional("lse", lse, fp32, (Bq, Tq, Hq), dev),
-            _optional("cu_seqlens_q", cu_seqlens_q, int64, (N + 1,), dev),
-            _optional("cu_seqlens_k", cu_seqlens_k, int64, (N + 1,), dev),
-            _optional("k_lens", k_lens, int64, (N,), dev), N, Bq, Tq, Bk, Tk, Hq, Hk, D,
-            int(splits), ws, ws_bytes, _stream_ptr(stream, dev))
-    _launch(lib.kda_attn_fwd, dev, args)
+    args = (lib.kda_attn_fwd_at, lib.kda_attn_workspace_bytes_at, q, k, v, scale, out, lse,
+            cu_seqlens_q, cu_seqlens_k, k_lens, splits)
+    st = _calls.attn_fwd(*args, workspace, stream)
+    if st > 0:  # the bytes it wants
+        st = _calls.attn_fwd(*args, _workspace(st, q, stream), stream)
+    if st != 0:
+        raise KdaError(st)
