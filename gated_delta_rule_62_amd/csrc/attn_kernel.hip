@@ -85,11 +85,11 @@ __device__ __forceinline__ bool set_tile(const AttnParams& p, int n, int64_t row
 }
 
 // Tile number `slot` of a key/value head, in any order; false if it has none.
-__device__ __forceinline__ bool find_tile(const AttnParams& p, int64_t slot, int tile_rows,
+__device__ __forceinline__ bool find_tile(const AttnParams& p, unsigned slot, int tile_rows,
                                           Tile& t) {
   if (p.cu_q == nullptr) {
-    const int64_t per = (p.Tq * p.G + tile_rows - 1) / tile_rows;
-    return slot / per < p.N && set_tile(p, (int)(slot / per), slot % per * tile_rows, t);
+    const unsigned per = (unsigned)((p.Tq * p.G + tile_rows - 1) / tile_rows), n = slot / per;
+    return n < (unsigned)p.N && set_tile(p, (int)n, (int64_t)(slot % per) * tile_rows, t);
   }
   // the last sequence whose first slot is not behind this one (first slots grow strictly)
   int lo = 0, hi = p.N - 1;
@@ -108,14 +108,14 @@ __device__ __forceinline__ bool find_tile(const AttnParams& p, int64_t slot, int
 // long one that starts last would set the time: batch rows by their tile, packed sequences
 // (of up to 16: the ranking costs a short workgroup more than it gains with many) longest
 // keys first, each from its last tile.  Whole waves call it.
-__device__ __forceinline__ bool find_tile_longest_first(const AttnParams& p, int64_t slot,
-                                                        int64_t slots, int tile_rows, Tile& t) {
+__device__ __forceinline__ bool find_tile_longest_first(const AttnParams& p, unsigned slot,
+                                                        unsigned slots, int tile_rows, Tile& t) {
   int n;
   int64_t row0;
   if (p.cu_q == nullptr) {
     const int64_t per = (p.Tq * p.G + tile_rows - 1) / tile_rows;
-    n = (int)(slot % p.N);
-    row0 = (per - 1 - slot / p.N) * tile_rows;
+    n = (int)(slot % (unsigned)p.N);
+    row0 = (per - 1 - slot / (unsigned)p.N) * tile_rows;
   } else if (p.N > 16) {
     return find_tile(p, slots - 1 - slot, tile_rows, t);
   } else {

@@ -104,8 +104,7 @@ __device__ __forceinline__ void seq_bounds(const LaParams& p, int n, int64_t& a,
 // so a group's heads sit 8 blocks apart, on one XCD and its L2.  False: no such unit.
 __device__ __forceinline__ bool find_unit(const LaParams& p, unsigned block, Unit& u) {
   const unsigned run = 8u * (unsigned)p.group;
-  const int64_t c = (int64_t)(block / run) * 8 + block % 8;
-  const int Hk = p.H / p.group;
+  const unsigned c = block / run * 8u + block % 8u, Hk = (unsigned)(p.H / p.group);
   const int64_t item = c / Hk;
   u.hk = (int)(c % Hk);
   u.h = u.hk * p.group + (int)((block / 8) % (unsigned)p.group);
@@ -318,26 +317,32 @@ __global__ __launch_bounds__(LaCfg<D>::THREADS,
     float d_all = d0 * d1 * d2 * d3;
     f32x4_t O[RT];
     if constexpr (!STATE_ONLY) {
-      // ---- scores: ten 16x16 tiles (i, j <= i) over the waves, as K Q^T: lane holds token
-      // i = l16 and four j
-      for (int m = wave; m < RT * (RT + 1) / 2; m += F::NW) {
-        const int i = m < 1 ? 0 : m < 3 ? 1 : m < 6 ? 2 : 3, j = m - i * (i + 1) / 2;
+      // ---- scores: ten 16x16 tiles (i, j <= i) over the waves, the four diagonal ones first,
+      // as K Q^T: lane holds token i = l16 and four j
+#pragma unroll F::NW <= 4 ? 5 : 1
+      for (int x = 0; x < (10 + F::NW - 1) / F::NW; ++x) {
+        const int m = wave + x * F::NW;
+        if ((x + 1) * F::NW > 10 && m >= 10) break;
+        const bool diagonal = F::NW <= 4 ? x < 4 / F::NW : m < 4;  // known for few waves
+        const int i = diagonal ? m : m < 5 ? 1 : m < 7 ? 2 : 3,
+                  j = diagonal ? m : m - 4 - i * (i - 1) / 2;
         f32x4_t a = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int ks = 0; ks < F::KS; ++ks)
           a = mfma(*reinterpret_cast<const u32x4_t*>(&sm.K[16 * j + l16][32 * ks + 8 * lg]),
                    *reinterpret_cast<const u32x4_t*>(&sm.Q[16 * i + l16][32 * ks + 8 * lg]), a);
         const int ti = 16 * i + l16, tj = 16 * j + 4 * lg;
-        if (i == j) {
+        if (diagonal) {
           const float pi = sm.p[ti];
           const f32x4_t pj = *reinterpret_cast<const f32x4_t*>(&sm.p[tj]);
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            a[r] = tj + r <= ti ? a[r] * __builtin_amdgcn_exp2f(pi - pj[r]) : 0.f;
+          for (int r = 0; r < 4; ++r) {
+            const float f = __builtin_amdgcn_exp2f(pi - pj[r]);
+            a[r] = tj + r <= ti ? a[r] * f : 0.f;
+          }
         } else {
-          float f = sm.ep[ti];
-          if (i - j > 1) f *= sm.tile[j + 1];
-          if (i - j > 2) f *= sm.tile[j + 2];
+          const float t1 = sm.tile[(j + 1) % RT], t2 = sm.tile[(j + 2) % RT];
+          const float f = sm.ep[ti] * (i - j > 1 ? t1 : 1.f) * (i - j > 2 ? t2 : 1.f);
           const f32x4_t ej = *reinterpret_cast<const f32x4_t*>(&sm.es[tj]);
 #pragma unroll
           for (int r = 0; r < 4; ++r) a[r] *= f * ej[r];
