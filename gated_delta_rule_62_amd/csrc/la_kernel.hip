@@ -238,9 +238,12 @@ __global__ __launch_bounds__(LaCfg<D>::THREADS,
                        rs, (uint32_t)(lrow + i * F::RPP) * row_bytes + lcol * 2u, 0, 0));
   };
   const float dec = p.decay ? p.decay[u.h] : 0.f;
-  auto load = [&](int64_t t) {
+  auto load_q = [&](int64_t t) {
+    if constexpr (!STATE_ONLY)
+      fetch(rq, p.q, p.q_row, u.hk * D, t, (int)(u.t1 - t < C ? u.t1 - t : C));
+  };
+  auto load_kv = [&](int64_t t) {
     const int valid = (int)(u.t1 - t < C ? u.t1 - t : C);
-    if constexpr (!STATE_ONLY) fetch(rq, p.q, p.q_row, u.hk * D, t, valid);
     fetch(rk, p.k, p.k_row, u.hk * D, t, valid);
     fetch(rv, p.v, p.v_row, u.h * D, t, valid);
     if (wave == 0 && p.g != nullptr) rg = lane < valid ? p.g[(t + lane) * H + u.h] : 0.f;
@@ -251,7 +254,10 @@ __global__ __launch_bounds__(LaCfg<D>::THREADS,
   auto inside = [&](int64_t t) { return STATE_ONLY ? t >= u.t0 : t < u.t1; };
   const int64_t first =
       STATE_ONLY && u.t0 < u.t1 ? u.t0 + (u.t1 - u.t0 - 1) / C * C : u.t0;
-  if (u.t0 < u.t1) load(first);
+  if (u.t0 < u.t1) {
+    load_q(first);
+    load_kv(first);
+  }
   // the state's loads end here: their first use inside the loop would make every chunk wait
   // for all loads in flight
 #pragma unroll
@@ -311,7 +317,7 @@ __global__ __launch_bounds__(LaCfg<D>::THREADS,
       sm.w[lane] = w;
     }
     lds_barrier();
-    if (inside(t + STEP)) load(t + STEP);
+    if (inside(t + STEP)) load_kv(t + STEP);
 
     const float d0 = sm.tile[0], d1 = sm.tile[1], d2 = sm.tile[2], d3 = sm.tile[3];
     float d_all = d0 * d1 * d2 * d3;
@@ -382,6 +388,9 @@ __global__ __launch_bounds__(LaCfg<D>::THREADS,
         O[i] *= f;
       }
       lds_barrier();  // the scores are written
+      // the loads of a chunk keep the address unit busy for 800 cycles, which its waves would
+      // wait for if they were all asked for at once (8% of a call with a workgroup per unit)
+      if (inside(t + STEP)) load_q(t + STEP);
     }
 
     // ---- V^T, from transposed reads: rows are values, slots tokens 32 b + 4g + i and
