@@ -122,7 +122,7 @@ float number(PyObject* o) {
   return static_cast<float>(x);
 }
 int64_t integer(PyObject* o) {
-  PyObject* i = PyNumber_Long(o);
+  PyObject* i = PyNumber_Index(o);
   const long long x = i ? PyLong_AsLongLong(i) : -1;
   Py_XDECREF(i);
   if (x == -1 && PyErr_Occurred()) throw Raise{nullptr, ""};
@@ -141,7 +141,7 @@ void* stream_of(PyObject* o, int dev) {
   PyObject* raw = PyObject_GetAttrString(o, "cuda_stream");
   if (raw == nullptr) {
     PyErr_Clear();
-    raw = PyNumber_Long(o);
+    raw = PyNumber_Index(o);
   }
   void* s = raw ? PyLong_AsVoidPtr(raw) : nullptr;
   Py_XDECREF(raw);

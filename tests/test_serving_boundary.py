@@ -92,6 +92,15 @@ def test_bindings_refuse_cpu_tensors():
         kda.kda_step(x, x, x, x, b, 1.0, x, torch.zeros(4), torch.zeros(4, 32), -1.0, pool)
     with pytest.raises(ValueError, match="GPU"):
         kda.kda_la_step(x, x, x, None, 1.0, x, pool)
+    y, cu = torch.zeros((1, 2, 4, 64), dtype=torch.bfloat16), torch.tensor([0, 2])
+    with pytest.raises(ValueError, match="GPU"):
+        kda.kda_la_fwd(y, y, y, None, 1.0, y, cu_seqlens=cu)
+    with pytest.raises(ValueError, match="GPU"):
+        kda.kda_attn_fwd(y, y, y, 1.0, y)
+    with pytest.raises(TypeError, match="q must be a tensor"):
+        kda.kda_attn_fwd(None, y, y, 1.0, y)
+    with pytest.raises(ValueError, match="q and v"):
+        kda.kda_la_fwd(x, x, x, None, 1.0, x)
 
 
 LA = ("q q_row k k_row v v_row g decay scale out s_in in_dtype s_out out_dtype cu N B T H Hk D "
