@@ -26,6 +26,10 @@
 //
 // Few rows leave the device idle; then `splits` workgroups share a tile's keys, write
 // unnormalised fp32 outputs with their maximum and sum, and a second kernel joins them.
+//
+// Measured (D 128): 8192 tokens of 32/8 heads 520-535 us, 1.05 PFLOP/s, where the matrix
+// products alone take 400 at the clock they bring the card down to; one token of each of 32
+// requests over 1024-8192 keys, 32/8 heads, 121 us, 5.0 TB/s, as its loads alone.
 #include "api_util.h"
 #include "gfx950.h"
 #include "ops_params.h"
