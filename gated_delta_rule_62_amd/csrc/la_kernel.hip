@@ -34,11 +34,15 @@
 // call.
 //
 // Segments.  One workgroup per (sequence, head) leaves most of the device idle for a few
-// long sequences.  Then three launches split the tokens: a state-only pass sums every
+// long sequences.  Then launches split the tokens: a state-only pass sums every
 // segment's own contribution from a zero state (k and v only), an elementwise scan turns
 // these into the state before each segment, and the main pass runs all segments at once.
 // The state-only pass goes backwards from the segment's end and stops once the decay of
-// what it has passed is zero in fp32: all earlier weights are.
+// what it has passed is zero in fp32: all earlier weights are.  Infinities and NaN of the tokens
+// it never reads belong in every later state all the same (a zero weight times one is NaN).
+// The main pass meets them: a segment whose true end state is not all finite leaves it in its
+// place of the workspace, and a fourth launch, a look at one flag per segment otherwise,
+// carries it to the outputs and the final state behind.
 //
 // Measured (D 128, bf16 states): 2 x 1024 tokens of 96 heads 58 us, where loads and stores alone
 // take 50; 32,768 tokens of 32 heads 350 us, 3.1 TB/s of q, k, v and out and 4.3 of all that
@@ -523,8 +527,32 @@ __global__ __launch_bounds__(LaCfg<D>::THREADS,
     for (int kt = 0; kt < F::KT; ++kt)
       *reinterpret_cast<f32x4_t*>(wseg + kt * F::THREADS * 4) = S[kt];
     if (tid == 0) p.ws_decay[u.slot * H + u.h] = after;
-  } else if (p.s_out != nullptr && u.s == u.nseg - 1) {
-    state_store(S, p.s_out, head, p.s_out_fp32);
+  } else {
+    const bool inner = u.s < u.nseg - 1;
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));  // addresses are formed anew, not kept through the loop
+    if (inner) {
+      // whether the state behind this segment is all finite, for la_carry_kernel; the scan is
+      // done with the segment's place and decay
+      float zero = 0.f;
+#pragma unroll
+      for (int kt = 0; kt < F::KT; ++kt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) zero = fmaf(S[kt][i], 0.f, zero);
+      const bool odd = __any(zero != zero);
+      if ((t & 63) == 0) sm.from[t >> 6] = odd;  // behind the barrier above nobody reads sm.from
+      lds_barrier();
+      int any = 0;
+#pragma unroll
+      for (int w = 0; w < F::NW; ++w) any |= sm.from[w];
+      if (t == 0) p.ws_decay[u.slot * H + u.h] = any ? 1.f : 0.f;
+      if (!any) return;
+    } else if (p.s_out == nullptr) {
+      return;
+    }
+    const int64_t at = inner ? u.slot * H + u.h : (int64_t)u.n * H + u.h;
+    const int row = 16 * (t >> 6) + (t & 15), key = 8 * (t >> 4 & 3);
+    state_store(S, inner ? p.ws : p.s_out, at * (D * D) + row * D + key, inner ? 1 : p.s_out_fp32);
   }
 }
 
@@ -566,6 +594,57 @@ __global__ __launch_bounds__(256) void la_scan_kernel(LaParams p) {
   *reinterpret_cast<f32x4_t*>(w) = S;
 }
 
+// Carries what is not finite in the state behind a segment to the outputs of the segments after
+// it, a value's from each of its keys, and to the final state.  One workgroup per (sequence,
+// head), its lanes as in la_kernel; without a flag it leaves.
+template <int D>
+__global__ __launch_bounds__(LaCfg<D>::THREADS) void la_carry_kernel(LaParams p) {
+  using F = LaCfg<D>;
+  const int64_t H = p.H;
+  const int n = (int)(blockIdx.x / (unsigned)p.H), h = (int)(blockIdx.x % (unsigned)p.H);
+  int64_t a, b;
+  seq_bounds(p, n, a, b);
+  const int nseg = (int)((b - a + p.seg - 1) / p.seg);
+  const int64_t slot = a / p.seg + n;
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lg = lane >> 4, wave = tid >> 6;
+  const int at = (16 * wave + l16) * D + 8 * lg;  // the lane's first element of a state
+  const float* flags = p.ws_decay + slot * H + h;
+  uint32_t bad = 0;    // bit 4 kt + i: element i of the lane's tile kt
+  int from = nseg;     // the first segment that its value's outputs are spoilt in
+  for (int s0 = 0; s0 < nseg - 1; s0 += 64) {
+    const bool flag = s0 + lane < nseg - 1 && flags[(int64_t)(s0 + lane) * H] != 0.f;
+    for (uint64_t left = __ballot(flag); left != 0; left &= left - 1) {
+      const int s = s0 + __builtin_ctzll(left);
+      const float* w = p.ws + ((slot + s) * H + h) * (int64_t)(D * D) + at;
+#pragma unroll
+      for (int kt = 0; kt < F::KT; ++kt) {
+        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(w + key0(kt, 0));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!(fabsf(x[i]) < __builtin_inff())) bad |= 1u << (4 * kt + i);
+      }
+      const uint64_t value = __ballot(bad != 0) >> l16 & 0x0001000100010001ull;
+      if (value != 0 && from == nseg) from = s + 1;
+    }
+  }
+  u16* out = p.out + h * D + 16 * wave + l16;
+  if (from < nseg)
+    for (int64_t t = a + (int64_t)from * p.seg + lg; t < b; t += 4) out[t * H * D] = 0x7fc0u;
+  if (bad != 0 && p.s_out != nullptr) {
+    const int64_t head = ((int64_t)n * H + h) * (D * D) + at;
+#pragma unroll
+    for (int kt = 0; kt < F::KT; ++kt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (bad >> (4 * kt + i) & 1u) {
+          if (p.s_out_fp32)
+            static_cast<float*>(p.s_out)[head + key0(kt, 0) + i] = __builtin_nanf("");
+          else
+            static_cast<u16*>(p.s_out)[head + key0(kt, 0) + i] = 0x7fc0u;
+        }
+  }
+}
+
 template <int D, int PARTS, bool FINE>
 hipError_t go(const LaParams& p, hipStream_t stream) {
   using F = LaCfg<D>;
@@ -578,6 +657,8 @@ hipError_t go(const LaParams& p, hipStream_t stream) {
     la_scan_kernel<D><<<dim3((unsigned)((int64_t)p.N * p.H * BLOCKS)), 256, 0, stream>>>(p);
   }
   la_kernel<D, false, PARTS, FINE><<<dim3((unsigned)blocks), F::THREADS, 0, stream>>>(p);
+  if (p.seg)
+    la_carry_kernel<D><<<dim3((unsigned)((int64_t)p.N * p.H)), F::THREADS, 0, stream>>>(p);
   return hipGetLastError();
 }
 

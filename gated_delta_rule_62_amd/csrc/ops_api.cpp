@@ -108,7 +108,8 @@ int la_step_check(const void* q, int64_t q_row, const void* k, int64_t k_row, co
 // estimated time.  The host knows the sequences' mean length only.  The constants
 // (microseconds, bytes per microsecond) are fitted to 130 measured calls, 1-4 sequences of
 // 512-32,768 tokens, 1-128 heads, D 64 and 128, with and without segments: the choice costs
-// 2% over the best of each on average.
+// 2% over the best of each on average.  (23.4: 21 as fitted, and 2.4 for the launch that carries
+// infinities and NaN on, 2.2 to 2.6 in the same calls.)
 int64_t la_auto_segment(int64_t T_total, int64_t N, int64_t H, int64_t D) {
   const double units = double(N) * H, mean = double(T_total) / N, chunk = kda::kLaChunk;
   const double room = 2.0 * kda::device_cus();  // workgroups at once
@@ -122,7 +123,7 @@ int64_t la_auto_segment(int64_t T_total, int64_t N, int64_t H, int64_t D) {
     // twice (the first pass ends where the decay is zero), each segment's state four times
     const double walk = (2.1 + 0.017 * D) * (seg / chunk) + 0.25 * mean / seg;
     const double move = (1.35 * bytes + 16.0 * D * D * H * (double(T_total) / seg)) / 4.6e6;
-    const double t = 21.0 + std::fmax(walk, move) + 0.13 * std::fmin(walk, move);
+    const double t = 23.4 + std::fmax(walk, move) + 0.13 * std::fmin(walk, move);
     if (t < best) {
       best = t;
       choice = seg;

@@ -431,7 +431,7 @@ int kda_la_step_check(const void* q, int64_t q_row, const void* k, int64_t k_row
  *   segment        0 (automatic), or tokens per segment: a multiple of 64, at most 2^20
  *                  (KDA_ERR_BAD_SCHEDULE).  A few long sequences do not fill the device
  *                  one workgroup per (sequence, head): their tokens are then split into
- *                  segments, whose own sums are formed first (three kernels instead of
+ *                  segments, whose own sums are formed first (four kernels instead of
  *                  one).  The state before a segment is then a sum in another order, so
  *                  results differ from the unsegmented ones by fp32 roundings of the state.
  *   workspace      caller-owned device memory, 16-byte aligned, of at least
@@ -439,7 +439,8 @@ int kda_la_step_check(const void* q, int64_t q_row, const void* k, int64_t k_row
  *                  (KDA_ERR_BAD_WORKSPACE), scratch on return: calls that may overlap in
  *                  time need one each.  With segment 0 it may be NULL: no segments then.
  * Infinities and NaN of one token reach outputs of that token and later ones of its sequence
- * only: those of q its own, of k all of its heads', of v its value's (as infinities or NaN).
+ * only: those of q its own, of k all of its heads', of v its value's (as infinities or NaN,
+ * whatever the decays since, in segments or without).
  */
 int kda_la_fwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
                int64_t v_row, const float* g, const float* decay, float scale, void* out,
