@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <limits>
 
 #include "../../include/kda.h"
 #include "api_util.h"
@@ -268,6 +269,9 @@ int64_t attn_ws_bytes(int64_t total, int64_t Hq, int64_t D, int64_t splits) {
   return splits > 1 ? splits * total * Hq * (D + 2) * 4 : 0;
 }
 
+// The factor of the scores in base 2.
+float attn_c(float scale) { return static_cast<float>(scale * 1.4426950408889634); }
+
 int attn_check(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
                int64_t v_row, float scale, const void* out, const float* lse, const int64_t* cu_q,
                const int64_t* cu_k, const int64_t* k_lens, int64_t N, int64_t Bq, int64_t Tq,
@@ -279,7 +283,7 @@ int attn_check(const void* q, int64_t q_row, const void* k, int64_t k_row, const
   if (st != KDA_OK) return st;
   if ((cu_q ? Bq != 1 : Bq != N) || (cu_k ? Bk != 1 : Bk != N) || (cu_k && k_lens))
     return KDA_ERR_BAD_VARLEN;
-  if (!std::isfinite(scale) || scale < 0.f) return KDA_ERR_BAD_SCALE;
+  if (!std::isfinite(attn_c(scale)) || scale < 0.f) return KDA_ERR_BAD_SCALE;
   const int64_t nq = Bq * Tq, nk = Bk * Tk;
   if ((nq > 0 && (!q || !out)) || (nq > 0 && nk > 0 && (!k || !v))) return KDA_ERR_NULL_ARG;
   if (q_row >= (1 << 24) || k_row >= (1 << 24) || v_row >= (1 << 24)) return KDA_ERR_BAD_SHAPE;
@@ -503,9 +507,9 @@ int kda_attn_fwd(const void* q, int64_t q_row, const void* k, int64_t k_row, con
   p.Hq = static_cast<int32_t>(Hq);
   p.Hk = static_cast<int32_t>(Hk);
   p.G = static_cast<int32_t>(Hq / Hk);
-  // never zero: minus infinity times it stands for a masked score (below 1e-30 every finite
-  // score times it is zero to the exponential anyway)
-  p.c = static_cast<float>(std::fmax(scale * 1.4426950408889634, 1e-30));
+  // never zero: minus infinity times it stands for a masked score.  The smallest float in
+  // place of zero moves a finite score by 2^-21 at most, six roundings of its exponential.
+  p.c = std::fmax(attn_c(scale), std::numeric_limits<float>::denorm_min());
   p.splits = static_cast<int32_t>(sp);
   p.ws_o = static_cast<float*>(workspace);
   p.ws_ml = sp > 1 ? p.ws_o + sp * p.Tq_total * Hq * D : nullptr;

@@ -64,7 +64,7 @@ extern "C" {
 #define KDA_ERR_BAD_LOWER_BOUND (-6) /* lower_bound not finite, not < 0, below -2.35e38 */
                                      /* (lb log2(e) not a finite float), or too strong   */
                                      /* for a forced chunk size (see kda_fwd)            */
-#define KDA_ERR_BAD_SCALE (-7)       /* scale not finite                                 */
+#define KDA_ERR_BAD_SCALE (-7)       /* scale not finite (kda_attn_fwd: its limits)      */
 #define KDA_ERR_BAD_SCHEDULE (-8)    /* unsupported forced chunk size or value tile      */
 #define KDA_ERR_HIP (-9)             /* the HIP runtime reported an error at launch      */
 #define KDA_ERR_BAD_WORKSPACE (-10)  /* kda_fwd_split: workspace smaller than required   */
@@ -477,7 +477,8 @@ int64_t kda_la_workspace_bytes(int64_t T_total, int64_t num_seqs, int64_t H, int
  *   k, v           bf16 [Bk, Tk, Hk, D], row strides k_row, v_row (below 2^24); query head h
  *                  uses key/value head h / (Hq / Hk).  Batch rows follow each other: token t
  *                  of batch row b is row b * T + t.
- *   scale          finite and not negative (KDA_ERR_BAD_SCALE).
+ *   scale          not negative; scale log2(e) a finite float (scale up to 2.35e38;
+ *                  KDA_ERR_BAD_SCALE).  Zero gives the mean of the visible v.
  *   out            bf16 [Bq, Tq, Hq, D], contiguous.
  *   lse            fp32 [Bq, Tq, Hq], or NULL.
  *   cu_seqlens_q   int64 [num_seqs + 1] device array (Bq == 1): sequence n's queries are
