@@ -190,9 +190,8 @@ __device__ __forceinline__ u32x4_t rows_words(const u16* base, int64_t row, int 
 
 // 16 bytes per lane from memory to LDS: lane l's land 16 l bytes behind `to` (uniform);
 // zeros where `off` is behind the descriptor's end.  It has no result the compiler could
-// track: kWaitLoads ends it, and a barrier shows it to the other waves.  (Nothing else in
-// these kernels uses m0.)  ONCE marks what no other workgroup reads, so that it does not
-// displace what others do.
+// track: wait_loads ends it, and a barrier shows it to the other waves.  ONCE marks what no
+// other workgroup reads, so that it does not displace what others do.
 template <bool ONCE>
 __device__ __forceinline__ void load_lds(u32x4_t rsrc, const u16* to, uint32_t off) {
   const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const u16*)to;
@@ -201,15 +200,27 @@ __device__ __forceinline__ void load_lds(u32x4_t rsrc, const u16* to, uint32_t o
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
                  :
                  : "s"(m0), "v"(off), "s"(rsrc)
-                 : "memory");
+                 : "memory", "m0");
   else
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
                  : "s"(m0), "v"(off), "s"(rsrc)
-                 : "memory");
+                 : "memory", "m0");
 }
-constexpr int kWaitLoads = 0x0f70;  // s_waitcnt: no vector memory access in flight (or n: | n)
-constexpr int kWaitLds = 0xc07f;    // s_waitcnt: no LDS access in flight
+
+// Waits until at most the N youngest of this wave's vector memory accesses are in flight, and
+// until its LDS accesses are done.  The compiler moves no access over either.
+template <int N = 0>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | (N >> 4 << 14));
+  asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void wait_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);
+  asm volatile("" ::: "memory");
+}
 
 // Row state and output tiles of NI 16-row tiles: lane = row l16, d = 16 dt + 4 lg + i.
 template <int D, int NI>
@@ -446,7 +457,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_tile_kernel(AttnParams p
     const int b = s & 1;
     // this wave's part of tile s is in LDS; behind the barrier every wave's is, and all have
     // read tile s - 1, whose buffer takes tile s + 1
-    __builtin_amdgcn_s_waitcnt(kWaitLoads);
+    wait_loads();
     const bool diagonal = (s + 1) * BN > tile_all_keys;  // some row does not see all these keys
     if (diagonal) {
       const bool any = any_odd(&sv[b][BN / 4 * wave][0], BN / 4 * D, lane, 64);
@@ -507,7 +518,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_tile_kernel(AttnParams p
   for (int s = max(first, tile_all_keys / BN); odd && s < end; ++s) {
     lds_barrier();  // reads of the tiles before are done
     load(s);
-    __builtin_amdgcn_s_waitcnt(kWaitLoads);
+    wait_loads();
     lds_barrier();
 #pragma unroll
     for (int js = 0; js < JT / 2; ++js)
@@ -613,9 +624,8 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_token_kernel(AttnParams 
   int buf = 0;
   for (int s = first + wave; s < end; s += 4, buf ^= 1) {
     // the oldest step is in place when only the next one's loads are in flight
-    if (s + 4 < end) __builtin_amdgcn_s_waitcnt(kWaitLoads | (2 * IPT & 15) | (2 * IPT >> 4 << 14));
-    else __builtin_amdgcn_s_waitcnt(kWaitLoads);
-    asm volatile("" ::: "memory");
+    if (s + 4 < end) wait_loads<2 * IPT>();
+    else wait_loads();
     // some row does not see all of these keys
     if ((s + 1) * KEYS > all_keys && any_odd(&sm.s.v[wave][buf][0][0], KEYS * D, lane, 64)) {
       odd = true;
@@ -670,8 +680,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_token_kernel(AttnParams 
       }
     }
     // this step's reads are done before its place is written again
-    __builtin_amdgcn_s_waitcnt(kWaitLds);
-    asm volatile("" ::: "memory");
+    wait_lds();
     if (s + 8 < end) load(s + 8, buf);
   }
 
@@ -679,11 +688,9 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_token_kernel(AttnParams 
   for (int s = first + wave; odd && s < end; s += 4) {
     if ((s + 1) * KEYS <= all_keys) continue;
     load(s, 0);
-    __builtin_amdgcn_s_waitcnt(kWaitLoads);
-    asm volatile("" ::: "memory");
+    wait_loads();
     add_odd(acc, s * KEYS + 4 * lg, last, [&](int d) { return v_op(0, d); });
-    __builtin_amdgcn_s_waitcnt(kWaitLds);
-    asm volatile("" ::: "memory");
+    wait_lds();
   }
 
   // ---- join the waves: maxima and sums first, then the outputs, one 16-row tile at a time
