@@ -26,16 +26,23 @@ def hipcc() -> str:
     return os.path.join(rocm(), "bin", "hipcc")
 
 
-def build_serving_calls(verbose: bool = False) -> str:
-    """Compile the serving bindings' calls (host code over torch's headers)."""
+def build_serving_calls(verbose: bool = False) -> str | None:
+    """Compile the serving bindings' calls (host code over torch's headers, with ROCm's own
+    compiler); None without torch, whose tensors they take."""
     import sysconfig
 
-    import torch
+    try:
+        import torch
+    except ImportError:
+        print("torch is not installed: the serving operators' calls from Python are not built",
+              flush=True)
+        return None
     root = os.path.dirname(torch.__file__)
     inc, lib = os.path.join(root, "include"), os.path.join(root, "lib")
     tmp = CALLS_PATH + ".tmp%d" % os.getpid()
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
-           "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+    cmd = [os.path.join(rocm(), "bin", "amdclang++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
            "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(rocm(), "include"),
            "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "serving_calls.cpp"),
@@ -49,9 +56,8 @@ def build_serving_calls(verbose: bool = False) -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source and link ``libkda.so``, and the serving bindings' calls
-    (always recompiles)."""
-    build_serving_calls(verbose)
+    """Compile every HIP source and link ``libkda.so``, which needs ROCm alone, then the serving
+    bindings' calls (always recompiles)."""
     objs = []
     for src in SOURCES:
         obj = os.path.join(CSRC, os.path.splitext(src)[0] + ".o")
@@ -67,6 +73,7 @@ def build(verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB_PATH)
+    build_serving_calls(verbose)
     return LIB_PATH
 
 
