@@ -10,10 +10,10 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 from . import _abi
-from ._build import LIB_PATH, build  # noqa: F401  (build() is the in-tree compile step)
-
+from ._build import CALLS_PATH, LIB_PATH, build  # noqa: F401  (build(): the in-tree compile step)
 
 __all__ = ["kda_fwd", "kda_fwd_sched", "kda_fwd_ordered", "kda_fwd_transposed_state",
            "kda_fwd_bf16_state",
@@ -41,18 +41,32 @@ KDA_DTYPE_FP32 = 1
 
 _lib = None
 
-# The serving operators live in a module that imports torch at once (their checks run for
-# every token), so it is loaded with the first of them that is used.
+# The serving operators live in a module that imports torch and their compiled calls at once
+# (their checks run for every token), so it is loaded with the first of them that is used.
+# Naming one, as ``import *`` does, needs neither: before both are there it gives a function
+# that looks again when it is called.
 _SERVING = ("kda_step", "kda_la_step", "kda_la_fwd", "kda_la_workspace_bytes", "kda_attn_fwd",
             "kda_attn_workspace_bytes")
+
+
+def _serving(name):
+    from . import serving
+    globals().update((n, getattr(serving, n)) for n in _SERVING)
+    return globals()[name]
 
 
 def __getattr__(name):
     if name not in _SERVING:
         raise AttributeError("module %r has no attribute %r" % (__name__, name))
-    from . import serving
-    globals().update((n, getattr(serving, n)) for n in _SERVING)
-    return globals()[name]
+    if sys.modules.get("torch") is not None and os.path.exists(CALLS_PATH):
+        return _serving(name)
+
+    def later(*args, **kwargs):
+        return _serving(name)(*args, **kwargs)
+
+    later.__name__ = later.__qualname__ = name
+    later.__doc__ = "%s of the module ``serving``, which is loaded by the first call." % name
+    return later
 
 
 class KdaError(RuntimeError):
