@@ -427,17 +427,25 @@ int kda_la_step_check(const void* q, int64_t q_row, const void* k, int64_t k_row
  *                  its head's chunk and all that follow.
  *   initial_state, final_state, cu_seqlens, num_seqs, B, T  as for kda_fwd, the in-place
  *                  state alias included.  An empty sequence passes its state through.
- *   H, Hk, D       H % Hk == 0, H * D < 2^24, D in {32, 64, 128}.
+ *   H, Hk, D       H % Hk == 0, H * D < 2^24, D in {32, 64, 128}.  (num_seqs + 8) * H at
+ *                  most 2^23 - 8, and the same for a workspace's slots (KDA_ERR_BAD_SHAPE).
  *   segment        0 (automatic), or tokens per segment: a multiple of 64, at most 2^20
  *                  (KDA_ERR_BAD_SCHEDULE).  A few long sequences do not fill the device
  *                  one workgroup per (sequence, head): their tokens are then split into
  *                  segments, whose own sums are formed first (four kernels instead of
- *                  one).  The state before a segment is then a sum in another order, so
- *                  results differ from the unsegmented ones by fp32 roundings of the state.
+ *                  one).  The state before a segment is then a sum in another order
+ *                  (fp32 roundings of the state).
  *   workspace      caller-owned device memory, 16-byte aligned, of at least
  *                  kda_la_workspace_bytes(B * T, num_seqs, H, D, segment) bytes
  *                  (KDA_ERR_BAD_WORKSPACE), scratch on return: calls that may overlap in
  *                  time need one each.  With segment 0 it may be NULL: no segments then.
+ * Roundings, relative to the sum of the absolute values of an output's (or state element's)
+ * terms: the scores times their weights and the state as an operand of S q are rounded to bf16
+ * once each, or held in two bf16 parts in calls of B * T * H <= 2048; the weighted v of the
+ * state's update to 2^-17, or to 2^-25 in those calls and where final_state is fp32.  So a
+ * sequence's results depend, by these roundings, on the size of its call, on segments (which the
+ * automatic choice takes from the whole batch), and on final_state's type.  They never depend
+ * on what the other sequences hold, and a call repeats itself bit for bit.
  * Infinities and NaN of one token reach outputs of that token and later ones of its sequence
  * only: those of q its own, of k all of its heads', of v its value's (as infinities or NaN,
  * whatever the decays since, in segments or without).
@@ -472,7 +480,8 @@ int64_t kda_la_workspace_bytes(int64_t T_total, int64_t num_seqs, int64_t H, int
  *
  *     out_i = sum_j softmax_j(scale q_i . k_j) v_j,    lse_i = log sum_j exp(scale q_i . k_j)
  *
- * and a query that sees no key (Lk < Lq, or no keys) gets out 0 and lse minus infinity.
+ * and a query that sees no key (Lk < Lq, or no keys), or only scores of minus infinity, gets out
+ * 0 and lse minus infinity.
  *   q              bf16 [Bq, Tq, Hq, D], row stride q_row (below 2^24).
  *   k, v           bf16 [Bk, Tk, Hk, D], row strides k_row, v_row (below 2^24); query head h
  *                  uses key/value head h / (Hq / Hk).  Batch rows follow each other: token t
@@ -500,7 +509,11 @@ int64_t kda_la_workspace_bytes(int64_t T_total, int64_t num_seqs, int64_t H, int
  *                  kda_attn_workspace_bytes(num_seqs, Bq, Tq, Bk, Tk, Hq, Hk, D, splits)
  *                  bytes (KDA_ERR_BAD_WORKSPACE), scratch on return: calls that may overlap
  *                  in time need one each.  With splits 0 it may be NULL: one part then.
- * Scores and sums are fp32; probabilities are rounded to bf16 for their product with v.
+ * Scores and sums are fp32.  For their product with v probabilities are rounded to bf16 once, or
+ * held in two bf16 parts in calls of at most 64 rows (query tokens times Hq / Hk) a sequence on
+ * average; splits sum in another order.  A sequence's results depend on its call by these
+ * roundings, relative to the sum of the absolute values of its terms, and a call repeats itself
+ * bit for bit.
  * Infinities and NaN reach the outputs of the queries that see them and no others.
  */
 int kda_attn_fwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
