@@ -1,9 +1,10 @@
 """MI355X (gfx950) KDA recurrent prefill forward.
 
-A thin ctypes binding over ``libkda.so`` (built from ``csrc/`` with hipcc): it
-checks tensor dtypes, devices and contiguity, passes raw device pointers, sizes
-and torch's current HIP stream to the C ABI declared in ``include/kda.h``, and
-turns status codes into exceptions.  Every step of the computation runs in the
+Thin bindings over ``libkda.so`` (built from ``csrc/`` with hipcc), the prefill's through
+ctypes, the serving operators' (module ``serving``) through a compiled module.  They
+check tensor dtypes, devices and contiguity, pass raw device pointers, sizes and
+torch's current HIP stream to the C ABI declared in ``include/kda.h``, and turn
+status codes into exceptions.  Every step of the computation runs in the
 library's kernels; there is no other code path.
 """
 from __future__ import annotations

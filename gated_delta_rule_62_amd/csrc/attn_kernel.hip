@@ -15,10 +15,11 @@
 // per lane and tile, two cross-lane steps reduce a row, and two accumulator tiles of P^T
 // pack into the operand of the second product without passing through LDS (V^T is read
 // transposed from LDS in the same key order).  The maximum is only raised when a row
-// outgrows it by 2^8: p then reaches 256 at most, which costs no accuracy in a float, and
-// almost every step skips the rescaling of the output.  p is rounded to bf16 for the
-// product (the sum uses the unrounded p): with the output's own rounding that stays below
-// 1.5 roundings of out.  The kernel for few rows takes a second bf16 part of p.
+// outgrows it by 2^8 (a published refinement of the running maximum): p then reaches 256 at
+// most, which costs no accuracy in a float, and almost every step skips the rescaling of the
+// output.  p is rounded to bf16 for the product, at most half a bf16 step of each term's
+// absolute value (the sum uses the unrounded p); a second part would be half as many products
+// again.  The kernel for few rows, bound by its loads, takes a second bf16 part of p.
 //
 // Infinities and NaN of v behind a row's last key would reach it through the product, as zero
 // times them.  On the diagonal's tiles they are dropped from LDS, and what they mean for the
@@ -27,7 +28,7 @@
 // Few rows leave the device idle; then `splits` workgroups share a tile's keys, write
 // unnormalised fp32 outputs with their maximum and sum, and a second kernel joins them.
 //
-// Measured (D 128): 8192 tokens of 32/8 heads 520-535 us, 1.05 PFLOP/s, where the matrix
+// Measured (D 128): 8192 tokens of 32/8 heads 520-542 us, 1.01-1.05 PFLOP/s, where the matrix
 // products alone take 400 at the clock they bring the card down to; one token of each of 32
 // requests over 1024-8192 keys, 32/8 heads, 121 us, 5.0 TB/s, as its loads alone.
 #include "api_util.h"
@@ -190,8 +191,8 @@ __device__ __forceinline__ u32x4_t rows_words(const u16* base, int64_t row, int 
 
 // 16 bytes per lane from memory to LDS: lane l's land 16 l bytes behind `to` (uniform);
 // zeros where `off` is behind the descriptor's end.  It has no result the compiler could
-// track: wait_loads ends it, and a barrier shows it to the other waves.  ONCE marks what no
-// other workgroup reads, so that it does not displace what others do.
+// track: wait_loads ends it, and a barrier shows it to the other waves.  ONCE (non-temporal)
+// is for what one workgroup alone reads as a rule, so that it does not displace what others do.
 template <bool ONCE>
 __device__ __forceinline__ void load_lds(u32x4_t rsrc, const u16* to, uint32_t off) {
   const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const u16*)to;
@@ -538,8 +539,9 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_tile_kernel(AttnParams p
 }
 
 // ---- single tokens: the four waves share NI 16-row tiles and take 32 keys each in turn.
-// Bound by HBM.  A key is read by one wave only, so each wave brings its keys and values
-// into a piece of LDS of its own, two steps deep, and waits for nobody until the waves join
+// Bound by HBM.  A key is read by one wave of a workgroup (and by one workgroup, but for a
+// long sequence among many short ones), so each wave brings its keys and values into a piece
+// of LDS of its own, two steps deep, and waits for nobody until the waves join
 // their results; one workgroup of a compute unit keeps up to 128 KB in flight.
 template <int D, int NI>
 __global__ __launch_bounds__(kAttnThreads, 1) void attn_token_kernel(AttnParams p) {

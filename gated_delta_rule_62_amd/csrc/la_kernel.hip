@@ -22,9 +22,8 @@
 // exponentials stand for a row of 64.
 //
 // Roundings.  Scores times weights, and the state as an operand of S q, are rounded to
-// bf16 once each: out is a bf16 sum of two such parts, so its error stays below 1.5 of
-// its own rounding (second parts of both cost 5-13% of a large call; small ones have them).
-// The state itself must not lose bits at each of thousands of chunks:
+// bf16 once each, at most half a bf16 step of each term's absolute value (second parts of
+// both cost 11-29% of a large call; small ones have them).  The state itself must not lose bits at each of thousands of chunks:
 // its update multiplies k (exact in bf16) by the weighted v in two or three bf16 parts,
 // whose sum holds the fp32 product to 2^-17 or 2^-25.
 //
@@ -45,8 +44,8 @@
 // carries it to the outputs and the final state behind.
 //
 // Measured (D 128, bf16 states): 2 x 1024 tokens of 96 heads 58 us, where loads and stores alone
-// take 50; 32,768 tokens of 32 heads 350 us, 3.1 TB/s of q, k, v and out and 4.3 of all that
-// the three passes move, a copy's rate in their access pattern; 64 prompts of 1-512 tokens, 32
+// take 50; 32,768 tokens of 32 heads 353 us, 3.1 TB/s of q, k, v and out and 4.2 of all that
+// the passes move, a copy's rate in their access pattern; 64 prompts of 1-512 tokens, 32
 // heads, fp32 states 160 us, 4.1 TB/s, loads and stores alone 136.
 #include "api_util.h"
 #include "gfx950.h"
@@ -664,9 +663,11 @@ hipError_t go(const LaParams& p, hipStream_t stream) {
 
 // An fp32 final state keeps three parts; where none leaves, or one rounded to bf16, two
 // parts hold it to 2^-17 and save a third of the update's products.
-// Few outputs take every second part: their call is bounded by its latency, not by products
-// (128 tokens of 2 heads: the same time either way; 512 tokens of 8 heads 23 and 24), and the fewer
-// roundings a result has, the less they average out.
+// Calls of few outputs take every second part.  It costs them 0.8 to 2.4 us (128 tokens of 2
+// heads, D 32: 7.0 and 7.8 us; 512 tokens of 4 heads, D 128: 24.0 and 26.4), as it would a
+// little beyond the limit (8 heads: 24.9 and 27.2), and large calls in proportion (2 x 1024
+// tokens of 96 heads 58.8 and 75.7 us; 64 short prompts of 32 heads 161 and 178): the limit is
+// a choice between accuracy and time, and stands in the operator's description.
 template <int D>
 hipError_t by_parts(const LaParams& p, hipStream_t stream) {
   if (p.T_total * p.H <= 2048) return go<D, 3, true>(p, stream);
