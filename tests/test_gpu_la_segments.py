@@ -68,8 +68,8 @@ PLANTS = {"gate": [("g", 3, 1, 0, NAN)], "v": [("v", 10, 2, 5, INF), ("v", 77, 1
 
 @pytest.mark.parametrize("plant", sorted(PLANTS))
 @pytest.mark.parametrize("lens,H,Hk,D,segment", [
-    ([700], 4, 2, 32, 128), ([700], 4, 2, 64, 192), ([450], 4, 2, 128, 128), ([900], 4, 2, 128, 256),
-    ([300, 0, 513, 40], 4, 2, 64, 64)])
+    ([700], 4, 2, 32, 128), ([700], 4, 2, 64, 192), ([450], 4, 2, 128, 128),
+    ([900], 4, 2, 128, 256), ([300, 0, 513, 40], 4, 2, 64, 64)])
 def test_reach_every_later_segment(lens, H, Hk, D, segment, plant):
     print("kda_la_fwd segments", plant, lens, H, Hk, D, segment, flush=True)
     x = _decaying(31, lens, H, Hk, D)

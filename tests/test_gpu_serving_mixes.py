@@ -8,12 +8,14 @@ from __future__ import annotations
 import pytest
 import torch
 
+import gated_delta_rule_62_amd as kda
 from tests.serving_forms import U16
-from tests.test_gpu_attn import _packed
+from tests.test_gpu_attn import _check_seq, _gen, _normal, _packed
 from tests.test_gpu_la import _compare, _inputs, _run
 from tests.test_gpu_la import test_infinities_and_nan_reach_later_tokens_only as odd_values
 
 pytestmark = pytest.mark.gpu
+DEV = "cuda"
 
 
 def _lengths(n, most, seed):
@@ -50,6 +52,57 @@ def test_prompts_beside_single_tokens(ql, Hq, Hk, D):
     _packed(len(ql), ql, kl, Hq, Hk, D)
 
 
+@pytest.mark.parametrize("ql,Hq,Hk,D,splits", [
+    ([1, 5, 0, 2], 8, 2, 128, 0), ([70, 1, 0, 200, 129], 4, 2, 64, 0),
+    ([1] * 9 + [30] * 11, 6, 1, 64, 3), ([90] * 18, 2, 2, 128, 2)])
+def test_packed_queries_over_caches(ql, Hq, Hk, D, splits):
+    """Packed queries, keys in rows of a cache filled to different lengths; NaN behind them."""
+    print("kda_attn_fwd packed over caches", ql, Hq, Hk, D, splits, flush=True)
+    g, N, cap = _gen(len(ql) + D), len(ql), 333
+    lens = [(q + 61 * n) % (cap + 1) for n, q in enumerate(ql)]
+    q = _normal(g, 1, sum(ql) + 2, Hq, D)
+    k, v = torch.split(_normal(g, N, cap, 2 * Hk, D), [Hk, Hk], dim=2)
+    for n, length in enumerate(lens):
+        k[n, length:], v[n, length:] = float("nan"), float("nan")
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:3], 7.0, device=DEV)
+    kda.kda_attn_fwd(q, k, v, 0.1, out, lse=lse, splits=splits,
+                     k_lens=torch.tensor(lens, device=DEV),
+                     cu_seqlens_q=torch.tensor([0] + ql).cumsum(0).to(DEV))
+    at = 0
+    for n, (length, lk) in enumerate(zip(ql, lens)):
+        s = slice(at, at + length)
+        _check_seq(out[0, s], lse[0, s], q[0, s], k[n, :lk], v[n, :lk], 0.1, "sequence %d" % n)
+        at += length
+    assert (out[0, at:] == 7.0).all() and (lse[0, at:] == 7.0).all()
+
+
+@pytest.mark.parametrize("Tq,kl,Hq,Hk,D", [(1, [5, 0, 400, 33], 8, 2, 64),
+                                           (150, [150, 20, 700], 4, 4, 128)])
+def test_rows_of_queries_over_packed_keys(Tq, kl, Hq, Hk, D):
+    """Queries as batch rows, keys packed."""
+    print("kda_attn_fwd rows over packed keys", Tq, kl, Hq, Hk, D, flush=True)
+    g, N = _gen(Tq), len(kl)
+    q = _normal(g, N, Tq, Hq, D)
+    k, v = _normal(g, 1, sum(kl), Hk, D), _normal(g, 1, sum(kl), Hk, D)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device=DEV)
+    kda.kda_attn_fwd(q, k, v, 0.1, out, lse=lse,
+                     cu_seqlens_k=torch.tensor([0] + kl).cumsum(0).to(DEV))
+    at = 0
+    for n, lk in enumerate(kl):
+        s = slice(at, at + lk)
+        _check_seq(out[n], lse[n], q[n], k[0, s], v[0, s], 0.1, "sequence %d" % n)
+        at += lk
+
+
+@pytest.mark.parametrize("segment", [0, 64])
+def test_no_tokens(segment):
+    """A packed batch without a token passes its states through, in segments too."""
+    H, D = 3, 32
+    x = _inputs(54, [0, 0], H, H, D)
+    out, final = _run(x, 1.0, segment=segment)
+    assert out.numel() == 0 and torch.equal(final, x["initial"])
+
+
 @pytest.mark.parametrize("D", [32, 64, 128])
 def test_one_prompt_alone_and_packed(D):
     """Few tokens carry second bf16 parts, more do not; a final state's type, or having none,
@@ -64,7 +117,7 @@ def test_one_prompt_alone_and_packed(D):
         one = {k: t[:, at:at + length] for k, t in x.items() if k in "qkv"}
         one.update(g=x["g"][:, at:at + length].contiguous(), decay=x["decay"],
                    initial=x["initial"][n:n + 1], lens=[length],
-                   cu=torch.tensor([0, length], device="cuda"))
+                   cu=torch.tensor([0, length], device=DEV))
         for out_state in (torch.float32, torch.bfloat16):
             alone, state = _run(one, scale, out_state)
             _compare(one, scale, alone, state)
