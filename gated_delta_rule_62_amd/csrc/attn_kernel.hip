@@ -32,6 +32,7 @@
 // products alone take 400 at the clock they bring the card down to; one token of each of 32
 // requests over 1024-8192 keys, 32/8 heads, 121 us, 5.0 TB/s, as its loads alone.
 #include "api_util.h"
+#include "attn_rows.h"
 #include "gfx950.h"
 #include "ops_params.h"
 
@@ -40,76 +41,7 @@ namespace {
 
 using namespace dev;
 
-constexpr float kRaise = 8.f;  // base-2 slack of the running maximum
-constexpr float kNone = -__builtin_inff();
-
-// A tile of rows: its sequence's queries and keys, its rows.
-struct Tile {
-  int64_t q0, k0;   // first query and key token
-  int Lq, Lk;       // lengths
-  int row0, rows;   // first row of the tile, rows of the sequence (Lq * G)
-};
-
-__device__ __forceinline__ int64_t clamp64(int64_t x, int64_t lo, int64_t hi) {
-  return x < lo ? lo : (x > hi ? hi : x);
-}
-
-__device__ __forceinline__ void query_bounds(const AttnParams& p, int n, int64_t& a, int64_t& b) {
-  if (p.cu_q != nullptr) {
-    a = clamp64(p.cu_q[n], 0, p.Tq_total);
-    b = clamp64(p.cu_q[n + 1], a, p.Tq_total);
-  } else {
-    a = (int64_t)n * p.Tq;
-    b = a + p.Tq;
-  }
-}
-
-__device__ __forceinline__ void key_bounds(const AttnParams& p, int n, int64_t& a, int64_t& b) {
-  if (p.cu_k != nullptr) {
-    a = clamp64(p.cu_k[n], 0, p.Tk);
-    b = clamp64(p.cu_k[n + 1], a, p.Tk);
-  } else {
-    a = (int64_t)n * p.Tk;
-    b = a + (p.k_lens != nullptr ? clamp64(p.k_lens[n], 0, p.Tk) : p.Tk);
-  }
-}
-
-// The tile of `tile_rows` rows that starts at row row0 of sequence n; false if there is none.
-__device__ __forceinline__ bool set_tile(const AttnParams& p, int n, int64_t row0, Tile& t) {
-  int64_t a, b;
-  query_bounds(p, n, a, b);
-  if (row0 < 0 || row0 >= (b - a) * p.G) return false;
-  t.row0 = (int)row0;
-  t.q0 = a;
-  t.Lq = (int)(b - a);
-  t.rows = t.Lq * p.G;
-  key_bounds(p, n, a, b);
-  t.k0 = a;
-  t.Lk = (int)(b - a);
-  return true;
-}
-
-// Tile number `slot` of a key/value head, in any order; false if it has none.
-__device__ __forceinline__ bool find_tile(const AttnParams& p, unsigned slot, int tile_rows,
-                                          Tile& t) {
-  if (p.cu_q == nullptr) {
-    const unsigned per = (unsigned)((p.Tq * p.G + tile_rows - 1) / tile_rows), n = slot / per;
-    return n < (unsigned)p.N && set_tile(p, (int)n, (int64_t)(slot % per) * tile_rows, t);
-  }
-  // the last sequence whose first slot is not behind this one (first slots grow strictly)
-  int lo = 0, hi = p.N - 1;
-  int64_t a, b;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    query_bounds(p, mid, a, b);
-    if (a * p.G / tile_rows + mid <= slot) lo = mid;
-    else hi = mid - 1;
-  }
-  query_bounds(p, lo, a, b);
-  return set_tile(p, lo, (slot - (a * p.G / tile_rows + lo)) * tile_rows, t);
-}
-
-// The same with the tiles that see the most keys first, as workgroups start in order and a
+// Tile number `slot` with the tiles that see the most keys first, as workgroups start in order and a
 // long one that starts last would set the time: batch rows by their tile, packed sequences
 // (of up to 16: the ranking costs a short workgroup more than it gains with many) longest
 // keys first, each from its last tile.  Whole waves call it.
@@ -147,19 +79,6 @@ __device__ __forceinline__ bool find_tile_longest_first(const AttnParams& p, uns
   return set_tile(p, __builtin_amdgcn_readfirstlane(n), row0, t);
 }
 
-__device__ __forceinline__ float max_over_groups(float x) {
-  Two t = swap16(x);
-  x = fmaxf(t.a, t.b);
-  t = swap32(x);
-  return fmaxf(t.a, t.b);
-}
-__device__ __forceinline__ float sum_over_groups(float x) {
-  Two t = swap16(x);
-  x = t.a + t.b;
-  t = swap32(x);
-  return t.a + t.b;
-}
-
 // Descriptor of `tokens` rows of one head from `base`; nothing when there are none.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const u16* base, int64_t row,
                                                             int tokens, int D) {
@@ -168,16 +87,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const u16* base, int
 
 __device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
-}
-
-// Waits for the loads of a tile of rows before the loop over the keys: their first use inside
-// it would make every step wait for all loads in flight.
-template <int KS, int NI>
-__device__ __forceinline__ void end_loads(u32x4_t (&q)[KS][NI]) {
-#pragma unroll
-  for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-    for (int i = 0; i < NI; ++i) asm volatile("" : "+v"(q[ks][i]));
 }
 
 // The same descriptor as four words, for load_lds.
@@ -222,69 +131,6 @@ __device__ __forceinline__ void wait_lds() {
   __builtin_amdgcn_s_waitcnt(0xc07f);
   asm volatile("" ::: "memory");
 }
-
-// Row state and output tiles of NI 16-row tiles: lane = row l16, d = 16 dt + 4 lg + i.
-template <int D, int NI>
-struct Acc {
-  static constexpr int DT = D / 16;
-  f32x4_t o[DT][NI];
-  float m[NI], l[NI];  // maximum of the scaled scores (base 2), this lane's part of the sum
-
-  __device__ __forceinline__ void init() {
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      m[i] = kNone;
-      l[i] = 0.f;
-#pragma unroll
-      for (int d = 0; d < DT; ++d) o[d][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    }
-  }
-
-  // Raises the running maximum where a row of x (scores, masked ones minus infinity) outgrows
-  // it.
-  template <int JT>
-  __device__ __forceinline__ void raise(const f32x4_t (&x)[JT][NI], float c) {
-    float top[NI];
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      float t = kNone;
-#pragma unroll
-      for (int j = 0; j < JT; ++j) {
-        t = fmaxf(t, fmaxf(x[j][i][0], x[j][i][1]));
-        t = fmaxf(t, fmaxf(x[j][i][2], x[j][i][3]));
-      }
-      top[i] = max_over_groups(t) * c;
-      any |= top[i] > m[i] + kRaise;  // minus infinity plus kRaise: any score raises it
-    }
-    if (__any(any)) {  // uniform
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const float now = fmaxf(m[i], top[i]);
-        const float f = now == kNone ? 1.f : __builtin_amdgcn_exp2f(m[i] - now);
-        m[i] = now;
-        l[i] *= f;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[d][i] *= f;
-      }
-    }
-  }
-
-  // One 16-key tile of scores to probabilities, in place.
-  __device__ __forceinline__ void exps(f32x4_t (&x)[NI], float c) {
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const float base = m[i] == kNone ? 0.f : -m[i];
-      float s = 0.f;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        x[i][r] = __builtin_amdgcn_exp2f(fmaf(x[i][r], c, base));
-        s += x[i][r];
-      }
-      l[i] += s;
-    }
-  }
-};
 
 // Probability tiles 2 js and 2 js + 1 as the operand of 32 keys.
 __device__ __forceinline__ u32x4_t p_op(f32x4_t a, f32x4_t b) {
@@ -756,8 +602,9 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_token_kernel(AttnParams 
 }
 
 // Joins the splits of a row, one wave per (query token, head): lane s weighs split s (there
-// are at most 64), then the lanes share the row's D values.
-template <int D>
+// are at most 64), then the lanes share the row's D values.  GAPS: a split without keys has no
+// outputs to read.
+template <int D, bool GAPS>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
   constexpr int V = D / 64;  // values per lane
   typedef float vec __attribute__((ext_vector_type(V)));
@@ -771,6 +618,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
   }
   f32x2_t ml = {kNone, 0.f};
   if (lane < p.splits) ml = *reinterpret_cast<const f32x2_t*>(p.ws_ml + 2 * (lane * rows + at));
+  const uint64_t filled = GAPS ? __ballot(!(ml[0] == kNone && ml[1] == 0.f)) : ~0ull;
   float m = ml[0];
 #pragma unroll
   for (int x = 1; x < 64; x *= 2) m = fmaxf(m, __shfl_xor(m, x));
@@ -784,7 +632,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
     vec x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      x[i] = s0 + i < p.splits ? *reinterpret_cast<const vec*>(o + (s0 + i) * rows * D) : vec{};
+      x[i] = s0 + i < p.splits && (filled >> (s0 + i) & 1) ? *reinterpret_cast<const vec*>(o + (s0 + i) * rows * D) : vec{};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       sum += x[i] * __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), (s0 + i) & 63));
@@ -795,6 +643,12 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
   else out[0] = (u16)pack_bf16(sum[0] * g, 0.f);
   if (p.lse != nullptr && lane == 0)
     p.lse[at] = l == 0.f ? kNone : (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+template <int D, bool GAPS>
+void join(const AttnParams& p, hipStream_t stream) {
+  const int64_t rows = p.Tq_total * p.Hq;
+  attn_join_kernel<D, GAPS><<<dim3((unsigned)((rows + 3) / 4)), 256, 0, stream>>>(p);
 }
 
 template <int D>
@@ -809,10 +663,7 @@ hipError_t go(const AttnParams& p, const AttnSchedule& s, hipStream_t stream) {
   } else {
     attn_tile_kernel<D, 2><<<grid, kAttnThreads, 0, stream>>>(p);
   }
-  if (p.splits > 1) {
-    const int64_t rows = p.Tq_total * p.Hq;
-    attn_join_kernel<D><<<dim3((unsigned)((rows + 3) / 4)), 256, 0, stream>>>(p);
-  }
+  if (p.splits > 1) join<D, false>(p, stream);
   return hipGetLastError();
 }
 
@@ -829,6 +680,12 @@ AttnSchedule attn_schedule(int64_t Tq_total, int64_t N, int64_t G) {
 
 hipError_t launch_attn(const AttnParams& p, const AttnSchedule& s, int D, hipStream_t stream) {
   return D == 64 ? go<64>(p, s, stream) : go<128>(p, s, stream);
+}
+
+hipError_t launch_attn_join(const AttnParams& p, int D, hipStream_t stream) {
+  if (D == 64) join<64, true>(p, stream);
+  else join<128, true>(p, stream);
+  return hipGetLastError();
 }
 
 }  // namespace kda

@@ -4,7 +4,6 @@
 
 #include <cmath>
 #include <cstdint>
-#include <limits>
 
 #include "../../include/kda.h"
 #include "api_util.h"
@@ -12,31 +11,20 @@
 
 namespace {
 
+using kda::aligned16;
+using kda::any_overlap;
+using kda::attn_c;
+using kda::attn_factor;
+using kda::batch_ok;
+using kda::kMaxBytes;
 using kda::make_range;
 using kda::overlaps;
 using kda::Range;
-
-constexpr int64_t kMaxBytes = (int64_t)1 << 62;  // of one tensor: the range arithmetic cannot wrap
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+using kda::row_ok;
+using kda::span_bytes;
+using kda::status;
 
 bool state_dtype_ok(int dtype) { return dtype == KDA_DTYPE_BF16 || dtype == KDA_DTYPE_FP32; }
-
-// A row stride in elements: whole 16-byte units, at least the row itself.
-bool row_ok(int64_t row, int64_t heads, int64_t D) { return row >= heads * D && row % 8 == 0; }
-
-// Bytes from the first element of `rows` bf16 rows to the last, or -1 beyond kMaxBytes.
-int64_t span_bytes(int64_t rows, int64_t row, int64_t heads, int64_t D) {
-  if (rows <= 0) return 0;
-  if (row > kMaxBytes / 2 / rows) return -1;
-  return ((rows - 1) * row + heads * D) * 2;
-}
-
-bool any_overlap(Range out, const Range* ins, int n) {
-  for (int i = 0; i < n; ++i)
-    if (overlaps(out, ins[i])) return true;
-  return false;
-}
 
 // What kda_step and kda_la_step share: sizes, the pool, the slots.
 int step_resolve(const void* state, int state_dtype, int64_t num_slots, const int64_t* slot_in,
@@ -155,15 +143,6 @@ int64_t la_ws_bytes(int64_t T_total, int64_t N, int64_t H, int64_t D, int64_t se
   return kda::la_ws_floats(kda::la_slots(T_total, N, seg), H, D) * 4;
 }
 
-// The sizes of a packed or batched call; num_seqs sequences.
-int batch_ok(const int64_t* cu, int64_t N, int64_t B, int64_t T) {
-  if (B < 1 || T < 0) return KDA_ERR_BAD_SHAPE;
-  if (T == 0 && !cu) return KDA_ERR_BAD_SHAPE;
-  if (T > ((int64_t)1 << 40) / B) return KDA_ERR_BAD_SHAPE;
-  if (cu ? (B != 1 || N < 1) : N != B) return KDA_ERR_BAD_VARLEN;
-  return KDA_OK;
-}
-
 int la_check(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
              int64_t v_row, const float* g, const float* decay, float scale, const void* out,
              const void* s_in, int in_dtype, const void* s_out, int out_dtype, const int64_t* cu,
@@ -269,9 +248,6 @@ int64_t attn_ws_bytes(int64_t total, int64_t Hq, int64_t D, int64_t splits) {
   return splits > 1 ? splits * total * Hq * (D + 2) * 4 : 0;
 }
 
-// The factor of the scores in base 2.
-float attn_c(float scale) { return static_cast<float>(scale * 1.4426950408889634); }
-
 int attn_check(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
                int64_t v_row, float scale, const void* out, const float* lse, const int64_t* cu_q,
                const int64_t* cu_k, const int64_t* k_lens, int64_t N, int64_t Bq, int64_t Tq,
@@ -308,8 +284,6 @@ int attn_check(const void* q, int64_t q_row, const void* k, int64_t k_row, const
   *splits_out = sp;
   return KDA_OK;
 }
-
-int status(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_HIP; }
 
 }  // namespace
 
@@ -507,9 +481,7 @@ int kda_attn_fwd(const void* q, int64_t q_row, const void* k, int64_t k_row, con
   p.Hq = static_cast<int32_t>(Hq);
   p.Hk = static_cast<int32_t>(Hk);
   p.G = static_cast<int32_t>(Hq / Hk);
-  // never zero: minus infinity times it stands for a masked score.  The smallest float in
-  // place of zero moves a finite score by 2^-21 at most, six roundings of its exponential.
-  p.c = std::fmax(attn_c(scale), std::numeric_limits<float>::denorm_min());
+  p.c = attn_factor(scale);
   p.splits = static_cast<int32_t>(sp);
   p.ws_o = static_cast<float*>(workspace);
   p.ws_ml = sp > 1 ? p.ws_o + sp * p.Tq_total * Hq * D : nullptr;

@@ -109,6 +109,8 @@ constexpr int kAttnThreads = 256;
 constexpr int kAttnKeys = 64;  // keys per step of the tile kernel
 
 hipError_t launch_attn(const AttnParams& p, const AttnSchedule& s, int D, hipStream_t stream);
+// Joins the splits of a call alone; one without keys has written its maximum and sum only.
+hipError_t launch_attn_join(const AttnParams& p, int D, hipStream_t stream);
 
 }  // namespace kda
 
