@@ -22,6 +22,8 @@ __all__ = ["kda_fwd", "kda_fwd_sched", "kda_fwd_ordered", "kda_fwd_transposed_st
            "kda_longest_first", "kda_fwd_check", "c_args",
            "kda_step", "kda_la_step", "kda_la_fwd", "kda_la_workspace_bytes",
            "kda_attn_fwd", "kda_attn_workspace_bytes",
+           "kda_norm", "kda_rope", "kda_rope_freqs", "kda_cache4_put", "kda_cache4_empty",
+           "kda_attn4_fwd", "kda_attn4_workspace_bytes",
            "kda_chunk_anchor", "kda_status_string", "KdaError", "library_path", "load_library"]
 
 KDA_OK = 0
@@ -47,7 +49,8 @@ _lib = None
 # Naming one, as ``import *`` does, needs neither: before both are there it gives a function
 # that looks again when it is called.
 _SERVING = ("kda_step", "kda_la_step", "kda_la_fwd", "kda_la_workspace_bytes", "kda_attn_fwd",
-            "kda_attn_workspace_bytes")
+            "kda_attn_workspace_bytes", "kda_norm", "kda_rope", "kda_rope_freqs",
+            "kda_cache4_put", "kda_cache4_empty", "kda_attn4_fwd", "kda_attn4_workspace_bytes")
 
 
 def _serving(name):

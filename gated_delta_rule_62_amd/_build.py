@@ -9,7 +9,8 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_PATH = os.path.join(PKG_DIR, "libkda.so")
 CALLS_PATH = os.path.join(PKG_DIR, "_serving_calls.so")
 SOURCES = ["kda_kernel.hip", "kda_api.cpp", "step_kernel.hip", "la_kernel.hip",
-           "attn_kernel.hip", "ops_api.cpp"]
+           "attn_kernel.hip", "ops_api.cpp", "norm_kernel.hip", "rope_kernel.hip",
+           "cache4_kernel.hip", "attn4_kernel.hip", "layer_api.cpp"]
 
 # Packed fp32 VALU forms are disabled for every device compile; hipcc's host pass
 # warns that it does not know the feature, which is harmless.

@@ -1,0 +1,467 @@
+// Host side of the operators around attention and recurrences declared in include/kda.h (norms,
+// rotary positions, 4-bit caches): argument validation, schedule selection and launches.
+// Nothing here touches device memory.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/kda.h"
+#include "api_util.h"
+#include "layer_params.h"
+
+namespace {
+
+using kda::aligned16;
+using kda::any_overlap;
+using kda::kCache4Tile;
+using kda::kMaxBytes;
+using kda::make_range;
+using kda::overlaps;
+using kda::Range;
+using kda::row_ok;
+using kda::span_bytes;
+using kda::status;
+
+constexpr int64_t kMostItems = ((int64_t)1 << 32) - 1;  // work-items of a launch
+
+// ---- kda_norm
+
+bool norm_group_ok(int64_t W, int64_t group) {
+  if (group == W) return true;
+  return group >= 32 && group <= 512 && (group & (group - 1)) == 0 && W % group == 0;
+}
+
+int norm_check(const void* x, int64_t x_row, const void* gate, int64_t gate_row, int gate_fn,
+               const void* post_weight, int64_t group, const void* weight, int weight_dtype,
+               float eps, const void* residual, const void* residual_out, int residual_dtype,
+               float residual_scale, const void* out, int64_t R, int64_t W) {
+  if (R < 0 || W < 8 || W % 8 != 0 || W > kda::kNormMaxW) return KDA_ERR_BAD_SHAPE;
+  if (post_weight && !norm_group_ok(W, group)) return KDA_ERR_BAD_SHAPE;
+  if (R > kMostItems / kda::norm_threads(W) / 8) return KDA_ERR_BAD_SHAPE;
+  if (gate && gate_fn != KDA_GATE_SIGMOID && gate_fn != KDA_GATE_SILU) return KDA_ERR_BAD_DTYPE;
+  if ((post_weight || weight) && weight_dtype != KDA_DTYPE_BF16 && weight_dtype != KDA_DTYPE_FP32)
+    return KDA_ERR_BAD_DTYPE;
+  if (residual && residual_dtype != KDA_DTYPE_BF16 && residual_dtype != KDA_DTYPE_FP32)
+    return KDA_ERR_BAD_DTYPE;
+  if (!std::isfinite(eps) || eps < 0.f || !std::isfinite(residual_scale))
+    return KDA_ERR_BAD_SCALE;
+  if (!post_weight && !gate && !weight && !residual) return KDA_ERR_NULL_ARG;
+  if ((residual == nullptr) != (residual_out == nullptr)) return KDA_ERR_NULL_ARG;
+  if (R > 0 && (!x || (!out && (weight || !residual)))) return KDA_ERR_NULL_ARG;
+  if (!row_ok(x_row, 1, W) || (gate && !row_ok(gate_row, 1, W)) || !aligned16(x) ||
+      !aligned16(gate) || !aligned16(post_weight) || !aligned16(weight) || !aligned16(residual) ||
+      !aligned16(residual_out) || !aligned16(out))
+    return KDA_ERR_BAD_LAYOUT;
+  const int64_t bx = span_bytes(R, x_row, 1, W), bg = gate ? span_bytes(R, gate_row, 1, W) : 0;
+  if (bx < 0 || bg < 0) return KDA_ERR_BAD_SHAPE;
+  const int64_t wb = weight_dtype == KDA_DTYPE_FP32 ? 4 : 2;
+  const int64_t rb = residual ? R * W * (residual_dtype == KDA_DTYPE_FP32 ? 4 : 2) : 0;
+  const Range ro = make_range(out, out ? R * W * 2 : 0), rh = make_range(residual_out, rb),
+              rr = make_range(residual, rb);
+  const Range ins[] = {make_range(x, bx), make_range(gate, bg),
+                       make_range(post_weight, post_weight ? group * wb : 0),
+                       make_range(weight, weight ? W * wb : 0)};
+  if (any_overlap(ro, ins, 4) || any_overlap(rh, ins, 4) || overlaps(ro, rh) || overlaps(ro, rr))
+    return KDA_ERR_BAD_ALIAS;
+  if (overlaps(rh, rr) && residual != residual_out) return KDA_ERR_BAD_ALIAS;
+  return KDA_OK;
+}
+
+// ---- kda_rope
+
+// Strided rows of one tensor: n rows of `len` elements, `row` apart.
+struct Rows {
+  const void* at;
+  int64_t row, len;
+};
+
+// Whether two tensors of n rows share a byte.  Rows of one stride that lie in other columns of
+// the same wider rows do not, though their ranges overlap.
+bool share(const Rows& a, const Rows& b, int64_t n) {
+  if (!overlaps(make_range(a.at, span_bytes(n, a.row, 1, a.len)),
+                make_range(b.at, span_bytes(n, b.row, 1, b.len))))
+    return false;
+  if (a.row != b.row) return true;
+  const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.at)) -
+                    static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.at));
+  const int64_t row = a.row * 2, shift = ((d % row) + row) % row;
+  return !(shift >= a.len * 2 && row - shift >= b.len * 2);
+}
+
+bool in_place(const Rows& a, const Rows& b) { return a.at == b.at && a.row == b.row; }
+
+int rope_check(const void* q, int64_t q_row, const void* q_out, int64_t q_out_row, const void* k,
+               int64_t k_row, const void* k_out, int64_t k_out_row, const double* freqs,
+               int64_t rot, float amplitude, const int64_t* positions, const int64_t* offsets,
+               const int64_t* cu, int64_t N, int64_t B, int64_t T, int64_t Hq, int64_t Hk,
+               int64_t D) {
+  if (D < 8 || D % 8 != 0 || D > kda::kRopeMaxD || rot < 2 || rot % 2 != 0 || rot > D)
+    return KDA_ERR_BAD_SHAPE;
+  if (Hq < 1 || Hk < 0 || Hq > (1 << 20) || Hk > (1 << 20)) return KDA_ERR_BAD_SHAPE;
+  const int sizes = kda::batch_ok(cu, N, B, T);
+  if (sizes != KDA_OK) return sizes;
+  if (N >= ((int64_t)1 << 31)) return KDA_ERR_BAD_SHAPE;
+  const int64_t tok = B * T;
+  // a workgroup for each token at most, or a few that share a token's heads
+  if (tok >= ((int64_t)1 << 24)) return KDA_ERR_BAD_SHAPE;
+  if (positions && (offsets || cu)) return KDA_ERR_BAD_VARLEN;
+  if (!std::isfinite(amplitude)) return KDA_ERR_BAD_SCALE;
+  if (!freqs || (tok > 0 && (!q || !q_out || (Hk > 0 && (!k || !k_out)))))
+    return KDA_ERR_NULL_ARG;
+  const Rows a = {q, q_row, Hq * D}, ao = {q_out, q_out_row, Hq * D}, b = {k, k_row, Hk * D},
+             bo = {k_out, k_out_row, Hk * D};
+  const Rows both[] = {a, ao, b, bo};
+  for (int i = 0; i < (Hk > 0 ? 4 : 2); ++i) {
+    if (!row_ok(both[i].row, 1, both[i].len) || !aligned16(both[i].at)) return KDA_ERR_BAD_LAYOUT;
+    if (span_bytes(tok, both[i].row, 1, both[i].len) < 0) return KDA_ERR_BAD_SHAPE;
+  }
+  if (tok == 0) return KDA_OK;
+  const Range small[] = {make_range(freqs, rot / 2 * 8), make_range(positions, positions ? tok * 8 : 0),
+                         make_range(offsets, offsets ? N * 8 : 0),
+                         make_range(cu, cu ? (N + 1) * 8 : 0)};
+  if (any_overlap(make_range(q_out, span_bytes(tok, q_out_row, 1, ao.len)), small, 4) ||
+      (share(a, ao, tok) && !in_place(a, ao)))
+    return KDA_ERR_BAD_ALIAS;
+  if (Hk > 0) {
+    if (any_overlap(make_range(k_out, span_bytes(tok, k_out_row, 1, bo.len)), small, 4) ||
+        (share(b, bo, tok) && !in_place(b, bo)) || share(a, bo, tok) || share(b, ao, tok) ||
+        share(ao, bo, tok))
+      return KDA_ERR_BAD_ALIAS;
+  }
+  return KDA_OK;
+}
+
+// ---- caches in 4 bits
+
+struct CacheRanges {
+  Range r[4];
+};
+
+// Sizes and pointers of a cache; its ranges.
+int cache4_check(const void* k4, const void* ks, const void* v4, const void* vs, int64_t slots,
+                 int64_t cap, int64_t Hk, int64_t D, CacheRanges* out) {
+  if (D != 64 && D != 128) return KDA_ERR_BAD_SHAPE;
+  if (slots < 1 || Hk < 1 || Hk >= (1 << 24) || cap < kCache4Tile || cap % kCache4Tile != 0 ||
+      cap > ((int64_t)1 << 30))
+    return KDA_ERR_BAD_SHAPE;
+  if (slots > kMaxBytes / cap / Hk / D) return KDA_ERR_BAD_SHAPE;
+  if (!k4 || !ks || !v4 || !vs) return KDA_ERR_NULL_ARG;
+  if (!aligned16(k4) || !aligned16(ks) || !aligned16(v4) || !aligned16(vs))
+    return KDA_ERR_BAD_LAYOUT;
+  const int64_t rows = slots * Hk * cap;
+  out->r[0] = make_range(k4, rows * (D / 2));
+  out->r[1] = make_range(ks, rows * (D / 32));
+  out->r[2] = make_range(v4, rows * (D / 2));
+  out->r[3] = make_range(vs, rows * (D / 32));
+  return KDA_OK;
+}
+
+int put4_check(const void* k, int64_t k_row, const void* v, int64_t v_row, const void* k4,
+               const void* ks, const void* v4, const void* vs, int64_t num_slots, int64_t cap,
+               const void* k_out, const void* v_out, const int64_t* offsets, const int64_t* slots,
+               const int64_t* cu, int64_t N, int64_t B, int64_t T, int64_t Hk, int64_t D) {
+  CacheRanges c;
+  const int st = cache4_check(k4, ks, v4, vs, num_slots, cap, Hk, D, &c);
+  if (st == KDA_ERR_BAD_SHAPE) return st;
+  const int sizes = kda::batch_ok(cu, N, B, T);
+  if (sizes != KDA_OK) return sizes;
+  const int64_t tok = B * T;
+  if (N >= ((int64_t)1 << 31) || (!slots && N > num_slots)) return KDA_ERR_BAD_SHAPE;
+  if (kda::put4_tiles(tok, T, N, cu != nullptr) > kMostItems / kda::put4_threads((int)D) / Hk)
+    return KDA_ERR_BAD_SHAPE;
+  if (st != KDA_OK) return st;
+  if ((tok > 0 && (!k || !v)) || (k_out == nullptr) != (v_out == nullptr)) return KDA_ERR_NULL_ARG;
+  if (!row_ok(k_row, Hk, D) || !row_ok(v_row, Hk, D) || !aligned16(k) || !aligned16(v) ||
+      !aligned16(k_out) || !aligned16(v_out))
+    return KDA_ERR_BAD_LAYOUT;
+  const int64_t bk = span_bytes(tok, k_row, Hk, D), bv = span_bytes(tok, v_row, Hk, D);
+  if (bk < 0 || bv < 0) return KDA_ERR_BAD_SHAPE;
+  const int64_t bo = k_out ? tok * Hk * D * 2 : 0;
+  const Range ins[] = {make_range(k, bk), make_range(v, bv),
+                       make_range(offsets, offsets ? N * 8 : 0),
+                       make_range(slots, slots ? N * 8 : 0), make_range(cu, cu ? (N + 1) * 8 : 0)};
+  const Range outs[] = {c.r[0], c.r[1], c.r[2], c.r[3], make_range(k_out, bo),
+                        make_range(v_out, bo)};
+  for (int i = 0; i < 6; ++i)
+    if (any_overlap(outs[i], ins, 5) || any_overlap(outs[i], outs + i + 1, 5 - i))
+      return KDA_ERR_BAD_ALIAS;
+  return KDA_OK;
+}
+
+// Keys of a part when the caller leaves the choice.
+int64_t attn4_auto_part(int64_t units, int64_t cap) {
+  int64_t part = 512;
+  while (cap > 64 * part) part *= 2;
+  return cap <= 1024 ? cap : part;
+}
+
+int attn4_sizes(int64_t N, int64_t Bq, int64_t Tq, int64_t cap, int64_t Hq, int64_t Hk, int64_t D,
+                int64_t part, int* rows, int64_t* part_out) {
+  if (D != 64 && D != 128) return KDA_ERR_BAD_SHAPE;
+  if (Hk < 1 || Hq < 1 || Hq % Hk != 0 || Hq >= (1 << 24)) return KDA_ERR_BAD_SHAPE;
+  if (N < 1 || N >= ((int64_t)1 << 31) || Bq < 1 || Tq < 0) return KDA_ERR_BAD_SHAPE;
+  if (Bq != 1 && Bq != N) return KDA_ERR_BAD_VARLEN;
+  if (cap < kCache4Tile || cap % kCache4Tile != 0 || cap > ((int64_t)1 << 30))
+    return KDA_ERR_BAD_SHAPE;
+  // rows of a sequence are 32-bit numbers
+  if (Tq > ((int64_t)1 << 30) / (Hq / Hk) || Tq > ((int64_t)1 << 40) / Bq)
+    return KDA_ERR_BAD_SHAPE;
+  if (part < 0 || part % kCache4Tile != 0 || (part && (cap + part - 1) / part > 64))
+    return KDA_ERR_BAD_SCHEDULE;
+  const int64_t G = Hq / Hk, total = Bq * Tq;
+  *rows = kda::attn4_rows(total, N, G);
+  const int64_t most = kMostItems / kda::kAttnThreads;
+  const int64_t tiles = kda::attn_slots(total, N, G, *rows) + (Bq == N ? N : 0);
+  if (tiles > most / Hk) return KDA_ERR_BAD_SHAPE;
+  int64_t pt = part ? part : attn4_auto_part(tiles * Hk, cap);
+  if (pt > cap) pt = cap;
+  const int64_t parts = (cap + pt - 1) / pt;
+  if (parts > 1 && (tiles * Hk > most / parts || total > 4 * most / Hq)) {
+    if (part) return KDA_ERR_BAD_SHAPE;
+    pt = cap;
+  }
+  *part_out = pt;
+  return KDA_OK;
+}
+
+int64_t attn4_ws_bytes(int64_t total, int64_t Hq, int64_t D, int64_t cap, int64_t part) {
+  const int64_t parts = (cap + part - 1) / part;
+  return parts > 1 ? parts * total * Hq * (D + 2) * 4 : 0;
+}
+
+int attn4_check(const void* q, int64_t q_row, const void* k4, const void* ks, const void* v4,
+                const void* vs, int64_t num_slots, int64_t cap, float scale, const void* out,
+                const float* lse, const int64_t* cu_q, const int64_t* k_lens, const int64_t* slots,
+                int64_t N, int64_t Bq, int64_t Tq, int64_t Hq, int64_t Hk, int64_t D, int64_t part,
+                const void* workspace, int64_t workspace_bytes, int* rows, int64_t* part_out) {
+  int64_t pt = cap;
+  int st = attn4_sizes(N, Bq, Tq, cap, Hq, Hk, D, part, rows, &pt);
+  if (st != KDA_OK) return st;
+  if (cu_q ? Bq != 1 : Bq != N) return KDA_ERR_BAD_VARLEN;
+  if (!slots && N > num_slots) return KDA_ERR_BAD_SHAPE;
+  CacheRanges c;
+  st = cache4_check(k4, ks, v4, vs, num_slots, cap, Hk, D, &c);
+  if (st != KDA_OK) return st;
+  if (!std::isfinite(kda::attn_c(scale)) || scale < 0.f) return KDA_ERR_BAD_SCALE;
+  const int64_t nq = Bq * Tq;
+  if (nq > 0 && (!q || !out)) return KDA_ERR_NULL_ARG;
+  if (q_row >= (1 << 24)) return KDA_ERR_BAD_SHAPE;
+  if (!row_ok(q_row, Hq, D) || !aligned16(q) || !aligned16(out) || !aligned16(workspace))
+    return KDA_ERR_BAD_LAYOUT;
+  const int64_t bq = span_bytes(nq, q_row, Hq, D);
+  if (bq < 0) return KDA_ERR_BAD_SHAPE;
+  if (part == 0 && !workspace) pt = cap;  // left to the library: without one, one part
+  const int64_t need = attn4_ws_bytes(nq, Hq, D, cap, pt);
+  if (need > 0 && !workspace) return KDA_ERR_NULL_ARG;
+  if (need > workspace_bytes) return KDA_ERR_BAD_WORKSPACE;
+  const Range ins[] = {make_range(q, bq),
+                       c.r[0],
+                       c.r[1],
+                       c.r[2],
+                       c.r[3],
+                       make_range(cu_q, cu_q ? (N + 1) * 8 : 0),
+                       make_range(k_lens, k_lens ? N * 8 : 0),
+                       make_range(slots, slots ? N * 8 : 0)};
+  const Range outs[] = {make_range(out, nq * Hq * D * 2), make_range(lse, lse ? nq * Hq * 4 : 0),
+                        make_range(workspace, need)};
+  for (int i = 0; i < 3; ++i)
+    if (any_overlap(outs[i], ins, 8) || any_overlap(outs[i], outs + i + 1, 2 - i))
+      return KDA_ERR_BAD_ALIAS;
+  *part_out = pt;
+  return KDA_OK;
+}
+
+kda::Cache4 cache_of(const void* k4, const void* ks, const void* v4, const void* vs, int64_t slots,
+                     int64_t cap) {
+  auto u8 = [](const void* x) { return static_cast<uint8_t*>(const_cast<void*>(x)); };
+  return kda::Cache4{u8(k4), u8(ks), u8(v4), u8(vs), slots, cap};
+}
+
+}  // namespace
+
+extern "C" {
+
+int kda_norm_check(const void* x, int64_t x_row, const void* gate, int64_t gate_row, int gate_fn,
+                   const void* post_weight, int64_t group, const void* weight, int weight_dtype,
+                   float eps, const void* residual, const void* residual_out, int residual_dtype,
+                   float residual_scale, const void* out, int64_t R, int64_t W) {
+  return norm_check(x, x_row, gate, gate_row, gate_fn, post_weight, group, weight, weight_dtype,
+                    eps, residual, residual_out, residual_dtype, residual_scale, out, R, W);
+}
+
+int kda_norm(const void* x, int64_t x_row, const void* gate, int64_t gate_row, int gate_fn,
+             const void* post_weight, int64_t group, const void* weight, int weight_dtype,
+             float eps, const void* residual, void* residual_out, int residual_dtype,
+             float residual_scale, void* out, int64_t R, int64_t W, void* stream) {
+  const int st = norm_check(x, x_row, gate, gate_row, gate_fn, post_weight, group, weight,
+                            weight_dtype, eps, residual, residual_out, residual_dtype,
+                            residual_scale, out, R, W);
+  if (st != KDA_OK || R == 0) return st;
+  kda::NormParams p = {};
+  p.x = static_cast<const uint16_t*>(x);
+  p.gate = static_cast<const uint16_t*>(gate);
+  p.post_w = post_weight;
+  p.w = weight;
+  p.res = residual;
+  p.res_out = residual_out;
+  p.out = static_cast<uint16_t*>(out);
+  p.x_row = x_row;
+  p.gate_row = gate_row;
+  p.group = static_cast<int32_t>(post_weight ? group : 8);
+  p.pieces = 1;
+  // groups that nothing couples: pieces of a row fill the device as rows of their own
+  const int64_t piece = weight || (post_weight && group == W) ? W : kda::norm_piece(W, p.group);
+  if (W > 2048 && piece >= 512) p.pieces = static_cast<int32_t>(W / piece);
+  p.W = static_cast<int32_t>(W / p.pieces);
+  p.items = R * p.pieces;
+  p.silu = gate_fn == KDA_GATE_SILU;
+  p.w_fp32 = weight_dtype == KDA_DTYPE_FP32;
+  p.res_fp32 = residual_dtype == KDA_DTYPE_FP32;
+  p.eps = eps;
+  p.alpha = residual_scale;
+  return status(kda::launch_norm(p, static_cast<hipStream_t>(stream)));
+}
+
+int kda_rope_check(const void* q, int64_t q_row, const void* q_out, int64_t q_out_row,
+                   const void* k, int64_t k_row, const void* k_out, int64_t k_out_row,
+                   const double* freqs, int64_t rot, float amplitude, int interleaved, int inverse,
+                   const int64_t* positions, const int64_t* offsets, const int64_t* cu_seqlens,
+                   int64_t num_seqs, int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t D) {
+  (void)interleaved;
+  (void)inverse;
+  return rope_check(q, q_row, q_out, q_out_row, k, k_row, k_out, k_out_row, freqs, rot, amplitude,
+                    positions, offsets, cu_seqlens, num_seqs, B, T, Hq, Hk, D);
+}
+
+int kda_rope(const void* q, int64_t q_row, void* q_out, int64_t q_out_row, const void* k,
+             int64_t k_row, void* k_out, int64_t k_out_row, const double* freqs, int64_t rot,
+             float amplitude, int interleaved, int inverse, const int64_t* positions,
+             const int64_t* offsets, const int64_t* cu_seqlens, int64_t num_seqs, int64_t B,
+             int64_t T, int64_t Hq, int64_t Hk, int64_t D, void* stream) {
+  const int st = rope_check(q, q_row, q_out, q_out_row, k, k_row, k_out, k_out_row, freqs, rot,
+                            amplitude, positions, offsets, cu_seqlens, num_seqs, B, T, Hq, Hk, D);
+  if (st != KDA_OK || B * T == 0) return st;
+  kda::RopeParams p = {};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.k_out = static_cast<uint16_t*>(k_out);
+  p.freqs = freqs;
+  p.pos = positions;
+  p.offsets = offsets;
+  p.cu = cu_seqlens;
+  p.q_row = q_row;
+  p.k_row = k_row;
+  p.q_out_row = q_out_row;
+  p.k_out_row = k_out_row;
+  p.T = T;
+  p.tokens = B * T;
+  p.N = static_cast<int32_t>(num_seqs);
+  p.Hq = static_cast<int32_t>(Hq);
+  p.Hk = static_cast<int32_t>(Hk);
+  p.D = static_cast<int32_t>(D);
+  p.rot = static_cast<int32_t>(rot);
+  p.q_copy = q != q_out;
+  p.k_copy = k != k_out;
+  p.interleaved = interleaved != 0;
+  p.amplitude = amplitude;
+  p.sign = inverse ? -1.f : 1.f;
+  kda::rope_schedule(p);
+  return status(kda::launch_rope(p, static_cast<hipStream_t>(stream)));
+}
+
+int kda_cache4_put_check(const void* k, int64_t k_row, const void* v, int64_t v_row,
+                         const void* k4, const void* ks, const void* v4, const void* vs,
+                         int64_t num_slots, int64_t cap, const void* k_out, const void* v_out,
+                         const int64_t* offsets, const int64_t* slots, const int64_t* cu_seqlens,
+                         int64_t num_seqs, int64_t B, int64_t T, int64_t Hk, int64_t D) {
+  return put4_check(k, k_row, v, v_row, k4, ks, v4, vs, num_slots, cap, k_out, v_out, offsets,
+                    slots, cu_seqlens, num_seqs, B, T, Hk, D);
+}
+
+int kda_cache4_put(const void* k, int64_t k_row, const void* v, int64_t v_row, void* k4, void* ks,
+                   void* v4, void* vs, int64_t num_slots, int64_t cap, void* k_out, void* v_out,
+                   const int64_t* offsets, const int64_t* slots, const int64_t* cu_seqlens,
+                   int64_t num_seqs, int64_t B, int64_t T, int64_t Hk, int64_t D, void* stream) {
+  const int st = put4_check(k, k_row, v, v_row, k4, ks, v4, vs, num_slots, cap, k_out, v_out,
+                            offsets, slots, cu_seqlens, num_seqs, B, T, Hk, D);
+  if (st != KDA_OK || B * T == 0) return st;
+  kda::Put4Params p = {};
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.c = cache_of(k4, ks, v4, vs, num_slots, cap);
+  p.k_out = static_cast<uint16_t*>(k_out);
+  p.v_out = static_cast<uint16_t*>(v_out);
+  p.offsets = offsets;
+  p.slot = slots;
+  p.cu = cu_seqlens;
+  p.k_row = k_row;
+  p.v_row = v_row;
+  p.T = T;
+  p.tokens = B * T;
+  p.N = static_cast<int32_t>(num_seqs);
+  p.Hk = static_cast<int32_t>(Hk);
+  return status(kda::launch_put4(p, static_cast<int>(D), static_cast<hipStream_t>(stream)));
+}
+
+int64_t kda_attn4_workspace_bytes(int64_t num_seqs, int64_t Bq, int64_t Tq, int64_t cap,
+                                  int64_t Hq, int64_t Hk, int64_t D, int64_t part) {
+  int rows = 0;
+  int64_t pt = 0;
+  const int st = attn4_sizes(num_seqs, Bq, Tq, cap, Hq, Hk, D, part, &rows, &pt);
+  return st != KDA_OK ? st : attn4_ws_bytes(Bq * Tq, Hq, D, cap, pt);
+}
+
+int kda_attn4_fwd_check(const void* q, int64_t q_row, const void* k4, const void* ks,
+                        const void* v4, const void* vs, int64_t num_slots, int64_t cap,
+                        float scale, const void* out, const float* lse,
+                        const int64_t* cu_seqlens_q, const int64_t* k_lens, const int64_t* slots,
+                        int64_t num_seqs, int64_t Bq, int64_t Tq, int64_t Hq, int64_t Hk,
+                        int64_t D, int64_t part, const void* workspace, int64_t workspace_bytes) {
+  int rows = 0;
+  int64_t pt = 0;
+  return attn4_check(q, q_row, k4, ks, v4, vs, num_slots, cap, scale, out, lse, cu_seqlens_q,
+                     k_lens, slots, num_seqs, Bq, Tq, Hq, Hk, D, part, workspace, workspace_bytes,
+                     &rows, &pt);
+}
+
+int kda_attn4_fwd(const void* q, int64_t q_row, const void* k4, const void* ks, const void* v4,
+                  const void* vs, int64_t num_slots, int64_t cap, float scale, void* out,
+                  float* lse, const int64_t* cu_seqlens_q, const int64_t* k_lens,
+                  const int64_t* slots, int64_t num_seqs, int64_t Bq, int64_t Tq, int64_t Hq,
+                  int64_t Hk, int64_t D, int64_t part, void* workspace, int64_t workspace_bytes,
+                  void* stream) {
+  int rows = 0;
+  int64_t pt = 0;
+  const int st = attn4_check(q, q_row, k4, ks, v4, vs, num_slots, cap, scale, out, lse,
+                             cu_seqlens_q, k_lens, slots, num_seqs, Bq, Tq, Hq, Hk, D, part,
+                             workspace, workspace_bytes, &rows, &pt);
+  if (st != KDA_OK || Bq * Tq == 0) return st;
+  kda::Attn4Params p = {};
+  kda::AttnParams& a = p.a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.cu_q = cu_seqlens_q;
+  a.k_lens = k_lens;
+  a.q_row = q_row;
+  a.Tq = Tq;
+  a.Tk = cap;
+  a.Tq_total = Bq * Tq;
+  a.N = static_cast<int32_t>(num_seqs);
+  a.Hq = static_cast<int32_t>(Hq);
+  a.Hk = static_cast<int32_t>(Hk);
+  a.G = static_cast<int32_t>(Hq / Hk);
+  a.c = kda::attn_factor(scale);
+  a.splits = static_cast<int32_t>((cap + pt - 1) / pt);
+  a.ws_o = static_cast<float*>(workspace);
+  a.ws_ml = a.splits > 1 ? a.ws_o + a.splits * a.Tq_total * Hq * D : nullptr;
+  p.c = cache_of(k4, ks, v4, vs, num_slots, cap);
+  p.slot = slots;
+  p.part = static_cast<int32_t>(pt / kCache4Tile);
+  return status(
+      kda::launch_attn4(p, rows, static_cast<int>(D), static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

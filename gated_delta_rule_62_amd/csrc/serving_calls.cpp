@@ -319,6 +319,210 @@ PyObject* attn_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// Address and row stride of a bf16 tensor [..., W] whose rows lie one stride apart.
+Rows flat_rows(const char* name, PyObject* o, at::IntArrayRef shape, int dev) {
+  const at::Tensor& t = unpack(name, o);
+  if (t.scalar_type() != bf16 || t.sizes() != shape) {
+    std::ostringstream s;
+    s << name << " must be " << bf16 << " " << shape << ", got " << t.scalar_type() << " "
+      << t.sizes();
+    fail(s.str());
+  }
+  if (!t.is_cuda() || t.get_device() != dev) fail("every tensor must live on the same GPU");
+  const int64_t dims = t.dim(), W = t.size(dims - 1);
+  int64_t row = W;
+  if (!t.is_contiguous()) {
+    bool ok = t.stride(dims - 1) == 1 || W == 1;
+    int64_t rows = 1;  // of the dimensions behind this one
+    for (int64_t d = dims - 2; d >= 0; --d) {
+      if (t.size(d) == 1) continue;
+      if (rows == 1) row = t.stride(d);
+      ok = ok && t.stride(d) == rows * row;
+      rows *= t.size(d);
+    }
+    if (!ok) fail(std::string(name) + " must have its rows one stride apart");
+  }
+  return Rows{t.data_ptr(), row};
+}
+// Address of a contiguous tensor of one of two dtypes.
+void* either(const char* name, PyObject* o, at::IntArrayRef shape, int dev, int* dtype) {
+  const at::Tensor& t = unpack(name, o);
+  const at::ScalarType d = t.scalar_type();
+  if ((d != bf16 && d != fp32) || t.sizes() != shape) {
+    std::ostringstream s;
+    s << name << " must be " << bf16 << " or " << fp32 << " " << shape << ", got " << d << " "
+      << t.sizes();
+    fail(s.str());
+  }
+  if (!t.is_cuda() || t.get_device() != dev) fail("every tensor must live on the same GPU");
+  if (!t.is_contiguous()) fail(std::string(name) + " must be contiguous");
+  *dtype = d == fp32 ? KDA_DTYPE_FP32 : KDA_DTYPE_BF16;
+  return t.data_ptr();
+}
+bool truth(PyObject* o) {
+  const int x = PyObject_IsTrue(o);
+  if (x < 0) throw Raise{nullptr, ""};
+  return x != 0;
+}
+
+PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 12, [&]() -> int64_t {
+    const auto fn = function<decltype(&kda_norm)>(a[0]);
+    const at::Tensor& tx = unpack("x", a[1]);
+    if (tx.dim() < 1) fail("x must be [..,W]");
+    const at::IntArrayRef shape = tx.sizes();
+    const int64_t W = shape.back();
+    int64_t R = 1;
+    for (size_t d = 0; d + 1 < shape.size(); ++d) R *= shape[d];
+    const int dev = gpu_of(tx);
+    const Rows x = flat_rows("x", a[1], shape, dev);
+    void* out = nullptr;
+    if (a[2] != Py_None) {
+      const at::Tensor& t = unpack("out", a[2]);
+      if (t.scalar_type() != bf16) fail("out must be bfloat16");
+      int dtype;
+      out = either("out", a[2], shape, dev, &dtype);
+    }
+    int wd = KDA_DTYPE_BF16, pd = KDA_DTYPE_BF16, rd = KDA_DTYPE_BF16, hd = KDA_DTYPE_BF16;
+    const void *w = nullptr, *post = nullptr, *res = nullptr;
+    void* res_out = nullptr;
+    int64_t group = W;
+    if (a[3] != Py_None) w = either("weight", a[3], {W}, dev, &wd);
+    const float eps = number(a[4]);
+    if (a[5] != Py_None) {
+      group = with_dims("post_weight", a[5], 1, "post_weight must be [G]").numel();
+      post = either("post_weight", a[5], {group}, dev, &pd);
+      if (w == nullptr) wd = pd;
+      else if (wd != pd) fail("weight and post_weight must have one dtype");
+    }
+    Rows gate{nullptr, W};
+    if (a[6] != Py_None) gate = flat_rows("gate", a[6], shape, dev);
+    const char* act = PyUnicode_Check(a[7]) ? PyUnicode_AsUTF8(a[7]) : "";
+    if (act == nullptr) throw Raise{nullptr, ""};
+    const std::string kind = act;
+    if (kind != "sigmoid" && kind != "silu") fail("gate_fn must be 'sigmoid' or 'silu'");
+    if (a[8] != Py_None) res = either("residual", a[8], shape, dev, &rd);
+    if (a[9] != Py_None) res_out = either("residual_out", a[9], shape, dev, &hd);
+    if (res && res_out && rd != hd) fail("residual and residual_out must have one dtype");
+    if (!res != !res_out) fail("residual and residual_out come together");
+    const float alpha = number(a[10]);
+    void* stream = stream_of(a[11], dev);
+    Device current(dev);
+    return without_gil([&] {
+      return fn(x.at, x.row, gate.at, gate.row,
+                kind == "silu" ? KDA_GATE_SILU : KDA_GATE_SIGMOID, post, group, w, wd, eps, res,
+                res_out, rd, alpha, out, R, W, stream);
+    });
+  });
+}
+
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 13, [&]() -> int64_t {
+    const auto fn = function<decltype(&kda_rope)>(a[0]);
+    const at::Tensor& tq = with_dims("q", a[1], 4, "q must be [B,T,heads,D]");
+    const int64_t B = tq.size(0), T = tq.size(1), Hq = tq.size(2), D = tq.size(3);
+    const int dev = gpu_of(tq);
+    const Rows q = rows("q", a[1], {B, T, Hq, D}, dev);
+    const double* freqs;
+    const int64_t half = with_dims("freqs", a[3], 1, "freqs must be [rot/2]").numel();
+    freqs = tensor<double>("freqs", a[3], at::kDouble, {half}, dev);
+    const Rows q_out = rows("q_out", a[4], {B, T, Hq, D}, dev);
+    Rows k{nullptr, 0}, k_out{nullptr, 0};
+    int64_t Hk = 0;
+    if ((a[2] == Py_None) != (a[5] == Py_None)) fail("k and k_out come together");
+    if (a[2] != Py_None) {
+      Hk = with_dims("k", a[2], 4, "k must be [B,T,heads,D]").size(2);
+      if (Hk < 1) fail("k must have heads");
+      k = rows("k", a[2], {B, T, Hk, D}, dev);
+      k_out = rows("k_out", a[5], {B, T, Hk, D}, dev);
+    }
+    const int64_t N = a[8] == Py_None ? B : unpack("cu_seqlens", a[8]).numel() - 1;
+    const int64_t *pos = optional<int64_t>("positions", a[6], int64, {B, T}, dev),
+                  *off = optional<int64_t>("offsets", a[7], int64, {N}, dev),
+                  *cu = optional<int64_t>("cu_seqlens", a[8], int64, {N + 1}, dev);
+    const bool inter = truth(a[9]);
+    const float amplitude = number(a[10]);
+    const bool inverse = truth(a[11]);
+    void* stream = stream_of(a[12], dev);
+    Device current(dev);
+    return without_gil([&] {
+      return fn(q.at, q.row, q_out.at, q_out.row, k.at, k.row, k_out.at, k_out.row, freqs,
+                2 * half, amplitude, inter, inverse, pos, off, cu, N, B, T, Hq, Hk, D, stream);
+    });
+  });
+}
+
+// The tensors k4, ks, v4, vs from o on, [slots, Hk, cap, D / 2] the first.
+struct Caches {
+  void *k4, *ks, *v4, *vs;
+  int64_t slots, cap;
+};
+Caches caches(PyObject* const* o, int64_t Hk, int64_t D, int dev) {
+  const at::Tensor& t = with_dims("k4", o[0], 4, "k4 must be [slots,Hk,capacity,D/2]");
+  const int64_t S = t.size(0), cap = t.size(2), tiles = cap / 32;
+  return Caches{tensor("k4", o[0], at::kByte, {S, Hk, cap, D / 2}, dev),
+                tensor("ks", o[1], at::kByte, {S, Hk, tiles, D / 32, 32}, dev),
+                tensor("v4", o[2], at::kByte, {S, Hk, tiles, 16 * D}, dev),
+                tensor("vs", o[3], at::kByte, {S, Hk, tiles, D / 32, 32}, dev),
+                S,
+                cap};
+}
+
+PyObject* put4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 13, [&]() -> int64_t {
+    const auto fn = function<decltype(&kda_cache4_put)>(a[0]);
+    const at::Tensor& tk = with_dims("k", a[1], 4, "k must be [B,T,heads,D]");
+    const int64_t B = tk.size(0), T = tk.size(1), Hk = tk.size(2), D = tk.size(3);
+    const int dev = gpu_of(tk);
+    const Rows k = rows("k", a[1], {B, T, Hk, D}, dev), v = rows("v", a[2], {B, T, Hk, D}, dev);
+    const Caches c = caches(a + 3, Hk, D, dev);
+    const int64_t N = a[8] == Py_None ? B : unpack("cu_seqlens", a[8]).numel() - 1;
+    const int64_t *off = optional<int64_t>("offsets", a[7], int64, {N}, dev),
+                  *cu = optional<int64_t>("cu_seqlens", a[8], int64, {N + 1}, dev),
+                  *slots = optional<int64_t>("slots", a[9], int64, {N}, dev);
+    if ((a[10] == Py_None) != (a[11] == Py_None)) fail("k_out and v_out come together");
+    void *k_out = optional("k_out", a[10], bf16, {B, T, Hk, D}, dev),
+         *v_out = optional("v_out", a[11], bf16, {B, T, Hk, D}, dev);
+    void* stream = stream_of(a[12], dev);
+    Device current(dev);
+    return without_gil([&] {
+      return fn(k.at, k.row, v.at, v.row, c.k4, c.ks, c.v4, c.vs, c.slots, c.cap, k_out, v_out,
+                off, slots, cu, N, B, T, Hk, D, stream);
+    });
+  });
+}
+
+PyObject* attn4_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 16, [&]() -> int64_t {
+    const auto fn = function<decltype(&kda_attn4_fwd)>(a[0]);
+    const auto ws_bytes = function<decltype(&kda_attn4_workspace_bytes)>(a[1]);
+    const at::Tensor &tq = with_dims("q", a[2], 4, "q must be [B,T,heads,D]"),
+                     &tk = with_dims("k4", a[3], 4, "k4 must be [slots,Hk,capacity,D/2]");
+    const int64_t Bq = tq.size(0), Tq = tq.size(1), Hq = tq.size(2), D = tq.size(3),
+                  Hk = tk.size(1);
+    const int dev = gpu_of(tq);
+    const Rows q = rows("q", a[2], {Bq, Tq, Hq, D}, dev);
+    const Caches c = caches(a + 3, Hk, D, dev);
+    const float scale = number(a[7]);
+    void* out = tensor("out", a[8], bf16, {Bq, Tq, Hq, D}, dev);
+    float* lse = optional<float>("lse", a[9], fp32, {Bq, Tq, Hq}, dev);
+    const int64_t N = a[11] == Py_None ? Bq : unpack("cu_seqlens_q", a[11]).numel() - 1;
+    const int64_t *k_lens = optional<int64_t>("k_lens", a[10], int64, {N}, dev),
+                  *cu = optional<int64_t>("cu_seqlens_q", a[11], int64, {N + 1}, dev),
+                  *slots = optional<int64_t>("slots", a[12], int64, {N}, dev);
+    const int64_t part = integer(a[13]);
+    void* stream = stream_of(a[15], dev);
+    Device current(dev);
+    const Workspace w =
+        workspace_of(a[14], ws_bytes(N, Bq, Tq, c.cap, Hq, Hk, D, part), dev);
+    if (w.want) return w.want;
+    return without_gil([&] {
+      return fn(q.at, q.row, c.k4, c.ks, c.v4, c.vs, c.slots, c.cap, scale, out, lse, cu, k_lens,
+                slots, N, Bq, Tq, Hq, Hk, D, part, w.at, w.bytes, stream);
+    });
+  });
+}
+
 PyCFunction fast(PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
 }
@@ -329,6 +533,10 @@ PyMethodDef methods[] = {
      "kda_la_fwd: its and its workspace function's address, arguments -> status, or the bytes "
      "of the workspace it wants."},
     {"attn_fwd", fast(attn_fwd), METH_FASTCALL, "The same for kda_attn_fwd."},
+    {"norm", fast(norm), METH_FASTCALL, "kda_norm: its address and arguments -> status."},
+    {"rope", fast(rope), METH_FASTCALL, "kda_rope: its address and arguments -> status."},
+    {"put4", fast(put4), METH_FASTCALL, "kda_cache4_put: its address and arguments -> status."},
+    {"attn4_fwd", fast(attn4_fwd), METH_FASTCALL, "As attn_fwd for kda_attn4_fwd."},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving_calls", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

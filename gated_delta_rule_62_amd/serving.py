@@ -1,5 +1,6 @@
 """Bindings of the serving operators: the single-token recurrences on pooled states, linear
-attention with one decay per head, and causal softmax attention with grouped heads.
+attention with one decay per head, causal softmax attention with grouped heads, and what layers
+call around them: norms with gate and residual, rotary positions, caches in 4 bits.
 
 Like the package's other bindings they check dtypes, shapes, devices and strides, pass raw
 pointers, sizes and torch's current stream to the C ABI declared in ``include/kda.h`` (both
@@ -7,6 +8,8 @@ in a compiled module, ``csrc/serving_calls.cpp``), and turn status codes into ex
 every computation runs in the library's kernels.
 """
 from __future__ import annotations
+
+import math
 
 import torch
 
@@ -124,5 +127,129 @@ def kda_attn_fwd(q, k, v, scale, out, lse=None, cu_seqlens_q=None, cu_seqlens_k=
     st = _calls.attn_fwd(*args, workspace, stream)
     if st > 0:  # the bytes it wants
         st = _calls.attn_fwd(*args, _workspace(st, q, stream), stream)
+    if st != 0:
+        raise KdaError(st)
+
+
+def kda_norm(x, out=None, weight=None, eps: float = 1e-6, post_weight=None, gate=None,
+             gate_fn: str = "sigmoid", residual=None, residual_out=None,
+             residual_scale: float = 1.0, stream=None) -> None:
+    """The norms before and after a block, with its gate and the residual sum, in one pass over
+    the rows (asynchronous on ``stream``); every part is optional:
+    ``u = rms_norm(x, groups) post_weight``, ``u = u act(gate)``,
+    ``h = residual + residual_scale u`` (written to residual_out),
+    ``out = rms_norm(h) weight``; without ``weight`` out is h.
+
+    x, gate: bf16 ``[..,W]`` (views whose rows lie one stride apart are taken as they are);
+    post_weight: ``[G]``, norms over groups of G channels (G: W, or 32, 64, 128, 256 or 512);
+    weight: ``[W]``; both bf16 or both fp32; gate_fn: "sigmoid" or "silu"; residual and
+    residual_out: bf16 or fp32 ``[..,W]``, possibly the same tensor; out: bf16 ``[..,W]``, which
+    may be left out with a residual and without a weight.
+    """
+    st = _calls.norm(load_library().kda_norm_at, x, out, weight, eps, post_weight, gate, gate_fn,
+                     residual, residual_out, residual_scale, stream)
+    if st != 0:
+        raise KdaError(st)
+
+
+def kda_rope_freqs(rot: int, base: float = 10000.0, method: str = "", factor: float = 1.0,
+                   original: int = 4096, slow: float = 1.0, fast: float = 32.0, device="cuda"):
+    """Frequencies for ``kda_rope``, fp64 ``[rot/2]``, and its amplitude.
+
+    method "": powers of the base.  "linear": positions interpolated, every frequency divided by
+    factor.  "yarn": a pair that turns at most ``slow`` times over the ``original`` context is
+    interpolated, one that turns ``fast`` times or more is kept, linearly blended between, and
+    the amplitude is ``0.1 ln(factor) + 1`` (1 for a factor of at most 1).
+    """
+    if rot < 2 or rot % 2 or not base > 0 or not factor > 0 or not fast > slow:
+        raise ValueError("rot must be even and positive, base and factor positive, fast above slow")
+    f = float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    amplitude = 1.0
+    if method == "linear":
+        f = f / factor
+    elif method == "yarn":
+        keep = ((original * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        f = f * keep + f / factor * (1 - keep)
+        amplitude = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    elif method:
+        raise ValueError("method must be '', 'linear' or 'yarn'")
+    return f.to(device), amplitude
+
+
+def kda_rope(q, k, freqs, q_out, k_out, positions=None, offsets=None, cu_seqlens=None,
+             interleaved: bool = False, amplitude: float = 1.0, inverse: bool = False,
+             stream=None) -> None:
+    """Rotary positions of queries and keys (asynchronous on ``stream``): pairs of a head's first
+    ``2 len(freqs)`` channels are turned by position times frequency, the rest is copied.
+
+    q, q_out: bf16 ``[B,T,Hq,D]``, k, k_out: bf16 ``[B,T,Hk,D]`` or both None; views with one row
+    stride are taken as they are, and an output may be its input.  freqs: fp64 ``[rot/2]`` radians
+    per position (``kda_rope_freqs``).  Positions: int64 ``[B,T]``, or ``offsets[n] + t`` for
+    token t of sequence n (int64 ``[N]``; None: 0), sequences packed (``cu_seqlens`` int64
+    ``[N+1]``, B == 1) or batch rows.  ``interleaved``: pairs ``(2i, 2i+1)`` instead of
+    ``(i, i + rot/2)``; ``amplitude`` multiplies the turned channels; ``inverse`` turns back.
+    """
+    st = _calls.rope(load_library().kda_rope_at, q, k, freqs, q_out, k_out, positions, offsets,
+                     cu_seqlens, interleaved, amplitude, inverse, stream)
+    if st != 0:
+        raise KdaError(st)
+
+
+def kda_cache4_empty(slots: int, heads: int, capacity: int, D: int, device="cuda"):
+    """An empty cache in 4 bits for ``kda_cache4_put`` and ``kda_attn4_fwd``: the tensors k4, ks,
+    v4, vs (uint8; ``include/kda.h`` says what is where) for ``slots`` requests of up to
+    ``capacity`` positions (a multiple of 32)."""
+    if capacity % 32 or D not in (64, 128):
+        raise ValueError("capacity must be a multiple of 32 and D 64 or 128")
+    tiles = capacity // 32
+    shapes = ((slots, heads, capacity, D // 2), (slots, heads, tiles, D // 32, 32),
+              (slots, heads, tiles, 16 * D), (slots, heads, tiles, D // 32, 32))
+    return tuple(torch.zeros(s, dtype=torch.uint8, device=device) for s in shapes)
+
+
+def kda_cache4_put(k, v, k4, ks, v4, vs, offsets=None, cu_seqlens=None, slots=None, k_out=None,
+                   v_out=None, stream=None) -> None:
+    """New keys and values into caches in 4 bits (asynchronous on ``stream``): token t of sequence
+    n goes to position ``offsets[n] + t`` of slot ``slots[n]``.
+
+    k, v: bf16 ``[B,T,Hk,D]`` (views with one row stride are taken as they are); k4, ks, v4, vs: as
+    ``kda_cache4_empty`` makes them, updated in place; offsets: int64 ``[N]`` (None: 0); slots:
+    int64 ``[N]`` (None: n); cu_seqlens as for ``kda_fwd``.  k_out, v_out: bf16 ``[B,T,Hk,D]`` for
+    the values that the cache then stands for, or both None.  Positions outside the capacity and
+    slots outside the cache are not stored.
+    """
+    st = _calls.put4(load_library().kda_cache4_put_at, k, v, k4, ks, v4, vs, offsets, cu_seqlens,
+                     slots, k_out, v_out, stream)
+    if st != 0:
+        raise KdaError(st)
+
+
+def kda_attn4_workspace_bytes(num_seqs: int, Bq: int, Tq: int, capacity: int, Hq: int, Hk: int,
+                              D: int, part: int = 0) -> int:
+    """Bytes of the workspace of ``kda_attn4_fwd`` (0: this call needs none)."""
+    n = load_library().kda_attn4_workspace_bytes(int(num_seqs), int(Bq), int(Tq), int(capacity),
+                                                 int(Hq), int(Hk), int(D), int(part))
+    if n < 0:
+        raise KdaError(int(n))
+    return int(n)
+
+
+def kda_attn4_fwd(q, k4, ks, v4, vs, scale, out, lse=None, k_lens=None, cu_seqlens_q=None,
+                  slots=None, part: int = 0, workspace=None, stream=None) -> None:
+    """``kda_attn_fwd`` over caches in 4 bits (asynchronous on ``stream``): sequence n's keys are
+    the first ``k_lens[n]`` positions (int64 ``[N]``; None: all) of slot ``slots[n]`` (int64
+    ``[N]``; None: n), its queries the last of them.
+
+    q, scale, out, lse, cu_seqlens_q: as for ``kda_attn_fwd``; k4, ks, v4, vs: as for
+    ``kda_cache4_put``, D 64 or 128.  ``part``: 0 (automatic) or keys per part, a multiple of 32;
+    ``workspace``: a uint8 tensor of at least ``kda_attn4_workspace_bytes(...)`` bytes for this
+    call alone; None takes one from torch's allocator where the call needs it.
+    """
+    lib = load_library()
+    args = (lib.kda_attn4_fwd_at, lib.kda_attn4_workspace_bytes_at, q, k4, ks, v4, vs, scale, out,
+            lse, k_lens, cu_seqlens_q, slots, part)
+    st = _calls.attn4_fwd(*args, workspace, stream)
+    if st > 0:  # the bytes it wants
+        st = _calls.attn4_fwd(*args, _workspace(st, q, stream), stream)
     if st != 0:
         raise KdaError(st)

@@ -56,7 +56,8 @@ extern "C" {
                                      /* tensor of more than 2^62 bytes, or a launch of    */
                                      /* more than 2^32 - 1 work-items (workgroups times   */
                                      /* their 128 to 768 threads)                         */
-#define KDA_ERR_BAD_DTYPE (-3)       /* unknown state dtype code                         */
+#define KDA_ERR_BAD_DTYPE (-3)       /* unknown state, weight or residual dtype, or gate */
+                                     /* function code                                    */
 #define KDA_ERR_BAD_VARLEN (-4)      /* cu_seqlens with B != 1, num_seqs < 1, or         */
                                      /* num_seqs != B without cu_seqlens                 */
 #define KDA_ERR_BAD_ALIAS (-5)       /* an output overlaps an input or the other output; */
@@ -74,9 +75,12 @@ extern "C" {
                                      /* not a multiple of 16 bytes, or a row stride is   */
                                      /* shorter than the row                             */
 
-/* State dtype codes (initial_state_dtype, final_state_dtype). */
+/* State dtype codes (initial_state_dtype, final_state_dtype); kda_norm's weights and residual. */
 #define KDA_DTYPE_BF16 0
 #define KDA_DTYPE_FP32 1
+/* kda_norm's gate functions. */
+#define KDA_GATE_SIGMOID 0
+#define KDA_GATE_SILU 1
 
 /*
  * kda_fwd -- the prefill forward (FlashKDA `fwd` contract: q, k, v, g, beta,
@@ -535,6 +539,170 @@ int kda_attn_fwd_check(const void* q, int64_t q_row, const void* k, int64_t k_ro
  */
 int64_t kda_attn_workspace_bytes(int64_t num_seqs, int64_t Bq, int64_t Tq, int64_t Bk, int64_t Tk,
                                  int64_t Hq, int64_t Hk, int64_t D, int64_t splits);
+
+/* ------------------------------------------------------------------------------
+ * What such layers call around their attention and recurrences: norms with the block's gate and
+ * the residual sum, rotary positions, and caches of keys and values in 4 bits with the attention
+ * that reads them.  The conventions of the serving operators apply.
+ * ------------------------------------------------------------------------------ */
+
+/*
+ * kda_norm -- the norms before and after a block, with its gate, the residual sum and its
+ * scale, in one pass over the rows.  For each row of W channels, every part optional:
+ *
+ *     u = x
+ *     u = u / sqrt(mean(u^2) + eps) post_weight        over each group of `group` channels
+ *     u = u sigmoid(gate), or u gate sigmoid(gate)
+ *     h = residual + residual_scale u                  -> residual_out     (without one h = u)
+ *     out = h / sqrt(mean(h^2) + eps) weight           over the row        (without one out = h)
+ *
+ *   x              bf16 [R, W], row stride x_row.
+ *   gate           bf16 [R, W], row stride gate_row, or NULL; gate_fn KDA_GATE_SIGMOID or
+ *                  KDA_GATE_SILU (KDA_ERR_BAD_DTYPE).
+ *   post_weight    [group] of weight_dtype, or NULL.  group: W, or 32, 64, 128, 256 or 512 and a
+ *                  divisor of W (KDA_ERR_BAD_SHAPE): a head's output norm shares its weights
+ *                  among the heads.
+ *   weight         [W] of weight_dtype, or NULL.
+ *   eps            finite, not negative (KDA_ERR_BAD_SCALE).
+ *   residual, residual_out  [R, W] of residual_dtype, contiguous, both or neither
+ *                  (KDA_ERR_NULL_ARG).  They may be exactly the same allocation (in place).
+ *   residual_scale finite.
+ *   out            bf16 [R, W], contiguous; may be NULL with a residual and without a weight.
+ *   R, W           rows (0: nothing is done); W a multiple of 8, 8 .. 16384.  R below
+ *                  2^32 / 4096 (KDA_ERR_BAD_SHAPE).
+ * At least one of post_weight, gate, weight and residual (KDA_ERR_NULL_ARG).
+ * Everything between loads and stores is fp32; the second norm takes h before residual_out is
+ * rounded.  Squares and their sums are fp32: a group's L2 norm stays below 1.8e19, and values
+ * whose squares underflow count as zero beside eps.  One kernel on `stream`.
+ */
+int kda_norm(const void* x, int64_t x_row, const void* gate, int64_t gate_row, int gate_fn,
+             const void* post_weight, int64_t group, const void* weight, int weight_dtype,
+             float eps, const void* residual, void* residual_out, int residual_dtype,
+             float residual_scale, void* out, int64_t R, int64_t W, void* stream);
+int kda_norm_check(const void* x, int64_t x_row, const void* gate, int64_t gate_row, int gate_fn,
+                   const void* post_weight, int64_t group, const void* weight, int weight_dtype,
+                   float eps, const void* residual, const void* residual_out, int residual_dtype,
+                   float residual_scale, const void* out, int64_t R, int64_t W);
+
+/*
+ * kda_rope -- rotary positions of queries and keys: each pair (a, b) of a head's first rot
+ * channels is turned by position times the pair's frequency,
+ *
+ *     (a, b) -> amplitude (a cos - b sin, a sin + b cos),
+ *
+ * the channels behind rot stay as they are.  inverse turns back (the gradient of the turn, or a
+ * key on its way to another position).
+ *   q, q_out       bf16 [B, T, Hq, D], row strides q_row, q_out_row.  In place where pointer and
+ *                  row stride are the same; any other shared byte is refused
+ *                  (KDA_ERR_BAD_ALIAS).  Rows of one stride in other columns of the same wider
+ *                  rows, as of one projection, share none.
+ *   k, k_out       the same with Hk heads; Hk 0 (NULL): queries alone.
+ *   freqs          float64 [rot / 2], radians per position: plain powers of a base, or scaled for
+ *                  long contexts.  Their product with the position is formed and reduced to a
+ *                  turn in 64 bits, its sine and cosine and the products are fp32.
+ *   rot            even, 2 .. D (KDA_ERR_BAD_SHAPE).  D a multiple of 8, up to 1024.
+ *   amplitude      finite (KDA_ERR_BAD_SCALE); of the turned channels only.
+ *   interleaved    0: pairs (i, i + rot / 2); else pairs (2 i, 2 i + 1).
+ *   positions      int64 [B, T] device array, or NULL: token t of sequence n is at position
+ *                  offsets[n] + t (int64 [num_seqs], NULL: 0), sequences as for kda_fwd
+ *                  (cu_seqlens, num_seqs, B, T).  positions exclude the other two
+ *                  (KDA_ERR_BAD_VARLEN).  Tokens outside every sequence keep their outputs.
+ *   B * T          below 2^24 (KDA_ERR_BAD_SHAPE).
+ * One kernel on `stream`.
+ */
+int kda_rope(const void* q, int64_t q_row, void* q_out, int64_t q_out_row, const void* k,
+             int64_t k_row, void* k_out, int64_t k_out_row, const double* freqs, int64_t rot,
+             float amplitude, int interleaved, int inverse, const int64_t* positions,
+             const int64_t* offsets, const int64_t* cu_seqlens, int64_t num_seqs, int64_t B,
+             int64_t T, int64_t Hq, int64_t Hk, int64_t D, void* stream);
+int kda_rope_check(const void* q, int64_t q_row, const void* q_out, int64_t q_out_row,
+                   const void* k, int64_t k_row, const void* k_out, int64_t k_out_row,
+                   const double* freqs, int64_t rot, float amplitude, int interleaved, int inverse,
+                   const int64_t* positions, const int64_t* offsets, const int64_t* cu_seqlens,
+                   int64_t num_seqs, int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t D);
+
+/*
+ * Caches in 4 bits.  A block of 32 channels of one token and head shares a power of two 2^e and
+ * holds a code for each value: bit 3 the sign, bits 0-2 the magnitude 0, .5, 1, 1.5, 2, 3, 4 or 6
+ * (the two-bit-exponent format with a scale per block of 32 that the device converts in
+ * hardware).  The scale's byte is e + 127; 255 says that the block held an infinity or NaN, and
+ * stands for NaN.  A cache has num_slots slots of Hk heads of cap positions, cap a multiple of 32:
+ *   k4             uint8 [num_slots, Hk, cap, D / 2]: two codes a byte, the even channel's low.
+ *   v4             uint8 [num_slots, Hk, cap / 32, 16 D]: tiles of 32 positions.  Position
+ *                  16 j + 4 i + g of a tile (j < 2, i < 4, g < 4), channel d, two channels a byte:
+ *                    D 128: byte 1024 j + 256 g + 16 (d / 8) + 4 i + d % 8 / 2,
+ *                    D  64: byte 256 g + 16 (d / 4) + 8 j + 2 i + d % 4 / 2.
+ *   ks, vs         uint8 [num_slots, Hk, cap / 32, D / 32, 32]: the scales of the tile's positions
+ *                  for each block of channels, position 16 j + 4 i + g at 8 g + 2 i + j.
+ * (These places are those of the matrix products' operands, so that kda_attn4_fwd loads 16
+ * bytes a lane and passes nothing through LDS.)  D in {64, 128}; cap up to 2^30.  A slot is
+ * contiguous in all four: copying it copies the cache of a request.
+ *
+ * kda_cache4_put -- new keys and values into such caches: token t of sequence n goes to
+ * position offsets[n] + t of slot slots[n].  2^e is the smallest power with
+ * max |x| <= 6 2^e over the block (not below 2^-127), a value takes the nearest code of x / 2^e,
+ * of two the even one; nothing saturates, and every step is exact.
+ *   k, v           bf16 [B, T, Hk, D], row strides k_row, v_row.
+ *   k_out, v_out   bf16 [B, T, Hk, D], contiguous, or both NULL: what the codes stand for, for
+ *                  attention over the prompt itself with the same keys as later tokens see.  (A
+ *                  magnitude from 1.75 2^127 on rounds to infinity.)
+ *   offsets        int64 [num_seqs] device array, NULL: 0.  Positions outside [0, cap) are not
+ *                  stored (k_out and v_out are).
+ *   slots          int64 [num_seqs] device array, NULL: n (num_seqs <= num_slots).  Sequences with
+ *                  an index outside [0, num_slots) are not stored.  A slot must not be named by
+ *                  two sequences whose positions meet.
+ *   cu_seqlens, num_seqs, B, T  as for kda_fwd; tokens outside every sequence are left out.
+ * Other positions keep what they hold.  One kernel on `stream`.
+ */
+int kda_cache4_put(const void* k, int64_t k_row, const void* v, int64_t v_row, void* k4, void* ks,
+                   void* v4, void* vs, int64_t num_slots, int64_t cap, void* k_out, void* v_out,
+                   const int64_t* offsets, const int64_t* slots, const int64_t* cu_seqlens,
+                   int64_t num_seqs, int64_t B, int64_t T, int64_t Hk, int64_t D, void* stream);
+int kda_cache4_put_check(const void* k, int64_t k_row, const void* v, int64_t v_row,
+                         const void* k4, const void* ks, const void* v4, const void* vs,
+                         int64_t num_slots, int64_t cap, const void* k_out, const void* v_out,
+                         const int64_t* offsets, const int64_t* slots, const int64_t* cu_seqlens,
+                         int64_t num_seqs, int64_t B, int64_t T, int64_t Hk, int64_t D);
+
+/*
+ * kda_attn4_fwd -- kda_attn_fwd over caches in 4 bits: the same formulas, masks and limits, with
+ * keys and values the products of codes and scales (exact in bf16; beyond its range infinity).
+ *   q, q_row, scale, out, lse, cu_seqlens_q, num_seqs, Bq, Tq, Hq, Hk, D  as for kda_attn_fwd.
+ *   k4, ks, v4, vs, num_slots, cap  the caches.
+ *   k_lens         int64 [num_seqs] device array, clamped into [0, cap]; NULL: all cap.  Positions
+ *                  behind a sequence's last are never used, whatever they hold.
+ *   slots          int64 [num_seqs] device array, NULL: n (num_seqs <= num_slots).  Several
+ *                  sequences may read one slot.  An index outside [0, num_slots) has no keys.
+ *   part           0 (automatic), or keys per part: a multiple of 32 with at most 64 parts in
+ *                  cap (KDA_ERR_BAD_SCHEDULE).  Each part of a row's keys has a workgroup of its
+ *                  own, and a second kernel joins them.
+ *   workspace      caller-owned device memory, 16-byte aligned, of at least
+ *                  kda_attn4_workspace_bytes(num_seqs, Bq, Tq, cap, Hq, Hk, D, part) bytes
+ *                  (KDA_ERR_BAD_WORKSPACE), scratch on return: calls that may overlap in time
+ *                  need one each.  With part 0 it may be NULL: one part then.
+ * Scores and sums are fp32; probabilities take two bf16 parts for their product with v.
+ * Parts sum in another order.  A call repeats itself bit for bit.  Infinities and NaN reach the
+ * outputs of the queries that see them and no others.
+ */
+int kda_attn4_fwd(const void* q, int64_t q_row, const void* k4, const void* ks, const void* v4,
+                  const void* vs, int64_t num_slots, int64_t cap, float scale, void* out,
+                  float* lse, const int64_t* cu_seqlens_q, const int64_t* k_lens,
+                  const int64_t* slots, int64_t num_seqs, int64_t Bq, int64_t Tq, int64_t Hq,
+                  int64_t Hk, int64_t D, int64_t part, void* workspace, int64_t workspace_bytes,
+                  void* stream);
+int kda_attn4_fwd_check(const void* q, int64_t q_row, const void* k4, const void* ks,
+                        const void* v4, const void* vs, int64_t num_slots, int64_t cap,
+                        float scale, const void* out, const float* lse,
+                        const int64_t* cu_seqlens_q, const int64_t* k_lens, const int64_t* slots,
+                        int64_t num_seqs, int64_t Bq, int64_t Tq, int64_t Hq, int64_t Hk,
+                        int64_t D, int64_t part, const void* workspace, int64_t workspace_bytes);
+
+/*
+ * kda_attn4_workspace_bytes -- bytes of kda_attn4_fwd's workspace: zero when the keys are one part,
+ * else parts * Bq * Tq * Hq * (D + 2) floats.  Returns the size or a negative status.
+ */
+int64_t kda_attn4_workspace_bytes(int64_t num_seqs, int64_t Bq, int64_t Tq, int64_t cap,
+                                  int64_t Hq, int64_t Hk, int64_t D, int64_t part);
 
 /* kda_status_string -- a static, human-readable name for a status code. */
 const char* kda_status_string(int status);
