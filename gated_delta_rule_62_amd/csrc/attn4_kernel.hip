@@ -124,12 +124,13 @@ __device__ __forceinline__ bool may_be_odd(const Step4<D>& s) {
 }
 
 template <int D, int NI>
-__global__ __launch_bounds__(kAttnThreads, NI == 1 ? 3 : NI == 2 ? 2 : 1) void attn4_kernel(
+__global__ __launch_bounds__(kAttnThreads, NI == 1 ? 3 : 2) void attn4_kernel(
     Attn4Params q4) {
+  constexpr int WAVES = kAttnThreads / 64;
   constexpr int KS = D / 32, DT = D / 16, ROWS = 16 * NI;
   constexpr int LO = D + 4;  // row stride of the join buffer (floats)
-  __shared__ alignas(16) float so[4][16][LO];
-  __shared__ float sml[4][ROWS][2];
+  __shared__ alignas(16) float so[WAVES][16][LO];
+  __shared__ float sml[WAVES][ROWS][2];
   const AttnParams& p = q4.a;
 
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lg = lane >> 4;
@@ -140,8 +141,7 @@ __global__ __launch_bounds__(kAttnThreads, NI == 1 ? 3 : NI == 2 ? 2 : 1) void a
   const int hk = (int)(unit % (unsigned)p.Hk);
   Tile t;
   if (!find_tile(p, unit / (unsigned)p.Hk, ROWS, t)) return;
-  const int seq = (int)(t.k0 / p.Tk);
-  const int64_t slot = q4.slot != nullptr ? q4.slot[seq] : seq;
+  const int64_t slot = q4.slot != nullptr ? q4.slot[t.n] : t.n;
   if (slot < 0 || slot >= q4.c.slots) t.Lk = 0;
 
   const int off = t.Lk - t.Lq;
@@ -183,8 +183,8 @@ __global__ __launch_bounds__(kAttnThreads, NI == 1 ? 3 : NI == 2 ? 2 : 1) void a
   Acc<D, NI> acc;
   acc.init();
   bool odd = false;  // some step dropped infinities or NaN of v
-  for (int s = first + wave; s < end; s += 4) {
-    if (s + 4 < end) next = view.load(s + 4);
+  for (int s = first + wave; s < end; s += WAVES) {
+    if (s + WAVES < end) next = view.load(s + WAVES);
     f32x4_t x[2][NI];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -200,6 +200,7 @@ __global__ __launch_bounds__(kAttnThreads, NI == 1 ? 3 : NI == 2 ? 2 : 1) void a
     }
     bool drop = false;
     if ((s + 1) * kCache4Tile > all_keys) {  // some row does not see all of these keys
+      asm volatile("");  // keeps this a branch
       drop = may_be_odd<D>(now);
       odd |= drop;
 #pragma unroll
@@ -255,7 +256,7 @@ __global__ __launch_bounds__(kAttnThreads, NI == 1 ? 3 : NI == 2 ? 2 : 1) void a
   }
 
   // what was dropped, after the loop, where it takes no registers from it
-  for (int s = first + wave; odd && s < end; s += 4) {
+  for (int s = first + wave; odd && s < end; s += WAVES) {
     if ((s + 1) * kCache4Tile <= all_keys) continue;
     now = view.load(s);
     if (!may_be_odd<D>(now)) continue;
@@ -304,7 +305,7 @@ __global__ __launch_bounds__(kAttnThreads, NI == 1 ? 3 : NI == 2 ? 2 : 1) void a
   for (int i = 0; i < NI; ++i) {
     float m = kNone;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) m = fmaxf(m, sml[w][16 * i + l16][0]);
+    for (int w = 0; w < WAVES; ++w) m = fmaxf(m, sml[w][16 * i + l16][0]);
     const float f = __builtin_amdgcn_exp2f(acc.m[i] - (m == kNone ? 0.f : m));
 #pragma unroll
     for (int r = 0; r < 4; ++r)
@@ -314,25 +315,26 @@ __global__ __launch_bounds__(kAttnThreads, NI == 1 ? 3 : NI == 2 ? 2 : 1) void a
             f32x4_t{acc.o[e][i][r], acc.o[e + 1][i][r], acc.o[e + 2][i][r], acc.o[e + 3][i][r]} *
             f;
     lds_barrier();
-    // thread: row tid / 16, D / 16 columns from (tid % 16) * 4 in strides of 64
-    const int rr = tid >> 4, r = t.row0 + 16 * i + rr;
+    // thread: row tid / TPT, D / TPT columns from (tid % TPT) * 4 in strides of 4 TPT
+    constexpr int TPT = kAttnThreads / 16;
+    const int rr = tid / TPT, r = t.row0 + 16 * i + rr;
     float mr = kNone, lr = 0.f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) mr = fmaxf(mr, sml[w][16 * i + rr][0]);
+    for (int w = 0; w < WAVES; ++w) mr = fmaxf(mr, sml[w][16 * i + rr][0]);
     const float br = mr == kNone ? 0.f : mr;
 #pragma unroll
-    for (int w = 0; w < 4; ++w)
+    for (int w = 0; w < WAVES; ++w)
       lr += sml[w][16 * i + rr][1] * __builtin_amdgcn_exp2f(sml[w][16 * i + rr][0] - br);
     if (r < t.rows) {
       const int64_t at = (t.q0 + r / p.G) * p.Hq + hk * p.G + r % p.G;
       const int64_t w = (int64_t)split * p.Tq_total * p.Hq + at;
       const float g = lr > 0.f ? 1.f / lr : lr == 0.f ? 0.f : lr;
 #pragma unroll
-      for (int cc = 0; cc < D / 64; ++cc) {
-        const int c = 64 * cc + 4 * (tid & 15);
+      for (int cc = 0; cc < D / (4 * TPT); ++cc) {
+        const int c = 4 * TPT * cc + 4 * (tid % TPT);
         f32x4_t o = *reinterpret_cast<const f32x4_t*>(&so[0][rr][c]);
 #pragma unroll
-        for (int ww = 1; ww < 4; ++ww) o += *reinterpret_cast<const f32x4_t*>(&so[ww][rr][c]);
+        for (int ww = 1; ww < WAVES; ++ww) o += *reinterpret_cast<const f32x4_t*>(&so[ww][rr][c]);
         if (p.splits > 1) {
           *reinterpret_cast<f32x4_t*>(p.ws_o + w * D + c) = o;
         } else {
@@ -340,13 +342,58 @@ __global__ __launch_bounds__(kAttnThreads, NI == 1 ? 3 : NI == 2 ? 2 : 1) void a
               u32x2_t{pack_bf16(o[0] * g, o[1] * g), pack_bf16(o[2] * g, o[3] * g)};
         }
       }
-      if ((tid & 15) == 0) {
+      if (tid % TPT == 0) {
         if (p.splits > 1) *reinterpret_cast<f32x2_t*>(p.ws_ml + 2 * w) = f32x2_t{mr, lr};
         else if (p.lse != nullptr)
           p.lse[at] = lr == 0.f ? kNone : (mr + __builtin_amdgcn_logf(lr)) * kLn2;
       }
     }
     if (i + 1 < NI) lds_barrier();
+  }
+}
+
+// ---- many rows: keys and values in bf16 to a workspace once, [N, cap, Hk, D], for the kernel of
+// kda_attn_fwd's prompts.  A workgroup takes a tile of 32 keys of one head; lengths go along.
+template <int D>
+__global__ __launch_bounds__(kAttnThreads) void expand4_kernel(Attn4Params q4) {
+  constexpr int LPT = D / 16;  // threads of a key, 16 channels each
+  const AttnParams& p = q4.a;
+  const int tid = threadIdx.x;
+  const unsigned tiles = (unsigned)(p.Tk / kCache4Tile);
+  const int hk = (int)(blockIdx.x % (unsigned)p.Hk);
+  const unsigned at = blockIdx.x / (unsigned)p.Hk;
+  const int n = (int)(at / tiles), tile = (int)(at % tiles);
+  const int64_t slot = q4.slot != nullptr ? q4.slot[n] : n;
+  const bool there = slot >= 0 && slot < q4.c.slots;
+  const int64_t len = !there ? 0 : p.k_lens != nullptr ? clamp64(p.k_lens[n], 0, p.Tk) : p.Tk;
+  if (tile == 0 && hk == 0 && tid == 0) q4.lens[n] = len;
+  if ((int64_t)tile * kCache4Tile >= len) return;
+
+  const int64_t unit = slot * p.Hk + hk, t = unit * tiles + tile;
+  const uint8_t *kc = q4.c.k4 + t * (16 * D), *vc = q4.c.v4 + t * (16 * D),
+                *ks = q4.c.ks + t * D, *vs = q4.c.vs + t * D;
+  for (int x = tid / LPT; x < kCache4Tile; x += kAttnThreads / LPT) {
+    const int c = tid % LPT, j = x >> 4, i = x >> 2 & 3, g = x & 3, place = 8 * g + 2 * i + j;
+    const int64_t to = (((int64_t)n * p.Tk + tile * kCache4Tile + x) * p.Hk + hk) * D + 16 * c;
+    const float fk = scale_of(ks[c / 2 * 32 + place], 0), fv = scale_of(vs[c / 2 * 32 + place], 0);
+    const u32x2_t wk = *reinterpret_cast<const u32x2_t*>(kc + x * (D / 2) + 8 * c);
+    unsigned v0, v1;
+    if constexpr (D == 128) {
+      const uint8_t* from = vc + 1024 * j + 256 * g + 32 * c + 4 * i;
+      v0 = *reinterpret_cast<const unsigned*>(from);
+      v1 = *reinterpret_cast<const unsigned*>(from + 16);
+    } else {
+      const uint8_t* from = vc + 256 * g + 64 * c + 8 * j + 2 * i;
+      const u16* h = reinterpret_cast<const u16*>(from);
+      v0 = h[0] | (unsigned)h[8] << 16;
+      v1 = h[16] | (unsigned)h[24] << 16;
+    }
+    u32x4_t* ko = reinterpret_cast<u32x4_t*>(q4.k_ws + to);
+    u32x4_t* vo = reinterpret_cast<u32x4_t*>(q4.v_ws + to);
+    ko[0] = eight_values(wk[0], fk);
+    ko[1] = eight_values(wk[1], fk);
+    vo[0] = eight_values(v0, fv);
+    vo[1] = eight_values(v1, fv);
   }
 }
 
@@ -357,8 +404,7 @@ hipError_t go(const Attn4Params& p, int rows, hipStream_t stream) {
   if (a.cu_q == nullptr) slots = a.N * ((a.Tq * a.G + rows - 1) / rows);
   const dim3 grid((unsigned)(slots * a.Hk * a.splits));
   if (rows == 16) attn4_kernel<D, 1><<<grid, kAttnThreads, 0, stream>>>(p);
-  else if (rows == 32) attn4_kernel<D, 2><<<grid, kAttnThreads, 0, stream>>>(p);
-  else attn4_kernel<D, 4><<<grid, kAttnThreads, 0, stream>>>(p);
+  else attn4_kernel<D, 2><<<grid, kAttnThreads, 0, stream>>>(p);
   if (a.splits > 1) return launch_attn_join(a, D, stream);
   return hipGetLastError();
 }
@@ -367,7 +413,14 @@ hipError_t go(const Attn4Params& p, int rows, hipStream_t stream) {
 
 int attn4_rows(int64_t Tq_total, int64_t N, int64_t G) {
   const int64_t mean = (Tq_total * G + N - 1) / N;  // rows of a sequence and key/value head
-  return mean <= 16 ? 16 : mean <= 32 ? 32 : 64;
+  return mean <= 16 ? 16 : 32;
+}
+
+hipError_t launch_expand4(const Attn4Params& p, int D, hipStream_t stream) {
+  const dim3 grid((unsigned)(p.a.N * (p.a.Tk / kCache4Tile) * p.a.Hk));
+  if (D == 64) expand4_kernel<64><<<grid, kAttnThreads, 0, stream>>>(p);
+  else expand4_kernel<128><<<grid, kAttnThreads, 0, stream>>>(p);
+  return hipGetLastError();
 }
 
 hipError_t launch_attn4(const Attn4Params& p, int rows, int D, hipStream_t stream) {

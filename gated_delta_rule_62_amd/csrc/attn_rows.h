@@ -14,6 +14,7 @@ constexpr float kNone = -__builtin_inff();
 
 // A tile of rows: its sequence's queries and keys, its rows.
 struct Tile {
+  int n;            // its sequence
   int64_t q0, k0;   // first query and key token
   int Lq, Lk;       // lengths
   int row0, rows;   // first row of the tile, rows of the sequence (Lq * G)
@@ -48,6 +49,7 @@ __device__ __forceinline__ bool set_tile(const AttnParams& p, int n, int64_t row
   int64_t a, b;
   query_bounds(p, n, a, b);
   if (row0 < 0 || row0 >= (b - a) * p.G) return false;
+  t.n = n;
   t.row0 = (int)row0;
   t.q0 = a;
   t.Lq = (int)(b - a);

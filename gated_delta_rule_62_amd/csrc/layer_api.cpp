@@ -189,15 +189,34 @@ int put4_check(const void* k, int64_t k_row, const void* v, int64_t v_row, const
   return KDA_OK;
 }
 
+// How a kda_attn4_fwd call runs: keys in parts of `part` straight from the cache, rows16 16-row
+// tiles a workgroup; or (expand) keys and values to a bf16 workspace first and then the kernel of
+// kda_attn_fwd's prompts with `splits` parts of each row's keys.
+struct Plan4 {
+  bool expand;
+  int rows;
+  int64_t part, splits;
+  kda::AttnSchedule sched;
+  int64_t bytes;  // of the workspace
+};
+
 // Keys of a part when the caller leaves the choice.
 int64_t attn4_auto_part(int64_t units, int64_t cap) {
-  int64_t part = 512;
+  int64_t part = 1024;
   while (cap > 64 * part) part *= 2;
   return cap <= 1024 ? cap : part;
 }
 
-int attn4_sizes(int64_t N, int64_t Bq, int64_t Tq, int64_t cap, int64_t Hq, int64_t Hk, int64_t D,
-                int64_t part, int* rows, int64_t* part_out) {
+constexpr int64_t kExpandMax = (int64_t)8 << 30;  // bytes of expanded keys and values, at most
+
+int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
+
+int64_t parts_bytes(int64_t parts, int64_t rows, int64_t D) {
+  return parts > 1 ? parts * rows * (D + 2) * 4 : 0;
+}
+
+int attn4_plan(int64_t N, int64_t Bq, int64_t Tq, int64_t cap, int64_t Hq, int64_t Hk, int64_t D,
+               int64_t part, bool workspace, Plan4* plan) {
   if (D != 64 && D != 128) return KDA_ERR_BAD_SHAPE;
   if (Hk < 1 || Hq < 1 || Hq % Hk != 0 || Hq >= (1 << 24)) return KDA_ERR_BAD_SHAPE;
   if (N < 1 || N >= ((int64_t)1 << 31) || Bq < 1 || Tq < 0) return KDA_ERR_BAD_SHAPE;
@@ -209,34 +228,46 @@ int attn4_sizes(int64_t N, int64_t Bq, int64_t Tq, int64_t cap, int64_t Hq, int6
     return KDA_ERR_BAD_SHAPE;
   if (part < 0 || part % kCache4Tile != 0 || (part && (cap + part - 1) / part > 64))
     return KDA_ERR_BAD_SCHEDULE;
-  const int64_t G = Hq / Hk, total = Bq * Tq;
-  *rows = kda::attn4_rows(total, N, G);
-  const int64_t most = kMostItems / kda::kAttnThreads;
-  const int64_t tiles = kda::attn_slots(total, N, G, *rows) + (Bq == N ? N : 0);
+  const int64_t G = Hq / Hk, total = Bq * Tq, most = kMostItems / kda::kAttnThreads;
+  plan->rows = kda::attn4_rows(total, N, G);
+  const int64_t tiles = kda::attn_slots(total, N, G, plan->rows) + (Bq == N ? N : 0);
   if (tiles > most / Hk) return KDA_ERR_BAD_SHAPE;
-  int64_t pt = part ? part : attn4_auto_part(tiles * Hk, cap);
+  plan->expand = false;
+  plan->splits = 1;
+  // (row, key/value head) pairs a sequence, and whether its keys may be expanded
+  const int64_t row_bytes = Hk * D * 4;
+  if (part == 0 && workspace && total * G > N * kda::kExpand4Rows &&
+      Hk * D < (1 << 24) && N <= kExpandMax / row_bytes / cap &&
+      N * Hk <= most / (cap / kCache4Tile)) {
+    plan->expand = true;
+    plan->sched = kda::AttnSchedule{0, 2, 128};
+    const int64_t slots = Bq == N ? N * ((Tq * G + 127) / 128) : kda::attn_slots(total, N, G, 128);
+    int64_t sp = kda::attn_auto_splits(plan->sched, slots, Hk, cap);
+    if (sp > 1 && (slots * Hk > most / sp || total > 4 * most / Hq)) sp = 1;
+    plan->splits = sp;
+    plan->part = cap;
+    plan->bytes = N * cap * row_bytes + round16(N * 8) + parts_bytes(sp, total * Hq, D);
+    return KDA_OK;
+  }
+  int64_t pt = part ? part : workspace ? attn4_auto_part(tiles * Hk, cap) : cap;
   if (pt > cap) pt = cap;
   const int64_t parts = (cap + pt - 1) / pt;
   if (parts > 1 && (tiles * Hk > most / parts || total > 4 * most / Hq)) {
     if (part) return KDA_ERR_BAD_SHAPE;
     pt = cap;
   }
-  *part_out = pt;
+  plan->part = pt;
+  plan->bytes = parts_bytes((cap + pt - 1) / pt, total * Hq, D);
   return KDA_OK;
-}
-
-int64_t attn4_ws_bytes(int64_t total, int64_t Hq, int64_t D, int64_t cap, int64_t part) {
-  const int64_t parts = (cap + part - 1) / part;
-  return parts > 1 ? parts * total * Hq * (D + 2) * 4 : 0;
 }
 
 int attn4_check(const void* q, int64_t q_row, const void* k4, const void* ks, const void* v4,
                 const void* vs, int64_t num_slots, int64_t cap, float scale, const void* out,
                 const float* lse, const int64_t* cu_q, const int64_t* k_lens, const int64_t* slots,
                 int64_t N, int64_t Bq, int64_t Tq, int64_t Hq, int64_t Hk, int64_t D, int64_t part,
-                const void* workspace, int64_t workspace_bytes, int* rows, int64_t* part_out) {
-  int64_t pt = cap;
-  int st = attn4_sizes(N, Bq, Tq, cap, Hq, Hk, D, part, rows, &pt);
+                const void* workspace, int64_t workspace_bytes, Plan4* plan) {
+  // left to the library: without a workspace, neither parts nor expanded keys
+  int st = attn4_plan(N, Bq, Tq, cap, Hq, Hk, D, part, workspace != nullptr, plan);
   if (st != KDA_OK) return st;
   if (cu_q ? Bq != 1 : Bq != N) return KDA_ERR_BAD_VARLEN;
   if (!slots && N > num_slots) return KDA_ERR_BAD_SHAPE;
@@ -251,8 +282,7 @@ int attn4_check(const void* q, int64_t q_row, const void* k4, const void* ks, co
     return KDA_ERR_BAD_LAYOUT;
   const int64_t bq = span_bytes(nq, q_row, Hq, D);
   if (bq < 0) return KDA_ERR_BAD_SHAPE;
-  if (part == 0 && !workspace) pt = cap;  // left to the library: without one, one part
-  const int64_t need = attn4_ws_bytes(nq, Hq, D, cap, pt);
+  const int64_t need = plan->bytes;
   if (need > 0 && !workspace) return KDA_ERR_NULL_ARG;
   if (need > workspace_bytes) return KDA_ERR_BAD_WORKSPACE;
   const Range ins[] = {make_range(q, bq),
@@ -268,7 +298,6 @@ int attn4_check(const void* q, int64_t q_row, const void* k4, const void* ks, co
   for (int i = 0; i < 3; ++i)
     if (any_overlap(outs[i], ins, 8) || any_overlap(outs[i], outs + i + 1, 2 - i))
       return KDA_ERR_BAD_ALIAS;
-  *part_out = pt;
   return KDA_OK;
 }
 
@@ -407,10 +436,9 @@ int kda_cache4_put(const void* k, int64_t k_row, const void* v, int64_t v_row, v
 
 int64_t kda_attn4_workspace_bytes(int64_t num_seqs, int64_t Bq, int64_t Tq, int64_t cap,
                                   int64_t Hq, int64_t Hk, int64_t D, int64_t part) {
-  int rows = 0;
-  int64_t pt = 0;
-  const int st = attn4_sizes(num_seqs, Bq, Tq, cap, Hq, Hk, D, part, &rows, &pt);
-  return st != KDA_OK ? st : attn4_ws_bytes(Bq * Tq, Hq, D, cap, pt);
+  Plan4 plan = {};
+  const int st = attn4_plan(num_seqs, Bq, Tq, cap, Hq, Hk, D, part, true, &plan);
+  return st != KDA_OK ? st : plan.bytes;
 }
 
 int kda_attn4_fwd_check(const void* q, int64_t q_row, const void* k4, const void* ks,
@@ -419,11 +447,10 @@ int kda_attn4_fwd_check(const void* q, int64_t q_row, const void* k4, const void
                         const int64_t* cu_seqlens_q, const int64_t* k_lens, const int64_t* slots,
                         int64_t num_seqs, int64_t Bq, int64_t Tq, int64_t Hq, int64_t Hk,
                         int64_t D, int64_t part, const void* workspace, int64_t workspace_bytes) {
-  int rows = 0;
-  int64_t pt = 0;
+  Plan4 plan = {};
   return attn4_check(q, q_row, k4, ks, v4, vs, num_slots, cap, scale, out, lse, cu_seqlens_q,
                      k_lens, slots, num_seqs, Bq, Tq, Hq, Hk, D, part, workspace, workspace_bytes,
-                     &rows, &pt);
+                     &plan);
 }
 
 int kda_attn4_fwd(const void* q, int64_t q_row, const void* k4, const void* ks, const void* v4,
@@ -432,11 +459,10 @@ int kda_attn4_fwd(const void* q, int64_t q_row, const void* k4, const void* ks, 
                   const int64_t* slots, int64_t num_seqs, int64_t Bq, int64_t Tq, int64_t Hq,
                   int64_t Hk, int64_t D, int64_t part, void* workspace, int64_t workspace_bytes,
                   void* stream) {
-  int rows = 0;
-  int64_t pt = 0;
+  Plan4 plan = {};
   const int st = attn4_check(q, q_row, k4, ks, v4, vs, num_slots, cap, scale, out, lse,
                              cu_seqlens_q, k_lens, slots, num_seqs, Bq, Tq, Hq, Hk, D, part,
-                             workspace, workspace_bytes, &rows, &pt);
+                             workspace, workspace_bytes, &plan);
   if (st != KDA_OK || Bq * Tq == 0) return st;
   kda::Attn4Params p = {};
   kda::AttnParams& a = p.a;
@@ -454,14 +480,31 @@ int kda_attn4_fwd(const void* q, int64_t q_row, const void* k4, const void* ks, 
   a.Hk = static_cast<int32_t>(Hk);
   a.G = static_cast<int32_t>(Hq / Hk);
   a.c = kda::attn_factor(scale);
-  a.splits = static_cast<int32_t>((cap + pt - 1) / pt);
-  a.ws_o = static_cast<float*>(workspace);
-  a.ws_ml = a.splits > 1 ? a.ws_o + a.splits * a.Tq_total * Hq * D : nullptr;
   p.c = cache_of(k4, ks, v4, vs, num_slots, cap);
   p.slot = slots;
-  p.part = static_cast<int32_t>(pt / kCache4Tile);
-  return status(
-      kda::launch_attn4(p, rows, static_cast<int>(D), static_cast<hipStream_t>(stream)));
+  p.part = static_cast<int32_t>(plan.part / kCache4Tile);
+  hipStream_t const on = static_cast<hipStream_t>(stream);
+  a.splits = static_cast<int32_t>(plan.expand ? plan.splits : (cap + plan.part - 1) / plan.part);
+  char* ws = static_cast<char*>(workspace);
+  if (plan.expand) {
+    const int64_t half = num_seqs * cap * Hk * D * 2;
+    p.k_ws = reinterpret_cast<uint16_t*>(ws);
+    p.v_ws = reinterpret_cast<uint16_t*>(ws + half);
+    p.lens = reinterpret_cast<int64_t*>(ws + 2 * half);
+    ws += 2 * half + round16(num_seqs * 8);
+  }
+  if (a.splits > 1) {
+    a.ws_o = reinterpret_cast<float*>(ws);
+    a.ws_ml = a.ws_o + a.splits * a.Tq_total * Hq * D;
+  }
+  if (!plan.expand) return status(kda::launch_attn4(p, plan.rows, static_cast<int>(D), on));
+  const hipError_t e = kda::launch_expand4(p, static_cast<int>(D), on);
+  if (e != hipSuccess) return status(e);
+  a.k = p.k_ws;
+  a.v = p.v_ws;
+  a.k_row = a.v_row = Hk * D;
+  a.k_lens = p.lens;
+  return status(kda::launch_attn(a, plan.sched, static_cast<int>(D), on));
 }
 
 }  // extern "C"

@@ -94,9 +94,15 @@ struct Attn4Params {
   Cache4 c;
   const int64_t* slot;     // [N] or nullptr (n)
   int32_t part;            // tiles of 32 keys per part
+  uint16_t* k_ws;          // expanded keys and values [N, cap, Hk, D] (many rows)
+  uint16_t* v_ws;
+  int64_t* lens;           // [N] their lengths
 };
-// Rows per workgroup of a call: 16, 32 or 64.
+// Rows of a sequence and key/value head from which on keys and values are expanded.
+constexpr int kExpand4Rows = 128;
+// Rows per workgroup of a call: 16 or 32.
 int attn4_rows(int64_t Tq_total, int64_t N, int64_t G);
+hipError_t launch_expand4(const Attn4Params& p, int D, hipStream_t stream);
 hipError_t launch_attn4(const Attn4Params& p, int rows, int D, hipStream_t stream);
 
 }  // namespace kda

@@ -105,6 +105,9 @@ AttnSchedule attn_schedule(int64_t Tq_total, int64_t N, int64_t G);
 constexpr int64_t attn_slots(int64_t Tq_total, int64_t N, int64_t G, int64_t rows) {
   return Tq_total * G / rows + N;
 }
+// Parts of each row's keys when the caller leaves the choice (slots tiles of rows and key/value
+// head, mean_k keys a sequence on average).
+int64_t attn_auto_splits(const AttnSchedule& s, int64_t slots, int64_t Hk, int64_t mean_k);
 constexpr int kAttnThreads = 256;
 constexpr int kAttnKeys = 64;  // keys per step of the tile kernel
 
