@@ -43,34 +43,87 @@ struct Step4<64> {
   unsigned ks;
 };
 
-// One (slot, key/value head) of a cache, and where this lane's parts of a tile lie.
+// One word a lane from memory to LDS, as load_lds.
+template <bool ONCE>
+__device__ __forceinline__ void load_lds_word(const uint8_t* at, const uint8_t* to) {
+  const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)to;
+  const uint32_t m0 = (uint32_t)__builtin_amdgcn_readfirstlane(lds);
+  if constexpr (ONCE)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off nt"
+                 :
+                 : "s"(m0), "v"(at)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+                 :
+                 : "s"(m0), "v"(at)
+                 : "memory", "m0");
+}
+
+// A tile of 32 keys on its way from a cache through LDS.  Every lane brings its own 16 (keys of
+// 64 channels: 8) bytes of each instruction and reads them back from where they land, so reads
+// meet no bank twice; the scales' two words of 32 positions lie side by side.
 template <int D>
+struct Tile4 {
+  uint8_t k[16 * D], v[16 * D], s[256];
+};
+template <int D, bool ONCE>
 struct View4 {
-  const uint8_t *k4, *v4, *ks, *vs;
+  static constexpr int LOADS = D == 128 ? 5 : 3;  // instructions of a tile
+  const uint8_t *k4, *v4, *sc;
+  uint32_t k_at, v_at, k_lds, ks_lds, vs_lds;
 
   __device__ __forceinline__ View4(const Cache4& c, int64_t unit, int lane) {
-    const int g = lane >> 4, l = lane & 15;
-    const int64_t tiles = c.cap / kCache4Tile;
-    k4 = c.k4 + unit * c.cap * (D / 2) + (4 * (l & 3) + (l >> 2)) * (D / 2) + g * (D / 8);
-    v4 = c.v4 + unit * tiles * (16 * D) + lane * 16;
-    ks = c.ks + unit * tiles * D + g * (D / 32) / 4 * 32 + 2 * l;
-    vs = c.vs + unit * tiles * D + l * (D / 32) / 16 * 32 + 8 * g;
-  }
-  __device__ __forceinline__ Step4<D> load(int tile) const {
-    Step4<D> s;
-    const int64_t at = (int64_t)tile * (16 * D), sc = (int64_t)tile * D;
+    const uint32_t g = lane >> 4, l = lane & 15;
+    const int64_t at = unit * (c.cap / kCache4Tile);
+    k4 = c.k4 + at * (16 * D);
+    v4 = c.v4 + at * (16 * D);
+    // lanes of the first half bring the keys' scales (a word each, D / 4 of them), of the second
+    // the values'; what lanes behind them bring lands behind and is not used
+    const uint32_t word = lane & 31;
+    sc = (lane < 32 ? c.ks : c.vs) + at * D + (word < D / 4 ? 4 * word : 0);
+    v_at = lane * 16;
+    const uint32_t row = 4 * (l & 3) + (l >> 2);  // the key of sixteen
     if constexpr (D == 128) {
-      s.k[0] = *reinterpret_cast<const u32x4_t*>(k4 + at);
-      s.k[1] = *reinterpret_cast<const u32x4_t*>(k4 + at + 1024);
-      s.v[0] = *reinterpret_cast<const u32x4_t*>(v4 + at);
-      s.v[1] = *reinterpret_cast<const u32x4_t*>(v4 + at + 1024);
+      k_at = row * 64 + g * 16;
+      k_lds = v_at;
     } else {
-      s.k[0] = *reinterpret_cast<const u32x2_t*>(k4 + at);
-      s.k[1] = *reinterpret_cast<const u32x2_t*>(k4 + at + 512);
-      s.v = *reinterpret_cast<const u32x4_t*>(v4 + at);
+      k_at = v_at;  // 32 keys at once, a lane the halves of two operands
+      k_lds = row * 32 + g * 8;
     }
-    s.ks = *reinterpret_cast<const u16*>(ks + sc);
-    s.vs = *reinterpret_cast<const u32x2_t*>(vs + sc);
+    ks_lds = g * (D / 32) / 4 * 32 + 2 * l;
+    vs_lds = 128 + l * (D / 32) / 16 * 32 + 8 * g;
+  }
+  static __device__ __forceinline__ u32x4_t words(const uint8_t* base) {
+    const uint64_t at = reinterpret_cast<uint64_t>(base);
+    return u32x4_t{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at),
+                   (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32) & 0xffffu),
+                   16u * D, 0x00020000u};
+  }
+  __device__ __forceinline__ void load(int tile, const Tile4<D>& to) const {
+    const u32x4_t dk = words(k4 + (int64_t)tile * (16 * D)),
+                  dv = words(v4 + (int64_t)tile * (16 * D));
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      load_lds<ONCE>(dk, reinterpret_cast<const u16*>(to.k + 1024 * i), k_at + 1024 * i);
+      load_lds<ONCE>(dv, reinterpret_cast<const u16*>(to.v + 1024 * i), v_at + 1024 * i);
+    }
+    load_lds_word<ONCE>(sc + (int64_t)tile * D, to.s);
+  }
+  __device__ __forceinline__ Step4<D> read(const Tile4<D>& from) const {
+    Step4<D> s;
+    if constexpr (D == 128) {
+      s.k[0] = *reinterpret_cast<const u32x4_t*>(from.k + k_lds);
+      s.k[1] = *reinterpret_cast<const u32x4_t*>(from.k + k_lds + 1024);
+      s.v[0] = *reinterpret_cast<const u32x4_t*>(from.v + v_at);
+      s.v[1] = *reinterpret_cast<const u32x4_t*>(from.v + v_at + 1024);
+    } else {
+      s.k[0] = *reinterpret_cast<const u32x2_t*>(from.k + k_lds);
+      s.k[1] = *reinterpret_cast<const u32x2_t*>(from.k + k_lds + 512);
+      s.v = *reinterpret_cast<const u32x4_t*>(from.v + v_at);
+    }
+    s.ks = *reinterpret_cast<const u16*>(from.s + ks_lds);
+    s.vs = *reinterpret_cast<const u32x2_t*>(from.s + vs_lds);
     return s;
   }
 };
@@ -123,13 +176,40 @@ __device__ __forceinline__ bool may_be_odd(const Step4<D>& s) {
   return __any(any);
 }
 
-template <int D, int NI>
-__global__ __launch_bounds__(kAttnThreads, NI == 1 ? 3 : 2) void attn4_kernel(
-    Attn4Params q4) {
-  constexpr int WAVES = kAttnThreads / 64;
-  constexpr int KS = D / 32, DT = D / 16, ROWS = 16 * NI;
+// Waits for a row's loads before the loop over the keys: their first use inside it would make every
+// step wait for all loads in flight.
+template <int KS>
+__device__ __forceinline__ void end_row_loads(u32x4_t (&q)[KS]) {
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) asm volatile("" : "+v"(q[ks]));
+}
+
+// The last of N sequences whose first slot of rows is not behind `slot` (packed queries; first
+// slots grow strictly).  64 lanes look at once: a binary search would wait for memory each step.
+__device__ __forceinline__ int find_sequence(const AttnParams& p, unsigned slot, int lane) {
+  int lo = 0, n = p.N;
+  while (n > 1) {
+    const int stride = (n + 63) >> 6, at = lo + lane * stride;
+    bool before = false;
+    if (at < lo + n)
+      before = clamp64(p.cu_q[at], 0, p.Tq_total) * p.G / kAttn4Rows + at <= slot;
+    const int k = max(1, (int)__popcll(__ballot(before))) - 1;
+    n = min(stride, n - k * stride);
+    lo += k * stride;
+  }
+  return lo;
+}
+
+template <int D, bool ONCE>
+__global__ __launch_bounds__(kAttnThreads, 3) void attn4_kernel(Attn4Params q4) {
+  constexpr int KS = D / 32, DT = D / 16, ROWS = kAttn4Rows, WAVES = kAttnThreads / 64;
+  constexpr int kAhead = 3;  // tiles of a wave on their way
   constexpr int LO = D + 4;  // row stride of the join buffer (floats)
-  __shared__ alignas(16) float so[WAVES][16][LO];
+  union Smem {
+    Tile4<D> tile[WAVES][kAhead];
+    float o[WAVES][ROWS][LO];
+  };
+  __shared__ alignas(16) Smem sm;
   __shared__ float sml[WAVES][ROWS][2];
   const AttnParams& p = q4.a;
 
@@ -137,66 +217,59 @@ __global__ __launch_bounds__(kAttnThreads, NI == 1 ? 3 : 2) void attn4_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const unsigned units = gridDim.x / (unsigned)p.splits;
   const int split = (int)(blockIdx.x / units);
-  const unsigned unit = blockIdx.x % units;
+  const unsigned unit = blockIdx.x % units, tile_no = unit / (unsigned)p.Hk;
   const int hk = (int)(unit % (unsigned)p.Hk);
   Tile t;
-  if (!find_tile(p, unit / (unsigned)p.Hk, ROWS, t)) return;
+  if (p.cu_q == nullptr) {
+    const unsigned n = tile_no / (unsigned)q4.row_tiles;
+    if (!set_tile(p, (int)n, (int64_t)(tile_no % (unsigned)q4.row_tiles) * ROWS, t)) return;
+  } else {
+    const int n = __builtin_amdgcn_readfirstlane(find_sequence(p, tile_no, lane));
+    int64_t a, b;
+    query_bounds(p, n, a, b);
+    if (!set_tile(p, n, (tile_no - (a * p.G / ROWS + n)) * ROWS, t)) return;
+  }
+  // this lane's row
+  const int row = t.row0 + l16, token = row / p.G;
+  u32x4_t q[KS];
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) q[ks] = u32x4_t{0u, 0u, 0u, 0u};
+  if (row < t.rows) {
+    const u16* src =
+        p.q + (t.q0 + token) * p.q_row + (hk * p.G + row - token * p.G) * D + D / 4 * lg;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) q[ks] = *reinterpret_cast<const u32x4_t*>(src + 8 * ks);
+  }
   const int64_t slot = q4.slot != nullptr ? q4.slot[t.n] : t.n;
   if (slot < 0 || slot >= q4.c.slots) t.Lk = 0;
-
-  const int off = t.Lk - t.Lq;
+  const int off = t.Lk - t.Lq, last = row < t.rows ? token + off : -1;
   const int keys = max(0, min(t.Lk, (min(t.rows, t.row0 + ROWS) - 1) / p.G + off + 1));
   const int all_keys = t.row0 / p.G + off + 1;
   const int steps = (keys + kCache4Tile - 1) / kCache4Tile;
   const int first = min(steps, split * q4.part), end = min(steps, first + q4.part);
-  if (split > 0 && first == end) {  // no keys in this part: the join reads no outputs of it
-    for (int i = tid; i < ROWS; i += kAttnThreads) {
-      const int r = t.row0 + i;
-      if (r < t.rows) {
-        const int64_t at = (t.q0 + r / p.G) * p.Hq + hk * p.G + r % p.G;
-        const int64_t w = (int64_t)split * p.Tq_total * p.Hq + at;
-        *reinterpret_cast<f32x2_t*>(p.ws_ml + 2 * w) = f32x2_t{kNone, 0.f};
-      }
+  if (split > 0 && first == end) {  // no keys in this part: the join uses no outputs of it
+    if (tid < ROWS && row < t.rows) {
+      const int64_t at = (t.q0 + token) * p.Hq + hk * p.G + row - token * p.G;
+      *reinterpret_cast<f32x2_t*>(p.ws_ml + 2 * ((int64_t)split * p.Tq_total * p.Hq + at)) =
+          f32x2_t{kNone, 0.f};
     }
     return;
   }
 
-  u32x4_t q[KS][NI];
-  int last[NI];
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int r = t.row0 + 16 * i + l16;
-    last[i] = r < t.rows ? r / p.G + off : -1;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) q[ks][i] = u32x4_t{0u, 0u, 0u, 0u};
-    if (r < t.rows) {
-      const u16* src = p.q + (t.q0 + r / p.G) * p.q_row + (hk * p.G + r % p.G) * D + D / 4 * lg;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) q[ks][i] = *reinterpret_cast<const u32x4_t*>(src + 8 * ks);
-    }
-  }
-  const View4<D> view(q4.c, slot * p.Hk + hk, lane);
-  Step4<D> now = {}, next = {};
-  if (first + wave < end) now = view.load(first + wave);
-  end_loads(q);
-
-  Acc<D, NI> acc;
+  const View4<D, ONCE> view(q4.c, slot * p.Hk + hk, lane);
+  end_row_loads(q);
+  Acc<D, 1> acc;
   acc.init();
   bool odd = false;  // some step dropped infinities or NaN of v
-  for (int s = first + wave; s < end; s += WAVES) {
-    if (s + WAVES < end) next = view.load(s + WAVES);
-    f32x4_t x[2][NI];
+  auto step = [&](const Step4<D>& now, int s) {
+    f32x4_t x[2][1];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const float scale = scale_of(now.ks, j);
+      x[j][0] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < NI; ++i) x[j][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const u32x4_t k = eight_values(now.k[j][ks], scale);
-#pragma unroll
-        for (int i = 0; i < NI; ++i) x[j][i] = mfma(k, q[ks][i], x[j][i]);
-      }
+      for (int ks = 0; ks < KS; ++ks)
+        x[j][0] = mfma(eight_values(now.k[j][ks], scale), q[ks], x[j][0]);
     }
     bool drop = false;
     if ((s + 1) * kCache4Tile > all_keys) {  // some row does not see all of these keys
@@ -206,28 +279,22 @@ __global__ __launch_bounds__(kAttnThreads, NI == 1 ? 3 : 2) void attn4_kernel(
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int key = s * kCache4Tile + 16 * j + 4 * r + lg;
-            if (key > last[i]) x[j][i][r] = kNone;
-          }
+        for (int r = 0; r < 4; ++r)
+          if (s * kCache4Tile + 16 * j + 4 * r + lg > last) x[j][0][r] = kNone;
     }
     acc.raise(x, p.c);
     acc.exps(x[0], p.c);
     acc.exps(x[1], p.c);
     // p in two bf16 parts, its upper half and the rest.  No part of a positive p is zero, so an
     // infinity of v stays one.
-    u32x4_t pr[NI], pr2[NI];
+    u32x4_t pr, pr2;
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float lo = x[e >> 1][i][2 * (e & 1)], hi = x[e >> 1][i][2 * (e & 1) + 1];
-        pr[i][e] = __float_as_uint(lo) >> 16 | (__float_as_uint(hi) & 0xffff0000u);
-        pr2[i][e] = pack_bf16(__builtin_amdgcn_fmed3f(lo - bf_lo(pr[i][e]), 1.2e-38f, lo),
-                              __builtin_amdgcn_fmed3f(hi - bf_hi(pr[i][e]), 1.2e-38f, hi));
-      }
+    for (int e = 0; e < 4; ++e) {
+      const float lo = x[e >> 1][0][2 * (e & 1)], hi = x[e >> 1][0][2 * (e & 1) + 1];
+      pr[e] = __float_as_uint(lo) >> 16 | (__float_as_uint(hi) & 0xffff0000u);
+      pr2[e] = pack_bf16(__builtin_amdgcn_fmed3f(lo - bf_lo(pr[e]), 1.2e-38f, lo),
+                         __builtin_amdgcn_fmed3f(hi - bf_hi(pr[e]), 1.2e-38f, hi));
+    }
     auto products = [&](auto dropped) {
       each(
           [&](auto m) {
@@ -240,34 +307,48 @@ __global__ __launch_bounds__(kAttnThreads, NI == 1 ? 3 : 2) void attn4_kernel(
                 v.b[e] = odd_split(v.b[e]).finite;
               }
             }
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-              acc.o[2 * M][i] = mfma(v.a, pr2[i], acc.o[2 * M][i]);
-              acc.o[2 * M][i] = mfma(v.a, pr[i], acc.o[2 * M][i]);
-              acc.o[2 * M + 1][i] = mfma(v.b, pr2[i], acc.o[2 * M + 1][i]);
-              acc.o[2 * M + 1][i] = mfma(v.b, pr[i], acc.o[2 * M + 1][i]);
-            }
+            acc.o[2 * M][0] = mfma(v.a, pr2, acc.o[2 * M][0]);
+            acc.o[2 * M + 1][0] = mfma(v.b, pr2, acc.o[2 * M + 1][0]);
+            acc.o[2 * M][0] = mfma(v.a, pr, acc.o[2 * M][0]);
+            acc.o[2 * M + 1][0] = mfma(v.b, pr, acc.o[2 * M + 1][0]);
           },
           std::make_integer_sequence<int, DT / 2>{});
     };
     if (drop) products(std::true_type{});
     else products(std::false_type{});
-    now = next;
+  };
+
+  // kAhead tiles are on their way, or as many as are left
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (first + wave + i * WAVES < end) view.load(first + wave + i * WAVES, sm.tile[wave][i]);
+  int buf = 0;
+  for (int s = first + wave; s < end; s += WAVES) {
+    constexpr int L = View4<D, ONCE>::LOADS;
+    if (s + 2 * WAVES < end) wait_loads<2 * L>();
+    else if (s + WAVES < end) wait_loads<L>();
+    else wait_loads();
+    const Step4<D> now = view.read(sm.tile[wave][buf]);
+    step(now, s);
+    wait_lds();  // this tile's reads are done before its place is written again
+    if (s + kAhead * WAVES < end) view.load(s + kAhead * WAVES, sm.tile[wave][buf]);
+    buf = buf + 1 == kAhead ? 0 : buf + 1;
   }
 
   // what was dropped, after the loop, where it takes no registers from it
   for (int s = first + wave; odd && s < end; s += WAVES) {
     if ((s + 1) * kCache4Tile <= all_keys) continue;
-    now = view.load(s);
+    view.load(s, sm.tile[wave][0]);
+    wait_loads();
+    const Step4<D> now = view.read(sm.tile[wave][0]);
+    wait_lds();
     if (!may_be_odd<D>(now)) continue;
-    u32x4_t sees[NI];
+    u32x4_t sees;
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int k = s * kCache4Tile + lg + 16 * (e >> 1) + 8 * (e & 1);
-        sees[i][e] = (k <= last[i] ? 0x3f80u : 0u) | (k + 4 <= last[i] ? 0x3f800000u : 0u);
-      }
+    for (int e = 0; e < 4; ++e) {
+      const int k = s * kCache4Tile + lg + 16 * (e >> 1) + 8 * (e & 1);
+      sees[e] = (k <= last ? 0x3f80u : 0u) | (k + 4 <= last ? 0x3f800000u : 0u);
+    }
     each(
         [&](auto m) {
           constexpr int M = decltype(m)::value;
@@ -277,78 +358,62 @@ __global__ __launch_bounds__(kAttnThreads, NI == 1 ? 3 : 2) void attn4_kernel(
             v.a[e] = odd_split(v.a[e]).code;
             v.b[e] = odd_split(v.b[e]).code;
           }
+          const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+          const f32x4_t na = mfma(v.a, sees, zero), nb = mfma(v.b, sees, zero);
 #pragma unroll
-          for (int i = 0; i < NI; ++i) {
-            const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-            const f32x4_t na = mfma(v.a, sees[i], zero), nb = mfma(v.b, sees[i], zero);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              acc.o[2 * M][i][r] += odd_value(na[r]);
-              acc.o[2 * M + 1][i][r] += odd_value(nb[r]);
-            }
+          for (int r = 0; r < 4; ++r) {
+            acc.o[2 * M][0][r] += odd_value(na[r]);
+            acc.o[2 * M + 1][0][r] += odd_value(nb[r]);
           }
         },
         std::make_integer_sequence<int, DT / 2>{});
   }
 
-  // ---- join the waves: maxima and sums first, then the outputs, one 16-row tile at a time
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const float l = sum_over_groups(acc.l[i]);
-    if (lg == 0) {
-      sml[wave][16 * i + l16][0] = acc.m[i];
-      sml[wave][16 * i + l16][1] = l;
-    }
+  // ---- join the waves (behind the barrier every wave's reads of its tiles are done): maxima and sums first, then the outputs
+  const float l = sum_over_groups(acc.l[0]);
+  if (lg == 0) {
+    sml[wave][l16][0] = acc.m[0];
+    sml[wave][l16][1] = l;
   }
   lds_barrier();
+  float m = kNone;
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    float m = kNone;
+  for (int w = 0; w < WAVES; ++w) m = fmaxf(m, sml[w][l16][0]);
+  const float f = __builtin_amdgcn_exp2f(acc.m[0] - (m == kNone ? 0.f : m));
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) m = fmaxf(m, sml[w][16 * i + l16][0]);
-    const float f = __builtin_amdgcn_exp2f(acc.m[i] - (m == kNone ? 0.f : m));
+  for (int r = 0; r < 4; ++r)
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int e = 0; e < DT; e += 4)
-        *reinterpret_cast<f32x4_t*>(&so[wave][l16][DT * (4 * lg + r) + e]) =
-            f32x4_t{acc.o[e][i][r], acc.o[e + 1][i][r], acc.o[e + 2][i][r], acc.o[e + 3][i][r]} *
-            f;
-    lds_barrier();
-    // thread: row tid / TPT, D / TPT columns from (tid % TPT) * 4 in strides of 4 TPT
-    constexpr int TPT = kAttnThreads / 16;
-    const int rr = tid / TPT, r = t.row0 + 16 * i + rr;
+    for (int e = 0; e < DT; e += 4)
+      *reinterpret_cast<f32x4_t*>(&sm.o[wave][l16][DT * (4 * lg + r) + e]) =
+          f32x4_t{acc.o[e][0][r], acc.o[e + 1][0][r], acc.o[e + 2][0][r], acc.o[e + 3][0][r]} * f;
+  lds_barrier();
+  // a thread: four columns of a row
+  for (int i = tid; i < ROWS * D / 4; i += kAttnThreads) {
+    const int rr = i / (D / 4), c = i % (D / 4) * 4, r = t.row0 + rr;
+    if (r >= t.rows) break;
     float mr = kNone, lr = 0.f;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) mr = fmaxf(mr, sml[w][16 * i + rr][0]);
+    for (int w = 0; w < WAVES; ++w) mr = fmaxf(mr, sml[w][rr][0]);
     const float br = mr == kNone ? 0.f : mr;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w)
-      lr += sml[w][16 * i + rr][1] * __builtin_amdgcn_exp2f(sml[w][16 * i + rr][0] - br);
-    if (r < t.rows) {
-      const int64_t at = (t.q0 + r / p.G) * p.Hq + hk * p.G + r % p.G;
-      const int64_t w = (int64_t)split * p.Tq_total * p.Hq + at;
+      lr += sml[w][rr][1] * __builtin_amdgcn_exp2f(sml[w][rr][0] - br);
+    f32x4_t o = *reinterpret_cast<const f32x4_t*>(&sm.o[0][rr][c]);
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) o += *reinterpret_cast<const f32x4_t*>(&sm.o[w][rr][c]);
+    const int tk = r / p.G;
+    const int64_t at = (t.q0 + tk) * p.Hq + hk * p.G + r - tk * p.G;
+    const int64_t w = (int64_t)split * p.Tq_total * p.Hq + at;
+    if (p.splits > 1) {
+      *reinterpret_cast<f32x4_t*>(p.ws_o + w * D + c) = o;
+      if (c == 0) *reinterpret_cast<f32x2_t*>(p.ws_ml + 2 * w) = f32x2_t{mr, lr};
+    } else {
       const float g = lr > 0.f ? 1.f / lr : lr == 0.f ? 0.f : lr;
-#pragma unroll
-      for (int cc = 0; cc < D / (4 * TPT); ++cc) {
-        const int c = 4 * TPT * cc + 4 * (tid % TPT);
-        f32x4_t o = *reinterpret_cast<const f32x4_t*>(&so[0][rr][c]);
-#pragma unroll
-        for (int ww = 1; ww < WAVES; ++ww) o += *reinterpret_cast<const f32x4_t*>(&so[ww][rr][c]);
-        if (p.splits > 1) {
-          *reinterpret_cast<f32x4_t*>(p.ws_o + w * D + c) = o;
-        } else {
-          *reinterpret_cast<u32x2_t*>(p.out + at * D + c) =
-              u32x2_t{pack_bf16(o[0] * g, o[1] * g), pack_bf16(o[2] * g, o[3] * g)};
-        }
-      }
-      if (tid % TPT == 0) {
-        if (p.splits > 1) *reinterpret_cast<f32x2_t*>(p.ws_ml + 2 * w) = f32x2_t{mr, lr};
-        else if (p.lse != nullptr)
-          p.lse[at] = lr == 0.f ? kNone : (mr + __builtin_amdgcn_logf(lr)) * kLn2;
-      }
+      *reinterpret_cast<u32x2_t*>(p.out + at * D + c) =
+          u32x2_t{pack_bf16(o[0] * g, o[1] * g), pack_bf16(o[2] * g, o[3] * g)};
+      if (p.lse != nullptr && c == 0)
+        p.lse[at] = lr == 0.f ? kNone : (mr + __builtin_amdgcn_logf(lr)) * kLn2;
     }
-    if (i + 1 < NI) lds_barrier();
   }
 }
 
@@ -398,23 +463,19 @@ __global__ __launch_bounds__(kAttnThreads) void expand4_kernel(Attn4Params q4) {
 }
 
 template <int D>
-hipError_t go(const Attn4Params& p, int rows, hipStream_t stream) {
+hipError_t go(Attn4Params p, hipStream_t stream) {
   const AttnParams& a = p.a;
-  int64_t slots = attn_slots(a.Tq_total, a.N, a.G, rows);
-  if (a.cu_q == nullptr) slots = a.N * ((a.Tq * a.G + rows - 1) / rows);
+  p.row_tiles = (int32_t)((a.Tq * a.G + kAttn4Rows - 1) / kAttn4Rows);
+  const int64_t slots = a.cu_q == nullptr ? a.N * (int64_t)p.row_tiles
+                                          : attn_slots(a.Tq_total, a.N, a.G, kAttn4Rows);
   const dim3 grid((unsigned)(slots * a.Hk * a.splits));
-  if (rows == 16) attn4_kernel<D, 1><<<grid, kAttnThreads, 0, stream>>>(p);
-  else attn4_kernel<D, 2><<<grid, kAttnThreads, 0, stream>>>(p);
+  if (p.once) attn4_kernel<D, true><<<grid, kAttnThreads, 0, stream>>>(p);
+  else attn4_kernel<D, false><<<grid, kAttnThreads, 0, stream>>>(p);
   if (a.splits > 1) return launch_attn_join(a, D, stream);
   return hipGetLastError();
 }
 
 }  // namespace
-
-int attn4_rows(int64_t Tq_total, int64_t N, int64_t G) {
-  const int64_t mean = (Tq_total * G + N - 1) / N;  // rows of a sequence and key/value head
-  return mean <= 16 ? 16 : 32;
-}
 
 hipError_t launch_expand4(const Attn4Params& p, int D, hipStream_t stream) {
   const dim3 grid((unsigned)(p.a.N * (p.a.Tk / kCache4Tile) * p.a.Hk));
@@ -423,8 +484,8 @@ hipError_t launch_expand4(const Attn4Params& p, int D, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_attn4(const Attn4Params& p, int rows, int D, hipStream_t stream) {
-  return D == 64 ? go<64>(p, rows, stream) : go<128>(p, rows, stream);
+hipError_t launch_attn4(const Attn4Params& p, int D, hipStream_t stream) {
+  return D == 64 ? go<64>(p, stream) : go<128>(p, stream);
 }
 
 }  // namespace kda

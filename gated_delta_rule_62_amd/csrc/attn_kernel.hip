@@ -89,49 +89,6 @@ __device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t off
   return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
-// The same descriptor as four words, for load_lds.
-__device__ __forceinline__ u32x4_t rows_words(const u16* base, int64_t row, int tokens, int D) {
-  const uint64_t at = reinterpret_cast<uint64_t>(base);
-  const uint32_t bytes = tokens > 0 ? (uint32_t)(tokens - 1) * (uint32_t)(row * 2) + D * 2u : 0u;
-  return u32x4_t{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at),
-                 (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32) & 0xffffu),
-                 (uint32_t)__builtin_amdgcn_readfirstlane(bytes), 0x00020000u};
-}
-
-// 16 bytes per lane from memory to LDS: lane l's land 16 l bytes behind `to` (uniform);
-// zeros where `off` is behind the descriptor's end.  It has no result the compiler could
-// track: wait_loads ends it, and a barrier shows it to the other waves.  ONCE (non-temporal)
-// is for what one workgroup alone reads as a rule, so that it does not displace what others do.
-template <bool ONCE>
-__device__ __forceinline__ void load_lds(u32x4_t rsrc, const u16* to, uint32_t off) {
-  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const u16*)to;
-  const uint32_t m0 = (uint32_t)__builtin_amdgcn_readfirstlane(at);
-  if constexpr (ONCE)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
-                 :
-                 : "s"(m0), "v"(off), "s"(rsrc)
-                 : "memory", "m0");
-  else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :
-                 : "s"(m0), "v"(off), "s"(rsrc)
-                 : "memory", "m0");
-}
-
-// Waits until at most the N youngest of this wave's vector memory accesses are in flight, and
-// until its LDS accesses are done.  The compiler moves no access over either.
-template <int N = 0>
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | (N >> 4 << 14));
-  asm volatile("" ::: "memory");
-}
-__device__ __forceinline__ void wait_lds() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0xc07f);
-  asm volatile("" ::: "memory");
-}
-
 // Probability tiles 2 js and 2 js + 1 as the operand of 32 keys.
 __device__ __forceinline__ u32x4_t p_op(f32x4_t a, f32x4_t b) {
   return u32x4_t{pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(b[0], b[1]),
@@ -602,8 +559,8 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_token_kernel(AttnParams 
 }
 
 // Joins the splits of a row, one wave per (query token, head): lane s weighs split s (there
-// are at most 64), then the lanes share the row's D values.  GAPS: a split without keys has no
-// outputs to read.
+// are at most 64), then the lanes share the row's D values.  GAPS: what the outputs of a
+// split without keys hold is loaded (the loads do not wait for the sums) but not used.
 template <int D, bool GAPS>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
   constexpr int V = D / 64;  // values per lane
@@ -612,31 +569,36 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
   const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int64_t rows = p.Tq_total * p.Hq;
   if (at >= rows) return;
-  if (p.cu_q != nullptr) {  // a query outside every sequence keeps its rows
-    const int64_t token = at / p.Hq;
-    if (token < p.cu_q[0] || token >= p.cu_q[p.N]) return;
+  // every load that does not wait for another one first
+  bool there = true;  // a query outside every sequence keeps its rows
+  if (p.cu_q != nullptr) {
+    const int64_t token = (uint32_t)at / (uint32_t)p.Hq;  // split calls have fewer than 2^26 rows
+    there = token >= p.cu_q[0] && token < p.cu_q[p.N];
   }
   f32x2_t ml = {kNone, 0.f};
   if (lane < p.splits) ml = *reinterpret_cast<const f32x2_t*>(p.ws_ml + 2 * (lane * rows + at));
-  const uint64_t filled = GAPS ? __ballot(!(ml[0] == kNone && ml[1] == 0.f)) : ~0ull;
-  float m = ml[0];
-#pragma unroll
-  for (int x = 1; x < 64; x *= 2) m = fmaxf(m, __shfl_xor(m, x));
-  const float f = __builtin_amdgcn_exp2f(ml[0] - (m == kNone ? 0.f : m));
-  float l = ml[1] * f;
-#pragma unroll
-  for (int x = 1; x < 64; x *= 2) l += __shfl_xor(l, x);
   const float* o = p.ws_o + at * D + lane * V;
+  vec x[8];  // eight loads in flight
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x[i] = s0 + i < p.splits ? *reinterpret_cast<const vec*>(o + (s0 + i) * rows * D) : vec{};
+  };
+  load(0);
+  const uint64_t filled = GAPS ? __ballot(!(ml[0] == kNone && ml[1] == 0.f)) : ~0ull;
+  const float m = wave_max(ml[0]);
+  const float f = __builtin_amdgcn_exp2f(ml[0] - (m == kNone ? 0.f : m));
+  const float l = wave_sum(ml[1] * f);
   vec sum = {};
-  for (int s0 = 0; s0 < p.splits; s0 += 8) {  // eight loads in flight
-    vec x[8];
+  for (int s0 = 0; s0 < p.splits; s0 += 8) {
+    if (s0 > 0) load(s0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      x[i] = s0 + i < p.splits && (filled >> (s0 + i) & 1) ? *reinterpret_cast<const vec*>(o + (s0 + i) * rows * D) : vec{};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 8; ++i) {
+      if (GAPS && !(filled >> ((s0 + i) & 63) & 1)) x[i] = vec{};
       sum += x[i] * __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), (s0 + i) & 63));
+    }
   }
+  if (!there) return;
   const float g = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
   u16* out = p.out + at * D + lane * V;
   if constexpr (V == 2) *reinterpret_cast<unsigned*>(out) = pack_bf16(sum[0] * g, sum[1] * g);

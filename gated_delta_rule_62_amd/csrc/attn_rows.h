@@ -103,6 +103,50 @@ __device__ __forceinline__ void end_loads(u32x4_t (&q)[KS][NI]) {
     for (int i = 0; i < NI; ++i) asm volatile("" : "+v"(q[ks][i]));
 }
 
+// Descriptor of `tokens` rows of one head from `base` as four words, for load_lds; nothing when
+// there are none.
+__device__ __forceinline__ u32x4_t rows_words(const u16* base, int64_t row, int tokens, int D) {
+  const uint64_t at = reinterpret_cast<uint64_t>(base);
+  const uint32_t bytes = tokens > 0 ? (uint32_t)(tokens - 1) * (uint32_t)(row * 2) + D * 2u : 0u;
+  return u32x4_t{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32) & 0xffffu),
+                 (uint32_t)__builtin_amdgcn_readfirstlane(bytes), 0x00020000u};
+}
+
+// 16 bytes per lane from memory to LDS: lane l's land 16 l bytes behind `to` (uniform);
+// zeros where `off` is behind the descriptor's end.  It has no result the compiler could
+// track: wait_loads ends it, and a barrier shows it to the other waves.  ONCE (non-temporal)
+// is for what one workgroup alone reads as a rule, so that it does not displace what others do.
+template <bool ONCE>
+__device__ __forceinline__ void load_lds(u32x4_t rsrc, const u16* to, uint32_t off) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const u16*)to;
+  const uint32_t m0 = (uint32_t)__builtin_amdgcn_readfirstlane(at);
+  if constexpr (ONCE)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
+                 :
+                 : "s"(m0), "v"(off), "s"(rsrc)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(m0), "v"(off), "s"(rsrc)
+                 : "memory", "m0");
+}
+
+// Waits until at most the N youngest of this wave's vector memory accesses are in flight, and
+// until its LDS accesses are done.  The compiler moves no access over either.
+template <int N = 0>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | (N >> 4 << 14));
+  asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void wait_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);
+  asm volatile("" ::: "memory");
+}
+
 // Row state and output tiles of NI 16-row tiles: lane = row l16, d = 16 dt + 4 lg + i.
 template <int D, int NI>
 struct Acc {

@@ -76,6 +76,22 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
+// Sum and maximum over the wave, in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+  const Two t = swap32(group_sum<32>(v));
+  return t.a + t.b;
+}
+__device__ __forceinline__ float wave_max(float v) {
+  v = fmaxf(v, dpp<0xB1>(v));
+  v = fmaxf(v, dpp<0x4E>(v));
+  v = fmaxf(v, dpp<0x141>(v));
+  v = fmaxf(v, dpp<0x140>(v));
+  Two t = swap16(v);
+  v = fmaxf(t.a, t.b);
+  t = swap32(v);
+  return fmaxf(t.a, t.b);
+}
+
 // Raw buffer descriptor over [base, base + bytes): loads past the end return zero and
 // stores past it are dropped.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {

@@ -189,22 +189,30 @@ int put4_check(const void* k, int64_t k_row, const void* v, int64_t v_row, const
   return KDA_OK;
 }
 
-// How a kda_attn4_fwd call runs: keys in parts of `part` straight from the cache, rows16 16-row
-// tiles a workgroup; or (expand) keys and values to a bf16 workspace first and then the kernel of
+// How a kda_attn4_fwd call runs: keys in parts of `part` straight from the cache; or
+// (expand) keys and values to a bf16 workspace first and then the kernel of
 // kda_attn_fwd's prompts with `splits` parts of each row's keys.
 struct Plan4 {
   bool expand;
-  int rows;
   int64_t part, splits;
   kda::AttnSchedule sched;
   int64_t bytes;  // of the workspace
 };
 
-// Keys of a part when the caller leaves the choice.
+// Keys of a part when the caller leaves the choice, for `units` (tile of rows, key/value head)
+// pairs: as many workgroups as fit at once, three a compute unit, and at least 1024 keys a part, or
+// 2048 when every second unit has a workgroup anyway (8192 positions, 8 heads a token, D 128, one
+// part and the chosen ones: 1 sequence of 32768 positions 194 and 16 us, 8 sequences 51 and 14,
+// 32 sequences 52 and 39; 64 sequences of 2048 positions: 16.4, 18.0 in two).  Lengths differ, so
+// parts are of equally many keys, not as many for each sequence.
 int64_t attn4_auto_part(int64_t units, int64_t cap) {
-  int64_t part = 1024;
-  while (cap > 64 * part) part *= 2;
-  return cap <= 1024 ? cap : part;
+  const int64_t cus = kda::device_cus(), least = 2 * units < cus ? 1024 : 2048;
+  int64_t parts = units > 0 ? 3 * cus / units : 1;
+  if (parts > cap / least) parts = cap / least;
+  if (parts > 64) parts = 64;
+  if (parts < 1) parts = 1;
+  const int64_t part = (cap + parts - 1) / parts;
+  return (part + kCache4Tile - 1) / kCache4Tile * kCache4Tile;
 }
 
 constexpr int64_t kExpandMax = (int64_t)8 << 30;  // bytes of expanded keys and values, at most
@@ -229,8 +237,7 @@ int attn4_plan(int64_t N, int64_t Bq, int64_t Tq, int64_t cap, int64_t Hq, int64
   if (part < 0 || part % kCache4Tile != 0 || (part && (cap + part - 1) / part > 64))
     return KDA_ERR_BAD_SCHEDULE;
   const int64_t G = Hq / Hk, total = Bq * Tq, most = kMostItems / kda::kAttnThreads;
-  plan->rows = kda::attn4_rows(total, N, G);
-  const int64_t tiles = kda::attn_slots(total, N, G, plan->rows) + (Bq == N ? N : 0);
+  const int64_t tiles = kda::attn_slots(total, N, G, kda::kAttn4Rows) + (Bq == N ? N : 0);
   if (tiles > most / Hk) return KDA_ERR_BAD_SHAPE;
   plan->expand = false;
   plan->splits = 1;
@@ -249,7 +256,9 @@ int attn4_plan(int64_t N, int64_t Bq, int64_t Tq, int64_t cap, int64_t Hq, int64
     plan->bytes = N * cap * row_bytes + round16(N * 8) + parts_bytes(sp, total * Hq, D);
     return KDA_OK;
   }
-  int64_t pt = part ? part : workspace ? attn4_auto_part(tiles * Hk, cap) : cap;
+  const int64_t units = Bq == N ? N * ((Tq * G + kda::kAttn4Rows - 1) / kda::kAttn4Rows) * Hk
+                                : tiles * Hk;
+  int64_t pt = part ? part : workspace ? attn4_auto_part(units, cap) : cap;
   if (pt > cap) pt = cap;
   const int64_t parts = (cap + pt - 1) / pt;
   if (parts > 1 && (tiles * Hk > most / parts || total > 4 * most / Hq)) {
@@ -483,6 +492,9 @@ int kda_attn4_fwd(const void* q, int64_t q_row, const void* k4, const void* ks, 
   p.c = cache_of(k4, ks, v4, vs, num_slots, cap);
   p.slot = slots;
   p.part = static_cast<int32_t>(plan.part / kCache4Tile);
+  // loads that do not stay in the caches: 10% of a batch of single tokens over long caches, but
+  // several tiles of rows read a sequence's keys from there (their times rise by up to a sixth)
+  p.once = a.Tq_total * a.G <= num_seqs * kda::kAttn4Rows;
   hipStream_t const on = static_cast<hipStream_t>(stream);
   a.splits = static_cast<int32_t>(plan.expand ? plan.splits : (cap + plan.part - 1) / plan.part);
   char* ws = static_cast<char*>(workspace);
@@ -497,7 +509,7 @@ int kda_attn4_fwd(const void* q, int64_t q_row, const void* k4, const void* ks, 
     a.ws_o = reinterpret_cast<float*>(ws);
     a.ws_ml = a.ws_o + a.splits * a.Tq_total * Hq * D;
   }
-  if (!plan.expand) return status(kda::launch_attn4(p, plan.rows, static_cast<int>(D), on));
+  if (!plan.expand) return status(kda::launch_attn4(p, static_cast<int>(D), on));
   const hipError_t e = kda::launch_expand4(p, static_cast<int>(D), on);
   if (e != hipSuccess) return status(e);
   a.k = p.k_ws;

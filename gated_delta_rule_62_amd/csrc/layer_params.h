@@ -97,13 +97,14 @@ struct Attn4Params {
   uint16_t* k_ws;          // expanded keys and values [N, cap, Hk, D] (many rows)
   uint16_t* v_ws;
   int64_t* lens;           // [N] their lengths
+  int32_t row_tiles;       // tiles of rows of a batch row
+  int32_t once;            // one tile of rows a sequence: its keys are read once
 };
 // Rows of a sequence and key/value head from which on keys and values are expanded.
 constexpr int kExpand4Rows = 128;
-// Rows per workgroup of a call: 16 or 32.
-int attn4_rows(int64_t Tq_total, int64_t N, int64_t G);
+constexpr int kAttn4Rows = 16;  // rows of a workgroup
 hipError_t launch_expand4(const Attn4Params& p, int D, hipStream_t stream);
-hipError_t launch_attn4(const Attn4Params& p, int rows, int D, hipStream_t stream);
+hipError_t launch_attn4(const Attn4Params& p, int D, hipStream_t stream);
 
 }  // namespace kda
 

@@ -72,7 +72,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormParams 
 
   // a sum over the row's threads
   auto row_sum = [&](float v, int which) {
-    v = lanes_sum(v, 64);
+    v = wave_sum(v);
     if constexpr (WAVES > 1) {
       if ((tid & 63) == 0) part[which][t >> 6] = v;
       lds_barrier();
