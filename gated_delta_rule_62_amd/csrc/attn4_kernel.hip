@@ -26,21 +26,18 @@ namespace {
 
 using namespace dev;
 
-// A lane's codes and scales of 32 keys.
+// A lane's codes and scales of a tile of 32 keys: D / 4 channels of two keys, and D / 16 of the values
+// at eight.
 template <int D>
-struct Step4;
-template <>
-struct Step4<128> {
-  u32x4_t k[2], v[2];
-  u32x2_t vs;
-  unsigned ks;
+struct Keys4 {
+  typedef unsigned part __attribute__((ext_vector_type(D / 32)));
+  part k[2];
+  unsigned scale;
 };
-template <>
-struct Step4<64> {
-  u32x2_t k[2];
-  u32x4_t v;
-  u32x2_t vs;
-  unsigned ks;
+template <int D>
+struct Values4 {
+  u32x4_t v[D / 64];
+  u32x2_t scale;
 };
 
 // One word a lane from memory to LDS, as load_lds.
@@ -110,36 +107,42 @@ struct View4 {
     }
     load_lds_word<ONCE>(sc + (int64_t)tile * D, to.s);
   }
-  __device__ __forceinline__ Step4<D> read(const Tile4<D>& from) const {
-    Step4<D> s;
+  __device__ __forceinline__ Keys4<D> keys(const Tile4<D>& from) const {
+    Keys4<D> s;
     if constexpr (D == 128) {
       s.k[0] = *reinterpret_cast<const u32x4_t*>(from.k + k_lds);
       s.k[1] = *reinterpret_cast<const u32x4_t*>(from.k + k_lds + 1024);
-      s.v[0] = *reinterpret_cast<const u32x4_t*>(from.v + v_at);
-      s.v[1] = *reinterpret_cast<const u32x4_t*>(from.v + v_at + 1024);
     } else {
       s.k[0] = *reinterpret_cast<const u32x2_t*>(from.k + k_lds);
       s.k[1] = *reinterpret_cast<const u32x2_t*>(from.k + k_lds + 512);
-      s.v = *reinterpret_cast<const u32x4_t*>(from.v + v_at);
     }
-    s.ks = *reinterpret_cast<const u16*>(from.s + ks_lds);
-    s.vs = *reinterpret_cast<const u32x2_t*>(from.s + vs_lds);
+    s.scale = *reinterpret_cast<const u16*>(from.s + ks_lds);
+    return s;
+  }
+  __device__ __forceinline__ Values4<D> values(const Tile4<D>& from) const {
+    Values4<D> s;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i)
+      s.v[i] = *reinterpret_cast<const u32x4_t*>(from.v + v_at + 1024 * i);
+    s.scale = *reinterpret_cast<const u32x2_t*>(from.s + vs_lds);
     return s;
   }
 };
 
-// Codes of channels D/16 c .. at key 16 j + 4 i + g, from bit 0.
-__device__ __forceinline__ unsigned v_codes(const Step4<128>& s, int j, int i) {
-  return s.v[j][i];
-}
-__device__ __forceinline__ unsigned v_codes(const Step4<64>& s, int j, int i) {
-  const unsigned w = s.v[2 * j + (i >> 1)];
-  return i & 1 ? w >> 16 : w;
+// Codes of channels D/16 c .. at key 16 j + 4 i + g, from bit 0, and their scale.
+template <int D>
+__device__ __forceinline__ unsigned v_codes(const Values4<D>& s, int j, int i) {
+  if constexpr (D == 128) {
+    return s.v[j][i];
+  } else {
+    const unsigned w = s.v[0][2 * j + (i >> 1)];
+    return i & 1 ? w >> 16 : w;
+  }
 }
 template <int D>
-__device__ __forceinline__ float v_scale(const Step4<D>& s, int j, int i) {
+__device__ __forceinline__ float v_scale(const Values4<D>& s, int j, int i) {
   const int byte = 2 * i + j;
-  return scale_of(s.vs[byte >> 2], byte & 3);
+  return scale_of(s.scale[byte >> 2], byte & 3);
 }
 
 // Operands of out^T's products 2 M and 2 M + 1.
@@ -147,13 +150,13 @@ struct VOps {
   u32x4_t a, b;
 };
 template <int D, int M>
-__device__ __forceinline__ VOps v_ops(const Step4<D>& s) {
+__device__ __forceinline__ VOps v_ops(const Values4<D>& s) {
   VOps r;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int j = e >> 1, i = 2 * (e & 1);
-    const unsigned lo = two_values<M>(v_codes(s, j, i), v_scale<D>(s, j, i)),
-                   hi = two_values<M>(v_codes(s, j, i + 1), v_scale<D>(s, j, i + 1));
+    const unsigned lo = two_values<M>(v_codes<D>(s, j, i), v_scale<D>(s, j, i)),
+                   hi = two_values<M>(v_codes<D>(s, j, i + 1), v_scale<D>(s, j, i + 1));
     r.a[e] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
     r.b[e] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
   }
@@ -166,11 +169,11 @@ __device__ __forceinline__ void each(F f, std::integer_sequence<int, M...>) {
 
 // Whether a scale of these values may give infinities or NaN (a byte of 252 and more).
 template <int D>
-__device__ __forceinline__ bool may_be_odd(const Step4<D>& s) {
+__device__ __forceinline__ bool may_be_odd(const Values4<D>& s) {
   bool any = false;
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    const unsigned z = ~s.vs[w] & 0xfcfcfcfcu;  // a zero byte where the six bits are ones
+    const unsigned z = ~s.scale[w] & 0xfcfcfcfcu;  // a zero byte where the six bits are ones
     any |= ((z - 0x01010101u) & ~z & 0x80808080u) != 0u;
   }
   return __any(any);
@@ -201,12 +204,12 @@ __device__ __forceinline__ int find_sequence(const AttnParams& p, unsigned slot,
 }
 
 template <int D, bool ONCE>
-__global__ __launch_bounds__(kAttnThreads, 3) void attn4_kernel(Attn4Params q4) {
+__global__ __launch_bounds__(kAttnThreads, 2) void attn4_kernel(Attn4Params q4) {
   constexpr int KS = D / 32, DT = D / 16, ROWS = kAttn4Rows, WAVES = kAttnThreads / 64;
-  constexpr int kAhead = 3;  // tiles of a wave on their way
+  constexpr int AHEAD = 2;  // pairs of tiles of a wave on their way
   constexpr int LO = D + 4;  // row stride of the join buffer (floats)
   union Smem {
-    Tile4<D> tile[WAVES][kAhead];
+    Tile4<D> tile[WAVES][AHEAD][2];
     float o[WAVES][ROWS][LO];
   };
   __shared__ alignas(16) Smem sm;
@@ -261,56 +264,71 @@ __global__ __launch_bounds__(kAttnThreads, 3) void attn4_kernel(Attn4Params q4) 
   Acc<D, 1> acc;
   acc.init();
   bool odd = false;  // some step dropped infinities or NaN of v
-  auto step = [&](const Step4<D>& now, int s) {
-    f32x4_t x[2][1];
+  // One step: a pair of tiles, the second there or not.  Two tiles at once give the matrix products,
+  // exponentials and conversions twice the independent work to fill their latencies with.
+  const int limit = min(last, end * kCache4Tile - 1);
+  const int all = min(all_keys, end * kCache4Tile);
+  auto step = [&](const Tile4<D> (&tile)[2], int s) {
+    f32x4_t x[4][1];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float scale = scale_of(now.ks, j);
-      x[j][0] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int h = 0; h < 2; ++h) {
+      const Keys4<D> k = view.keys(tile[h]);
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-        x[j][0] = mfma(eight_values(now.k[j][ks], scale), q[ks], x[j][0]);
+      for (int j = 0; j < 2; ++j) {
+        const float scale = scale_of(k.scale, j);
+        f32x4_t y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) y = mfma(eight_values(k.k[j][ks], scale), q[ks], y);
+        x[2 * h + j][0] = y;
+      }
     }
+    const Values4<D> v[2] = {view.values(tile[0]), view.values(tile[1])};
     bool drop = false;
-    if ((s + 1) * kCache4Tile > all_keys) {  // some row does not see all of these keys
+    if ((s + 2) * kCache4Tile > all) {  // some row does not see all of these keys
       asm volatile("");  // keeps this a branch
-      drop = may_be_odd<D>(now);
+      drop = may_be_odd<D>(v[0]) || may_be_odd<D>(v[1]);
       odd |= drop;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (s * kCache4Tile + 16 * j + 4 * r + lg > last) x[j][0][r] = kNone;
+          if (s * kCache4Tile + 16 * j + 4 * r + lg > limit) x[j][0][r] = kNone;
     }
     acc.raise(x, p.c);
-    acc.exps(x[0], p.c);
-    acc.exps(x[1], p.c);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc.exps(x[j], p.c);
     // p in two bf16 parts, its upper half and the rest.  No part of a positive p is zero, so an
     // infinity of v stays one.
-    u32x4_t pr, pr2;
+    u32x4_t pr[2], pr2[2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float lo = x[e >> 1][0][2 * (e & 1)], hi = x[e >> 1][0][2 * (e & 1) + 1];
-      pr[e] = __float_as_uint(lo) >> 16 | (__float_as_uint(hi) & 0xffff0000u);
-      pr2[e] = pack_bf16(__builtin_amdgcn_fmed3f(lo - bf_lo(pr[e]), 1.2e-38f, lo),
-                         __builtin_amdgcn_fmed3f(hi - bf_hi(pr[e]), 1.2e-38f, hi));
-    }
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float lo = x[2 * h + (e >> 1)][0][2 * (e & 1)],
+                    hi = x[2 * h + (e >> 1)][0][2 * (e & 1) + 1];
+        pr[h][e] = __float_as_uint(lo) >> 16 | (__float_as_uint(hi) & 0xffff0000u);
+        pr2[h][e] = pack_bf16(__builtin_amdgcn_fmed3f(lo - bf_lo(pr[h][e]), 1.2e-38f, lo),
+                              __builtin_amdgcn_fmed3f(hi - bf_hi(pr[h][e]), 1.2e-38f, hi));
+      }
     auto products = [&](auto dropped) {
       each(
           [&](auto m) {
             constexpr int M = decltype(m)::value;
-            VOps v = v_ops<D, M>(now);
-            if constexpr (decltype(dropped)::value) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                v.a[e] = odd_split(v.a[e]).finite;
-                v.b[e] = odd_split(v.b[e]).finite;
+            for (int h = 0; h < 2; ++h) {
+              VOps o = v_ops<D, M>(v[h]);
+              if constexpr (decltype(dropped)::value) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  o.a[e] = odd_split(o.a[e]).finite;
+                  o.b[e] = odd_split(o.b[e]).finite;
+                }
               }
+              acc.o[2 * M][0] = mfma(o.a, pr2[h], acc.o[2 * M][0]);
+              acc.o[2 * M + 1][0] = mfma(o.b, pr2[h], acc.o[2 * M + 1][0]);
+              acc.o[2 * M][0] = mfma(o.a, pr[h], acc.o[2 * M][0]);
+              acc.o[2 * M + 1][0] = mfma(o.b, pr[h], acc.o[2 * M + 1][0]);
             }
-            acc.o[2 * M][0] = mfma(v.a, pr2, acc.o[2 * M][0]);
-            acc.o[2 * M + 1][0] = mfma(v.b, pr2, acc.o[2 * M + 1][0]);
-            acc.o[2 * M][0] = mfma(v.a, pr, acc.o[2 * M][0]);
-            acc.o[2 * M + 1][0] = mfma(v.b, pr, acc.o[2 * M + 1][0]);
           },
           std::make_integer_sequence<int, DT / 2>{});
     };
@@ -318,31 +336,32 @@ __global__ __launch_bounds__(kAttnThreads, 3) void attn4_kernel(Attn4Params q4) 
     else products(std::false_type{});
   };
 
-  // kAhead tiles are on their way, or as many as are left
+  // AHEAD pairs are on their way, or what is left; a missing second tile takes the first's place
+  auto load = [&](int s, Tile4<D> (&to)[2]) {
+    view.load(s, to[0]);
+    view.load(min(s + 1, end - 1), to[1]);
+  };
+  constexpr int NEXT = 2 * WAVES, L = 2 * View4<D, ONCE>::LOADS;
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i)
-    if (first + wave + i * WAVES < end) view.load(first + wave + i * WAVES, sm.tile[wave][i]);
+  for (int i = 0; i < AHEAD; ++i)
+    if (first + 2 * wave + i * NEXT < end) load(first + 2 * wave + i * NEXT, sm.tile[wave][i]);
   int buf = 0;
-  for (int s = first + wave; s < end; s += WAVES) {
-    constexpr int L = View4<D, ONCE>::LOADS;
-    if (s + 2 * WAVES < end) wait_loads<2 * L>();
-    else if (s + WAVES < end) wait_loads<L>();
+  for (int s = first + 2 * wave; s < end; s += NEXT, buf ^= 1) {
+    if (s + NEXT < end) wait_loads<L>();
     else wait_loads();
-    const Step4<D> now = view.read(sm.tile[wave][buf]);
-    step(now, s);
-    wait_lds();  // this tile's reads are done before its place is written again
-    if (s + kAhead * WAVES < end) view.load(s + kAhead * WAVES, sm.tile[wave][buf]);
-    buf = buf + 1 == kAhead ? 0 : buf + 1;
+    step(sm.tile[wave][buf], s);
+    wait_lds();  // this pair's reads are done before its place is written again
+    if (s + AHEAD * NEXT < end) load(s + AHEAD * NEXT, sm.tile[wave][buf]);
   }
 
   // what was dropped, after the loop, where it takes no registers from it
-  for (int s = first + wave; odd && s < end; s += WAVES) {
-    if ((s + 1) * kCache4Tile <= all_keys) continue;
-    view.load(s, sm.tile[wave][0]);
+  for (int pair = first + 2 * wave, s = pair; odd && s < end; s = s == pair ? s + 1 : pair += NEXT) {
+    if ((pair + 2) * kCache4Tile <= all) continue;
+    view.load(s, sm.tile[wave][0][0]);
     wait_loads();
-    const Step4<D> now = view.read(sm.tile[wave][0]);
+    const Values4<D> v = view.values(sm.tile[wave][0][0]);
     wait_lds();
-    if (!may_be_odd<D>(now)) continue;
+    if (!may_be_odd<D>(v)) continue;
     u32x4_t sees;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -352,14 +371,14 @@ __global__ __launch_bounds__(kAttnThreads, 3) void attn4_kernel(Attn4Params q4) 
     each(
         [&](auto m) {
           constexpr int M = decltype(m)::value;
-          VOps v = v_ops<D, M>(now);
+          VOps o = v_ops<D, M>(v);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            v.a[e] = odd_split(v.a[e]).code;
-            v.b[e] = odd_split(v.b[e]).code;
+            o.a[e] = odd_split(o.a[e]).code;
+            o.b[e] = odd_split(o.b[e]).code;
           }
           const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-          const f32x4_t na = mfma(v.a, sees, zero), nb = mfma(v.b, sees, zero);
+          const f32x4_t na = mfma(o.a, sees, zero), nb = mfma(o.b, sees, zero);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             acc.o[2 * M][0][r] += odd_value(na[r]);

@@ -200,19 +200,25 @@ struct Plan4 {
 };
 
 // Keys of a part when the caller leaves the choice, for `units` (tile of rows, key/value head)
-// pairs: as many workgroups as fit at once, three a compute unit, and at least 1024 keys a part, or
-// 2048 when every second unit has a workgroup anyway (8192 positions, 8 heads a token, D 128, one
-// part and the chosen ones: 1 sequence of 32768 positions 194 and 16 us, 8 sequences 51 and 14,
-// 32 sequences 52 and 39; 64 sequences of 2048 positions: 16.4, 18.0 in two).  Lengths differ, so
-// parts are of equally many keys, not as many for each sequence.
-int64_t attn4_auto_part(int64_t units, int64_t cap) {
-  const int64_t cus = kda::device_cus(), least = 2 * units < cus ? 1024 : 2048;
-  int64_t parts = units > 0 ? 3 * cus / units : 1;
-  if (parts > cap / least) parts = cap / least;
+// pairs.  Parts are of equally many keys, not as many for each sequence, whose lengths differ.
+// Few units: at least 1024 keys (8192 positions and more, 8 heads a token, D 128, in one part and
+// in parts of 1024, 512: 1 sequence 168, 14.7, 14.9 us, 8 sequences 45, 12.7, 13.5).  When every
+// second compute unit has a workgroup anyway: none of 2048 positions or fewer (64 sequences 15.5,
+// 18.2 in two), else at least 1536 with D 128 (32 sequences of 8192 in one part 46, parts of 4096,
+// 1536, 1024: 43, 39.8, 41.5) and 1024 with D 64 (16 sequences, 40 rows, of 4096: 21, 20 in two
+// parts, 17.1 in four).  None from two units a compute unit on (32 sequences of 4096, 32 rows: 37.6,
+// 49 in four).
+int64_t attn4_auto_part(int64_t units, int64_t cap, int64_t D) {
+  const int64_t cus = kda::device_cus();
+  const bool many = 2 * units >= cus;
+  if (units >= 2 * cus || (many && cap <= 2048)) return cap;
+  int64_t parts = units > 0 ? 5 * cus / units : 1;
+  const int64_t most = cap / (many && D == 128 ? 1536 : 1024);
+  if (parts > most) parts = most;
   if (parts > 64) parts = 64;
   if (parts < 1) parts = 1;
   const int64_t part = (cap + parts - 1) / parts;
-  return (part + kCache4Tile - 1) / kCache4Tile * kCache4Tile;
+  return (part + 63) / 64 * 64;
 }
 
 constexpr int64_t kExpandMax = (int64_t)8 << 30;  // bytes of expanded keys and values, at most
@@ -241,9 +247,15 @@ int attn4_plan(int64_t N, int64_t Bq, int64_t Tq, int64_t cap, int64_t Hq, int64
   if (tiles > most / Hk) return KDA_ERR_BAD_SHAPE;
   plan->expand = false;
   plan->splits = 1;
-  // (row, key/value head) pairs a sequence, and whether its keys may be expanded
+  const int64_t units = Bq == N ? N * ((Tq * G + kda::kAttn4Rows - 1) / kda::kAttn4Rows) * Hk
+                                : tiles * Hk;
+  // Expanded keys pay from some 450 rows of a sequence and key/value head on (32 sequences of 4096
+  // positions, 8 heads, D 128, 256 rows: 241 us, from the cache 210; 512 rows: 376 and 405), and
+  // only where their tiles fill the device many times over (1 sequence of 8192, 512 rows: 36 and
+  // 21, 2048 rows: 52 and 60; 3 sequences of 2208, D 64, 1024 rows: 45 and 32, 2048 rows: 53, 57).
   const int64_t row_bytes = Hk * D * 4;
   if (part == 0 && workspace && total * G > N * kda::kExpand4Rows &&
+      units > (D == 128 ? 3 : 8) * kda::device_cus() &&
       Hk * D < (1 << 24) && N <= kExpandMax / row_bytes / cap &&
       N * Hk <= most / (cap / kCache4Tile)) {
     plan->expand = true;
@@ -256,9 +268,7 @@ int attn4_plan(int64_t N, int64_t Bq, int64_t Tq, int64_t cap, int64_t Hq, int64
     plan->bytes = N * cap * row_bytes + round16(N * 8) + parts_bytes(sp, total * Hq, D);
     return KDA_OK;
   }
-  const int64_t units = Bq == N ? N * ((Tq * G + kda::kAttn4Rows - 1) / kda::kAttn4Rows) * Hk
-                                : tiles * Hk;
-  int64_t pt = part ? part : workspace ? attn4_auto_part(units, cap) : cap;
+  int64_t pt = part ? part : workspace ? attn4_auto_part(units, cap, D) : cap;
   if (pt > cap) pt = cap;
   const int64_t parts = (cap + pt - 1) / pt;
   if (parts > 1 && (tiles * Hk > most / parts || total > 4 * most / Hq)) {

@@ -101,7 +101,7 @@ struct Attn4Params {
   int32_t once;            // one tile of rows a sequence: its keys are read once
 };
 // Rows of a sequence and key/value head from which on keys and values are expanded.
-constexpr int kExpand4Rows = 128;
+constexpr int kExpand4Rows = 448;
 constexpr int kAttn4Rows = 16;  // rows of a workgroup
 hipError_t launch_expand4(const Attn4Params& p, int D, hipStream_t stream);
 hipError_t launch_attn4(const Attn4Params& p, int D, hipStream_t stream);
