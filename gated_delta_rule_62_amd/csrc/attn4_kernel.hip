@@ -187,22 +187,6 @@ __device__ __forceinline__ void end_row_loads(u32x4_t (&q)[KS]) {
   for (int ks = 0; ks < KS; ++ks) asm volatile("" : "+v"(q[ks]));
 }
 
-// The last of N sequences whose first slot of rows is not behind `slot` (packed queries; first
-// slots grow strictly).  64 lanes look at once: a binary search would wait for memory each step.
-__device__ __forceinline__ int find_sequence(const AttnParams& p, unsigned slot, int lane) {
-  int lo = 0, n = p.N;
-  while (n > 1) {
-    const int stride = (n + 63) >> 6, at = lo + lane * stride;
-    bool before = false;
-    if (at < lo + n)
-      before = clamp64(p.cu_q[at], 0, p.Tq_total) * p.G / kAttn4Rows + at <= slot;
-    const int k = max(1, (int)__popcll(__ballot(before))) - 1;
-    n = min(stride, n - k * stride);
-    lo += k * stride;
-  }
-  return lo;
-}
-
 template <int D, bool ONCE>
 __global__ __launch_bounds__(kAttnThreads, 2) void attn4_kernel(Attn4Params q4) {
   constexpr int KS = D / 32, DT = D / 16, ROWS = kAttn4Rows, WAVES = kAttnThreads / 64;
@@ -227,7 +211,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn4_kernel(Attn4Params q4) 
     const unsigned n = tile_no / (unsigned)q4.row_tiles;
     if (!set_tile(p, (int)n, (int64_t)(tile_no % (unsigned)q4.row_tiles) * ROWS, t)) return;
   } else {
-    const int n = __builtin_amdgcn_readfirstlane(find_sequence(p, tile_no, lane));
+    // the last sequence whose first slot is not behind this one (first slots grow strictly)
+    const int n = find_last(p.N, [&](int i) {
+      return clamp64(p.cu_q[i], 0, p.Tq_total) * p.G / ROWS + i <= tile_no;
+    });
     int64_t a, b;
     query_bounds(p, n, a, b);
     if (!set_tile(p, n, (tile_no - (a * p.G / ROWS + n)) * ROWS, t)) return;

@@ -53,14 +53,8 @@ __global__ __launch_bounds__(put4_threads(D)) void put4_kernel(Put4Params p) {
     n = (int)(tile_no / per);
     nth = tile_no % per;
   } else {
-    int lo = 0, hi = p.N - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (starts(p, mid) / kCache4Tile + 2 * (int64_t)mid <= tile_no) lo = mid;
-      else hi = mid - 1;
-    }
-    n = lo;
-    nth = tile_no - (starts(p, lo) / kCache4Tile + 2 * (int64_t)lo);
+    n = find_last(p.N, [&](int i) { return starts(p, i) / kCache4Tile + 2 * (int64_t)i <= tile_no; });
+    nth = tile_no - (starts(p, n) / kCache4Tile + 2 * (int64_t)n);
   }
   const int64_t t0 = starts(p, n);
   int64_t len = starts(p, n + 1) - t0;
@@ -85,8 +79,10 @@ __global__ __launch_bounds__(put4_threads(D)) void put4_kernel(Put4Params p) {
     x[0][j] = x[1][j] = u32x4_t{0u, 0u, 0u, 0u};
     if (has[j]) {
       const int64_t e = (int64_t)h * D + 8 * piece;
-      x[0][j] = *reinterpret_cast<const u32x4_t*>(p.k + (t0 + rel) * p.k_row + e);
-      x[1][j] = *reinterpret_cast<const u32x4_t*>(p.v + (t0 + rel) * p.v_row + e);
+      x[0][j] = __builtin_nontemporal_load(
+          reinterpret_cast<const u32x4_t*>(p.k + (t0 + rel) * p.k_row + e));
+      x[1][j] = __builtin_nontemporal_load(
+          reinterpret_cast<const u32x4_t*>(p.v + (t0 + rel) * p.v_row + e));
     }
   }
   unsigned code[2][2], byte[2][2];

@@ -92,6 +92,22 @@ __device__ __forceinline__ float wave_max(float v) {
   return fmaxf(t.a, t.b);
 }
 
+// The last of n items for which `before` holds; it holds for a first part of them and counts as
+// holding for the first.  Whole waves call it: 64 lanes look at once, where a binary search would
+// wait for memory each step.
+template <class F>
+__device__ __forceinline__ int find_last(int n, F before) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0;
+  while (n > 1) {
+    const int stride = (n + 63) >> 6, at = lane * stride;
+    const int k = max(1, (int)__popcll(__ballot(at < n && before(lo + at)))) - 1;
+    lo += k * stride;
+    n = min(stride, n - k * stride);
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
 // Raw buffer descriptor over [base, base + bytes): loads past the end return zero and
 // stores past it are dropped.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {

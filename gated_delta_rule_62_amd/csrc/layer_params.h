@@ -49,7 +49,6 @@ struct RopeParams {
   int32_t interleaved;
   float amplitude, sign;   // sign -1 turns back
   int32_t tpb;             // tokens of a workgroup
-  int32_t splits;          // workgroups that share a group of tokens' heads
 };
 constexpr int kRopeThreads = 256;
 constexpr int kRopePairs = 512;   // cosines and sines of a workgroup, at most

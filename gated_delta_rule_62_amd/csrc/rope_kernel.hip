@@ -7,6 +7,11 @@
 // multiplied in 64 bits and reduced to a fraction of a turn there, whose sine and cosine are
 // fp32.  They are the same for all heads of a token: a workgroup forms those of its tokens once,
 // in LDS, then streams the heads past them, bound by HBM.
+//
+// Measured: 2024 tokens of 96/8 heads, D 128, 21.6 us, 8192 tokens of 32/8 heads, half of each turned
+// in pairs side by side, 32.1 us: 5.0 and 5.2 TB/s, a copy's rate.  Loads that do not stay in the
+// caches gave a tenth; stores that do not would lose a fifth where a row's turned part is half a
+// cache line.
 #include "gfx950.h"
 #include "layer_params.h"
 
@@ -15,14 +20,15 @@ namespace {
 
 using namespace dev;
 
-__device__ __forceinline__ int64_t position(const RopeParams& p, int64_t token) {
+// Position of a token; with cu, `near` is the sequence of the workgroup's first token.
+__device__ __forceinline__ int64_t position(const RopeParams& p, int64_t token, int near) {
   if (p.pos != nullptr) return p.pos[token];
   int64_t n, first;
   if (p.cu == nullptr) {
     n = token / p.T;
     first = n * p.T;
   } else {  // the last sequence that starts at or before the token
-    int lo = 0, hi = p.N - 1;
+    int lo = near, hi = near + 1 < p.N && p.cu[near + 1] <= token ? p.N - 1 : near;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (p.cu[mid] <= token) lo = mid;
@@ -35,88 +41,144 @@ __device__ __forceinline__ int64_t position(const RopeParams& p, int64_t token) 
   return (int64_t)(from + (uint64_t)(token - first));
 }
 
-// Whether some sequence holds the token (with cu: one between its ends).
-__device__ __forceinline__ bool in_batch(const RopeParams& p, int64_t token) {
-  return p.cu == nullptr || (token >= p.cu[0] && token < p.cu[p.N]);
-}
-
-// VEC: units of 8 pairs (rot a multiple of 16), 16-byte accesses; else of one pair.
-template <bool VEC, bool INTER>
-__global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeParams p) {
-  __shared__ f32x2_t turn[kRopePairs];
-  const int tid = threadIdx.x, half = p.rot / 2;
-  const int64_t token0 = (int64_t)(blockIdx.x / (unsigned)p.splits) * p.tpb;
-  const int tokens = (int)min((int64_t)p.tpb, p.tokens - token0);
-  const int split = (int)(blockIdx.x % (unsigned)p.splits);
-
-  for (int e = tid; e < tokens * half; e += kRopeThreads) {
+// Cosines and sines of `tokens` tokens from token0 on, in LDS.
+__device__ __forceinline__ void turns_of(const RopeParams& p, int64_t token0, int tokens,
+                                         f32x2_t* turn) {
+  const int half = p.rot / 2;
+  const int near =
+      p.cu == nullptr ? 0 : find_last(p.N, [&](int i) { return p.cu[i] <= token0; });
+  for (int e = threadIdx.x; e < tokens * half; e += kRopeThreads) {
     const int tk = e / half, i = e - tk * half;
-    const double turns = (double)position(p, token0 + tk) * (p.freqs[i] * 0.15915494309189535);
+    const double turns = (double)position(p, token0 + tk, near) * (p.freqs[i] * 0.15915494309189535);
     float s, c;
     sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
     turn[e] = f32x2_t{c * p.amplitude, s * p.amplitude * p.sign};
   }
-  lds_barrier();
+}
 
-  // a thread's unit: 8 pairs (or one) of a head, or behind them 16 copied channels (or one)
-  constexpr int P = VEC ? 8 : 1, CP = VEC ? 16 : 1;
-  const int turned = half / P, rest = p.D - p.rot, units = turned + (rest + CP - 1) / CP;
-  const int heads = p.Hq + p.Hk, rows = tokens * heads;
-  const int per = max(1, kRopeThreads / units);
-  const int stride = p.splits * per;
-  for (int unit = tid % units; unit < units; unit += kRopeThreads) {
-    if (tid / units >= per) break;
-    for (int r = split * per + tid / units; r < rows; r += stride) {
-      const int tk = r / heads, h = r - tk * heads;
-      const int64_t token = token0 + tk;
-      const bool is_q = h < p.Hq;
-      const u16* in = is_q ? p.q + token * p.q_row + (int64_t)h * p.D
-                           : p.k + token * p.k_row + (int64_t)(h - p.Hq) * p.D;
-      u16* out = is_q ? p.q_out + token * p.q_out_row + (int64_t)h * p.D
-                      : p.k_out + token * p.k_out_row + (int64_t)(h - p.Hq) * p.D;
-      if (!in_batch(p, token)) continue;
-      if (unit >= turned) {
-        if (!(is_q ? p.q_copy : p.k_copy)) continue;
-        const int e = p.rot + (unit - turned) * CP;
-        if constexpr (VEC) {
-          *reinterpret_cast<u32x4_t*>(out + e) = *reinterpret_cast<const u32x4_t*>(in + e);
-          if (e + 8 < p.D)
-            *reinterpret_cast<u32x4_t*>(out + e + 8) =
-                *reinterpret_cast<const u32x4_t*>(in + e + 8);
-        } else {
-          out[e] = in[e];
-        }
-        continue;
-      }
-      const f32x2_t* cs = turn + tk * half + unit * P;
-      if constexpr (VEC) {
-        const int e0 = INTER ? unit * 16 : unit * 8, e1 = INTER ? e0 + 8 : half + e0;
-        u32x4_t a = *reinterpret_cast<const u32x4_t*>(in + e0),
-                b = *reinterpret_cast<const u32x4_t*>(in + e1);
+// The tokens of a workgroup that some sequence holds: [first, last) of its p.tpb.
+struct Span {
+  int first, last;
+};
+__device__ __forceinline__ Span span_of(const RopeParams& p, int64_t token0) {
+  int64_t a = 0, b = p.tokens;
+  if (p.cu != nullptr) {
+    a = p.cu[0];
+    b = min(b, p.cu[p.N]);
+  }
+  const int tokens = (int)min((int64_t)p.tpb, p.tokens - token0);
+  return Span{(int)max((int64_t)0, min(a - token0, (int64_t)tokens)),
+              (int)max((int64_t)0, min(b - token0, (int64_t)tokens))};
+}
+
+// A head's row of a token: h counts the query heads, then the key heads.
+__device__ __forceinline__ const u16* in_row(const RopeParams& p, int64_t token, int h) {
+  return h < p.Hq ? p.q + token * p.q_row + (int64_t)h * p.D
+                  : p.k + token * p.k_row + (int64_t)(h - p.Hq) * p.D;
+}
+__device__ __forceinline__ u16* out_row(const RopeParams& p, int64_t token, int h) {
+  return h < p.Hq ? p.q_out + token * p.q_out_row + (int64_t)h * p.D
+                  : p.k_out + token * p.k_out_row + (int64_t)(h - p.Hq) * p.D;
+}
+
+// 16 bytes that this call reads once.
+__device__ __forceinline__ u32x4_t load_once(const u16* x) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(x));
+}
+
+// 8 pairs, or 16 channels to copy, a thread and head (rot a multiple of 16): 16-byte accesses.  A
+// thread keeps its place in the head and walks the heads, eight of them in flight; the first eight
+// are asked for before the turns are formed.
+template <bool INTER>
+__global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeParams p) {
+  __shared__ f32x2_t turn[kRopePairs];
+  constexpr int AT_ONCE = 8;
+  const int tid = threadIdx.x, half = p.rot / 2;
+  const int64_t token0 = (int64_t)blockIdx.x * p.tpb;
+  const Span in = span_of(p, token0);
+  const int turned = half / 8, units = turned + (p.D - p.rot + 15) / 16;
+  const int heads = p.Hq + p.Hk, per = kRopeThreads / units;
+  const int unit = tid % units, row0 = in.first * heads + tid / units;
+  const int rows = tid < per * units ? in.last * heads : 0;
+  const bool turns = unit < turned;
+  // two pieces of 8 channels, one in each half of what is turned (also of pairs side by side, so
+  // that neighbours' pieces touch), or of what is copied
+  const int e0 = turns ? unit * 8 : p.rot + (unit - turned) * 8;
+  const int e1 = e0 + (turns ? half : (p.D - p.rot + 15) / 16 * 8);
+  const bool two = e1 < p.D;
+
+  u32x4_t a[AT_ONCE], b[AT_ONCE];
+  auto load = [&](int r0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (INTER) {  // a word is a pair
-            const f32x2_t ca = cs[i], cb = cs[4 + i];
-            const float a0 = bf_lo(a[i]), a1 = bf_hi(a[i]), b0 = bf_lo(b[i]), b1 = bf_hi(b[i]);
-            a[i] = pack_bf16(a0 * ca[0] - a1 * ca[1], a0 * ca[1] + a1 * ca[0]);
-            b[i] = pack_bf16(b0 * cb[0] - b1 * cb[1], b0 * cb[1] + b1 * cb[0]);
-          } else {
-            const f32x2_t cl = cs[2 * i], ch = cs[2 * i + 1];
-            const float a0 = bf_lo(a[i]), a1 = bf_hi(a[i]), b0 = bf_lo(b[i]), b1 = bf_hi(b[i]);
-            a[i] = pack_bf16(a0 * cl[0] - b0 * cl[1], a1 * ch[0] - b1 * ch[1]);
-            b[i] = pack_bf16(a0 * cl[1] + b0 * cl[0], a1 * ch[1] + b1 * ch[0]);
-          }
-        }
-        *reinterpret_cast<u32x4_t*>(out + e0) = a;
-        *reinterpret_cast<u32x4_t*>(out + e1) = b;
-      } else {
-        const int e0 = INTER ? 2 * unit : unit, e1 = INTER ? e0 + 1 : e0 + half;
-        const float a = bf2f(in[e0]), b = bf2f(in[e1]);
-        const f32x2_t c = cs[0];
-        out[e0] = (u16)pack_bf16(a * c[0] - b * c[1], 0.f);
-        out[e1] = (u16)pack_bf16(a * c[1] + b * c[0], 0.f);
+    for (int i = 0; i < AT_ONCE; ++i) {
+      const int r = r0 + i * per;
+      a[i] = b[i] = u32x4_t{0u, 0u, 0u, 0u};
+      if (r < rows) {
+        const u16* x = in_row(p, token0 + r / heads, r % heads);
+        a[i] = load_once(x + e0);
+        if (two) b[i] = load_once(x + e1);
       }
     }
+  };
+  load(row0);
+  turns_of(p, token0, in.last, turn);
+  lds_barrier();
+  for (int r0 = row0; r0 < rows; r0 += AT_ONCE * per) {
+    if (r0 > row0) load(r0);
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {
+      const int r = r0 + i * per;
+      if (r >= rows) break;
+      const int tk = r / heads, h = r - tk * heads;
+      if (turns) {
+        const f32x2_t* cs = turn + tk * half + unit * (INTER ? 4 : 8);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float a0 = bf_lo(a[i][w]), a1 = bf_hi(a[i][w]), b0 = bf_lo(b[i][w]),
+                      b1 = bf_hi(b[i][w]);
+          if constexpr (INTER) {  // a word is a pair
+            const f32x2_t ca = cs[w], cb = cs[half / 2 + w];
+            a[i][w] = pack_bf16(a0 * ca[0] - a1 * ca[1], a0 * ca[1] + a1 * ca[0]);
+            b[i][w] = pack_bf16(b0 * cb[0] - b1 * cb[1], b0 * cb[1] + b1 * cb[0]);
+          } else {
+            const f32x2_t cl = cs[2 * w], ch = cs[2 * w + 1];
+            a[i][w] = pack_bf16(a0 * cl[0] - b0 * cl[1], a1 * ch[0] - b1 * ch[1]);
+            b[i][w] = pack_bf16(a0 * cl[1] + b0 * cl[0], a1 * ch[1] + b1 * ch[0]);
+          }
+        }
+      } else if (!(h < p.Hq ? p.q_copy : p.k_copy)) {
+        continue;
+      }
+      u16* y = out_row(p, token0 + tk, h);
+      *reinterpret_cast<u32x4_t*>(y + e0) = a[i];
+      if (two) *reinterpret_cast<u32x4_t*>(y + e1) = b[i];
+    }
+  }
+}
+
+// Any even rot: a pair, or a channel to copy, a thread at a time.
+__global__ __launch_bounds__(kRopeThreads) void rope_pairs_kernel(RopeParams p) {
+  __shared__ f32x2_t turn[kRopePairs];
+  const int half = p.rot / 2, heads = p.Hq + p.Hk, units = half + p.D - p.rot;
+  const int64_t token0 = (int64_t)blockIdx.x * p.tpb;
+  const Span in = span_of(p, token0);
+  turns_of(p, token0, in.last, turn);
+  lds_barrier();
+  const int64_t end = (int64_t)in.last * heads * units;
+  for (int64_t e = (int64_t)in.first * heads * units + threadIdx.x; e < end; e += kRopeThreads) {
+    const int r = (int)(e / units), unit = (int)(e - (int64_t)r * units);
+    const int tk = r / heads, h = r - tk * heads;
+    const u16* x = in_row(p, token0 + tk, h);
+    u16* y = out_row(p, token0 + tk, h);
+    if (unit >= half) {
+      if (h < p.Hq ? p.q_copy : p.k_copy) y[half + unit] = x[half + unit];
+      continue;
+    }
+    const int e0 = p.interleaved ? 2 * unit : unit, e1 = p.interleaved ? e0 + 1 : e0 + half;
+    const float a = bf2f(x[e0]), b = bf2f(x[e1]);
+    const f32x2_t c = turn[tk * half + unit];
+    y[e0] = (u16)pack_bf16(a * c[0] - b * c[1], 0.f);
+    y[e1] = (u16)pack_bf16(a * c[1] + b * c[0], 0.f);
   }
 }
 
@@ -124,22 +186,19 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeParams p) {
 
 void rope_schedule(RopeParams& p) {
   const int half = p.rot / 2;
-  // one cosine and sine a thread, and as many workgroups as there are tokens for
+  // one cosine and sine a thread at most, and two workgroups a compute unit first (2024 tokens of
+  // 104 heads: three tokens each 21.6 us, one 23.6)
   int64_t tpb = kRopeThreads / half;
-  if (tpb < 1) tpb = 1;
-  const int64_t fill = p.tokens / 2048;
-  if (tpb > fill) tpb = fill < 1 ? 1 : fill;
-  p.tpb = (int32_t)tpb;
-  p.splits = 1;
+  const int64_t fill = p.tokens / 512;
+  if (tpb > fill) tpb = fill;
+  p.tpb = tpb < 1 ? 1 : (int32_t)tpb;
 }
 
 hipError_t launch_rope(const RopeParams& p, hipStream_t stream) {
-  const dim3 grid((unsigned)((p.tokens + p.tpb - 1) / p.tpb * p.splits));
-  const bool vec = p.rot % 16 == 0;
-  if (vec && p.interleaved) rope_kernel<true, true><<<grid, kRopeThreads, 0, stream>>>(p);
-  else if (vec) rope_kernel<true, false><<<grid, kRopeThreads, 0, stream>>>(p);
-  else if (p.interleaved) rope_kernel<false, true><<<grid, kRopeThreads, 0, stream>>>(p);
-  else rope_kernel<false, false><<<grid, kRopeThreads, 0, stream>>>(p);
+  const dim3 grid((unsigned)((p.tokens + p.tpb - 1) / p.tpb));
+  if (p.rot % 16 != 0) rope_pairs_kernel<<<grid, kRopeThreads, 0, stream>>>(p);
+  else if (p.interleaved) rope_kernel<true><<<grid, kRopeThreads, 0, stream>>>(p);
+  else rope_kernel<false><<<grid, kRopeThreads, 0, stream>>>(p);
   return hipGetLastError();
 }
 
