@@ -201,20 +201,20 @@ struct Plan4 {
 
 // Keys of a part when the caller leaves the choice, for `units` (tile of rows, key/value head)
 // pairs.  Parts are of equally many keys, not as many for each sequence, whose lengths differ.
-// Few units: at least 1024 keys (8192 positions and more, 8 heads a token, D 128, in one part and
-// in parts of 1024, 512: 1 sequence 168, 14.7, 14.9 us, 8 sequences 45, 12.7, 13.5).  When every
-// second compute unit has a workgroup anyway: none of 2048 positions or fewer (64 sequences 15.5,
-// 18.2 in two), else at least 1536 with D 128 (32 sequences of 8192 in one part 46, parts of 4096,
-// 1536, 1024: 43, 39.8, 41.5) and 1024 with D 64 (16 sequences, 40 rows, of 4096: 21, 20 in two
-// parts, 17.1 in four).  None from two units a compute unit on (32 sequences of 4096, 32 rows: 37.6,
-// 49 in four).
-int64_t attn4_auto_part(int64_t units, int64_t cap, int64_t D) {
+// One part up to 1024 positions (8 units, D 64: 7.4 us, 8.6 in two).  Up to a quarter of the compute
+// units: a workgroup for each, and at least 512 keys (D 128; 8 units,
+// 2048 positions, in one part and in parts of 1024, 512, 256: 14.4, 11.7, 9.5, 8.7 us; 32 units, 8192:
+// 45, 12.4, 13.5, 17.9; 8 units, 131072, parts of 8192, 4096, 2048: 49, 31, 37).  Up to two units
+// each: five workgroups and at least 1024 keys (256 units, 8192 positions, in one part and parts of
+// 4096, 1536, 1024: 46, 43, 39.8, 41.5), but more units than half of them with 2048 positions or
+// fewer in one (256 units 15.5, 18.2 in two).  Beyond: one part (512 units of 4096 positions 37.6, in
+// four 49).
+int64_t attn4_auto_part(int64_t units, int64_t cap) {
   const int64_t cus = kda::device_cus();
-  const bool many = 2 * units >= cus;
-  if (units >= 2 * cus || (many && cap <= 2048)) return cap;
-  int64_t parts = units > 0 ? 5 * cus / units : 1;
-  const int64_t most = cap / (many && D == 128 ? 1536 : 1024);
-  if (parts > most) parts = most;
+  if (units < 1 || units >= 2 * cus || cap <= (2 * units > cus ? 2048 : 1024)) return cap;
+  const bool few = 4 * units <= cus;
+  int64_t parts = (few ? 1 : 5) * cus / units;
+  if (parts > cap / (few ? 512 : 1024)) parts = cap / (few ? 512 : 1024);
   if (parts > 64) parts = 64;
   if (parts < 1) parts = 1;
   const int64_t part = (cap + parts - 1) / parts;
@@ -268,7 +268,7 @@ int attn4_plan(int64_t N, int64_t Bq, int64_t Tq, int64_t cap, int64_t Hq, int64
     plan->bytes = N * cap * row_bytes + round16(N * 8) + parts_bytes(sp, total * Hq, D);
     return KDA_OK;
   }
-  int64_t pt = part ? part : workspace ? attn4_auto_part(units, cap, D) : cap;
+  int64_t pt = part ? part : workspace ? attn4_auto_part(units, cap) : cap;
   if (pt > cap) pt = cap;
   const int64_t parts = (cap + pt - 1) / pt;
   if (parts > 1 && (tiles * Hk > most / parts || total > 4 * most / Hq)) {

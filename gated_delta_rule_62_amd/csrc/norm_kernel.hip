@@ -71,21 +71,23 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes) {
   return v;
 }
 
-// TPR threads own a row, C chunks of 8 channels each; a workgroup holds max(TPR, 256) threads.
+// TPR threads own a row, C chunks of 8 channels each; a workgroup holds max(TPR, 256) threads, and
+// several rows of a wave or less.
 template <int TPR, int C>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormParams p) {
-  constexpr int WG = TPR < 256 ? 256 : TPR, WAVES = TPR / 64;
+  constexpr int WG = TPR < 256 ? 256 : TPR, WAVES = TPR < 64 ? 1 : TPR / 64;
   __shared__ float part[2][WAVES];
   const int tid = threadIdx.x, t = tid % TPR;
-  const int64_t item = (int64_t)blockIdx.x * (WG / TPR) + tid / TPR;
-  if (TPR < 256 && item >= p.items) return;  // whole waves; no barrier with these sizes
+  int64_t item = (int64_t)blockIdx.x * (WG / TPR) + tid / TPR;
+  const int W = item < p.items ? p.W : 0;  // a row that is not there has no channels
+  if (item >= p.items) item = p.items - 1;
   const int64_t row = p.pieces == 1 ? item : item / p.pieces;
   const int first = p.pieces == 1 ? 0 : (int)(item % p.pieces) * p.W;
   const int64_t at = item * p.W;  // rows of res, res_out and out follow each other
 
   // a sum over the row's threads
   auto row_sum = [&](float v, int which) {
-    v = wave_sum(v);
+    v = lanes_sum(v, TPR < 64 ? TPR : 64);
     if constexpr (WAVES > 1) {
       if ((tid & 63) == 0) part[which][t >> 6] = v;
       lds_barrier();
@@ -103,7 +105,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormParams 
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int e = (c * TPR + t) * 8;
-    const bool in = e < p.W;
+    const bool in = e < W;
     u32x4_t w = u32x4_t{0u, 0u, 0u, 0u};
     gate[c] = w;
     r[c] = F8{};
@@ -138,7 +140,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormParams 
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int e = (c * TPR + t) * 8;
-      if (e < p.W) {
+      if (e < W) {
         const float f = rsqrtf(s[c] / n + p.eps);
         const F8 w = load8<false>(p.post_w, p.group < p.W ? e & (p.group - 1) : e, p.w_fp32);
 #pragma unroll
@@ -170,7 +172,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormParams 
       const int e = (c * TPR + t) * 8;
 #pragma unroll
       for (int i = 0; i < 8; ++i) u[c].v[i] = fmaf(p.alpha, u[c].v[i], r[c].v[i]);
-      if (e < p.W) {
+      if (e < W) {
         if (p.res_fp32) {
           f32x4_t* to = reinterpret_cast<f32x4_t*>(static_cast<float*>(p.res_out) + at + e);
           to[0] = f32x4_t{u[c].v[0], u[c].v[1], u[c].v[2], u[c].v[3]};
@@ -191,7 +193,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormParams 
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int e = (c * TPR + t) * 8;
-      if (e < p.W) {
+      if (e < W) {
         const F8 w = load8<false>(p.w, e, p.w_fp32);
 #pragma unroll
         for (int i = 0; i < 8; ++i) u[c].v[i] = u[c].v[i] * f * w.v[i];
@@ -202,7 +204,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormParams 
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int e = (c * TPR + t) * 8;
-      if (e < p.W) *reinterpret_cast<u32x4_t*>(p.out + at + e) = narrow(u[c]);
+      if (e < W) *reinterpret_cast<u32x4_t*>(p.out + at + e) = narrow(u[c]);
     }
   }
 }
@@ -212,7 +214,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormParams 
 // A wave for rows of up to 1024 channels (32,768 rows of 800: 39 us, 49 by workgroups), else a
 // workgroup: 512 threads from 2048 on (8192 rows of 4096: 85 us, 87 with 256; more threads gain half
 // a microsecond with few rows and lose 4-17% of many).
-int norm_threads(int64_t W) { return W <= 1024 ? 64 : W <= 2048 ? 256 : 512; }
+int norm_threads(int64_t W) {
+  return W <= 64 ? 8 : W <= 128 ? 16 : W <= 256 ? 32 : W <= 1024 ? 64 : W <= 2048 ? 256 : 512;
+}
 
 int norm_piece(int64_t W, int64_t group) {
   int64_t piece = group;
@@ -224,7 +228,10 @@ hipError_t launch_norm(const NormParams& p, hipStream_t stream) {
   const int W = p.W, threads = norm_threads(W);
   const int64_t per = threads < 256 ? 256 / threads : 1;
   const dim3 grid((unsigned)((p.items + per - 1) / per));
-  if (W <= 512) norm_kernel<64, 1><<<grid, 256, 0, stream>>>(p);
+  if (W <= 64) norm_kernel<8, 1><<<grid, 256, 0, stream>>>(p);
+  else if (W <= 128) norm_kernel<16, 1><<<grid, 256, 0, stream>>>(p);
+  else if (W <= 256) norm_kernel<32, 1><<<grid, 256, 0, stream>>>(p);
+  else if (W <= 512) norm_kernel<64, 1><<<grid, 256, 0, stream>>>(p);
   else if (W <= 1024) norm_kernel<64, 2><<<grid, 256, 0, stream>>>(p);
   else if (W <= 2048) norm_kernel<256, 1><<<grid, 256, 0, stream>>>(p);
   else if (W <= 4096) norm_kernel<512, 1><<<grid, 512, 0, stream>>>(p);
