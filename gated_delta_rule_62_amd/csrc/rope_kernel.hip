@@ -38,7 +38,7 @@ __device__ __forceinline__ int64_t position(const RopeParams& p, int64_t token, 
     first = p.cu[lo];
   }
   const uint64_t from = p.offsets != nullptr ? (uint64_t)p.offsets[n] : 0u;
-  return (int64_t)(from + (uint64_t)(token - first));
+  return (int64_t)(from + (uint64_t)token - (uint64_t)first);
 }
 
 // Cosines and sines of `tokens` tokens from token0 on, in LDS.
@@ -61,14 +61,12 @@ struct Span {
   int first, last;
 };
 __device__ __forceinline__ Span span_of(const RopeParams& p, int64_t token0) {
-  int64_t a = 0, b = p.tokens;
-  if (p.cu != nullptr) {
-    a = p.cu[0];
-    b = min(b, p.cu[p.N]);
-  }
-  const int tokens = (int)min((int64_t)p.tpb, p.tokens - token0);
-  return Span{(int)max((int64_t)0, min(a - token0, (int64_t)tokens)),
-              (int)max((int64_t)0, min(b - token0, (int64_t)tokens))};
+  auto in_group = [&](int64_t token) {  // token of the batch, clamped, as one of the group
+    const int64_t t = token < token0 ? token0 : token;
+    return (int)(min(t, min(token0 + p.tpb, p.tokens)) - token0);
+  };
+  if (p.cu == nullptr) return Span{0, in_group(p.tokens)};
+  return Span{in_group(p.cu[0]), in_group(p.cu[p.N])};
 }
 
 // A head's row of a token: h counts the query heads, then the key heads.

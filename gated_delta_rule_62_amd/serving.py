@@ -243,7 +243,8 @@ def kda_attn4_fwd(q, k4, ks, v4, vs, scale, out, lse=None, k_lens=None, cu_seqle
     q, scale, out, lse, cu_seqlens_q: as for ``kda_attn_fwd``; k4, ks, v4, vs: as for
     ``kda_cache4_put``, D 64 or 128.  ``part``: 0 (automatic) or keys per part, a multiple of 32;
     ``workspace``: a uint8 tensor of at least ``kda_attn4_workspace_bytes(...)`` bytes for this
-    call alone; None takes one from torch's allocator where the call needs it.
+    call alone; None takes one from torch's allocator where the call needs it (prompts: up to
+    8 GiB for the caches in bf16); an empty one: no workspace, one part.
     """
     lib = load_library()
     args = (lib.kda_attn4_fwd_at, lib.kda_attn4_workspace_bytes_at, q, k4, ks, v4, vs, scale, out,

@@ -675,14 +675,21 @@ int kda_cache4_put_check(const void* k, int64_t k_row, const void* v, int64_t v_
  *                  sequences may read one slot.  An index outside [0, num_slots) has no keys.
  *   part           0 (automatic), or keys per part: a multiple of 32 with at most 64 parts in
  *                  cap (KDA_ERR_BAD_SCHEDULE).  Each part of a row's keys has a workgroup of its
- *                  own, and a second kernel joins them.
+ *                  own, and a second kernel joins them.  With many rows (prompts: more than 448
+ *                  (query token, head) pairs a sequence and key/value head on average, and enough
+ *                  of them to fill the device many times over) the automatic choice expands the
+ *                  caches in use to bf16 once, where that takes 8 GiB at most, and runs
+ *                  kda_attn_fwd's kernels over them.
  *   workspace      caller-owned device memory, 16-byte aligned, of at least
  *                  kda_attn4_workspace_bytes(num_seqs, Bq, Tq, cap, Hq, Hk, D, part) bytes
  *                  (KDA_ERR_BAD_WORKSPACE), scratch on return: calls that may overlap in time
- *                  need one each.  With part 0 it may be NULL: one part then.
- * Scores and sums are fp32; probabilities take two bf16 parts for their product with v.
- * Parts sum in another order.  A call repeats itself bit for bit.  Infinities and NaN reach the
- * outputs of the queries that see them and no others.
+ *                  need one each.  With part 0 it may be NULL: one part straight from the caches
+ *                  then.
+ * Scores and sums are fp32.  For their product with v probabilities are held in two bf16 parts, or
+ * rounded to bf16 once where the caches are expanded; parts sum in another order.  A sequence's
+ * results depend on its call by these roundings, relative to the sum of the absolute values of its
+ * terms, and a call repeats itself bit for bit.  Infinities and NaN reach the outputs of the
+ * queries that see them and no others.
  */
 int kda_attn4_fwd(const void* q, int64_t q_row, const void* k4, const void* ks, const void* v4,
                   const void* vs, int64_t num_slots, int64_t cap, float scale, void* out,
@@ -699,7 +706,9 @@ int kda_attn4_fwd_check(const void* q, int64_t q_row, const void* k4, const void
 
 /*
  * kda_attn4_workspace_bytes -- bytes of kda_attn4_fwd's workspace: zero when the keys are one part,
- * else parts * Bq * Tq * Hq * (D + 2) floats.  Returns the size or a negative status.
+ * parts * Bq * Tq * Hq * (D + 2) floats for several, or num_seqs * cap * Hk * D * 4 bytes for
+ * expanded caches, with their lengths and the parts of kda_attn_fwd.  Returns the size or a
+ * negative status.
  */
 int64_t kda_attn4_workspace_bytes(int64_t num_seqs, int64_t Bq, int64_t Tq, int64_t cap,
                                   int64_t Hq, int64_t Hk, int64_t D, int64_t part);

@@ -139,6 +139,30 @@ def test_long_caches_in_the_automatic_parts():
     _run(63, [150], [5003], 4, 1, 64, 5024)
 
 
+PROMPTS = [([700, 500], [700, 900], 16, 2, 128, 928), ([650, 1, 900], [2000, 40, 900], 8, 1, 128, 2016),
+           ([600, 0, 700], [600, 33, 701], 32, 4, 64, 704), ([1500], [1400], 12, 1, 128, 1408)]
+
+
+@pytest.mark.parametrize("ql,kl,Hq,Hk,D,cap", PROMPTS)
+def test_prompts_expand_the_caches(ql, kl, Hq, Hk, D, cap):
+    """Enough rows for the automatic choice to expand the caches; slots in another order, one
+    outside, rows behind the last sequence; and the same call without a workspace."""
+    print("kda_attn4_fwd prompts", ql, kl, Hq, Hk, D, cap, flush=True)
+    N = len(ql)
+    need = kda.kda_attn4_workspace_bytes(N, 1, sum(ql) + 3, cap, Hq, Hk, D)
+    assert need >= N * cap * Hk * D * 4
+    _run(71, ql, kl, Hq, Hk, D, cap, behind=3)
+    _run(72, ql, kl, Hq, Hk, D, cap, S=N + 2, slots=[N + 1 - n for n in range(N)], behind=3)
+    _run(73, ql, kl, Hq, Hk, D, cap, S=N, slots=[-1] + list(range(1, N)), behind=3)
+    _run(74, ql, kl, Hq, Hk, D, cap, behind=3,
+         workspace=torch.empty(0, dtype=torch.uint8, device=DEV))
+
+
+def test_prompts_as_batch_rows():
+    assert kda.kda_attn4_workspace_bytes(3, 3, 400, 448, 16, 2, 128) >= 3 * 448 * 2 * 128 * 4
+    _run(75, [400] * 3, [448, 400, 12], 16, 2, 128, 448, packed=False)
+
+
 def test_large_and_growing_scores():
     """Scores of a few hundred, growing along the keys, and falling."""
     g = _gen(5)
@@ -176,7 +200,7 @@ def test_scales_of_every_size():
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("Lq,Lk,Hq,Hk,part", [
     (1, 700, 8, 2, 0), (4, 100, 8, 2, 0), (4, 100, 8, 2, 32), (40, 500, 2, 1, 512),
-    (200, 200, 2, 2, 0), (300, 333, 4, 2, 128), (150, 130, 12, 1, 0)])
+    (200, 200, 2, 2, 0), (300, 333, 4, 2, 128), (150, 130, 12, 1, 0), (1200, 1250, 24, 2, 0)])
 def test_infinities_and_nan_behind_the_last_visible_key(Lq, Lk, Hq, Hk, part, D):
     """Blocks of NaN and values beyond bf16's range, in k and v, reach the queries that see them,
     and nothing else."""

@@ -176,6 +176,16 @@ def test_attn4_refusals(lib):
     assert lib.kda_attn4_workspace_bytes(*sizes, 1024) == 0
     assert lib.kda_attn4_workspace_bytes(*sizes, 1 << 20) == 0
     assert lib.kda_attn4_workspace_bytes(1, 1, 1, 32768, 32, 8, 128, 0) > 0
+    # prompts: the caches in bf16 and their lengths, but 8 GiB at most; without a workspace none
+    prompt = (3, 1, 2024, 2208, 96, 8, 128)
+    assert lib.kda_attn4_workspace_bytes(*prompt, 0) == 3 * 2208 * 8 * 128 * 4 + 32
+    assert lib.kda_attn4_workspace_bytes(*prompt, 2208) == 0
+    assert lib.kda_attn4_workspace_bytes(64, 64, 1024, 1 << 17, 32, 8, 128, 0) == 0
+    big = dict(cu=6 * GB, N=3, Bq=1, Tq=2024, cap=2208, Hq=96, Hk=8, q_row=96 * 128)
+    assert st(**big) == kda.KDA_OK
+    assert st(**big, ws=50 * GB, ws_bytes=1 << 20) == kda.KDA_ERR_BAD_WORKSPACE
+    assert st(**big, ws=50 * GB, ws_bytes=GB) == kda.KDA_OK
+    assert st(**big, ws=40 * GB, ws_bytes=GB) == kda.KDA_ERR_BAD_ALIAS
     for bad in ((0,) + sizes[1:], sizes[:6] + (80,)):
         assert lib.kda_attn4_workspace_bytes(*bad, 0) == kda.KDA_ERR_BAD_SHAPE
 
