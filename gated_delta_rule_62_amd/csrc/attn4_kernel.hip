@@ -3,17 +3,31 @@
 // two (cache4_kernel.hip).  Their bf16 values are exact, so the products are those of a bf16 cache
 // that holds the same values, and the bytes read are 17/64 of its.
 //
-// The four waves of a workgroup share a tile of rows and take 32 keys each in turn, straight from
-// memory into registers, a step ahead.  One 16-byte load a lane is a lane's part of 16 keys' rows,
-// one is the values of eight channels at four keys: the places of codes and scales in the cache are
-// those of the matrix products' operands.
+// The waves of a workgroup share a tile of 16 rows and take 64 keys, two tiles of the cache, each in
+// turn.  Codes and scales go from memory straight into a ring in LDS, two such steps ahead, every
+// lane its own 16 bytes of 16 keys' rows and of the values of eight channels at four keys: the places
+// in the cache are those of the matrix products' operands, so nothing is exchanged.
 //   x^T = K Q^T: lane (g, c) holds channels D/4 g .. of key 4 (c % 4) + c / 4 of sixteen, so that
 //     accumulator row 4 g + r is key 4 r + g;
 //   out^T = V^T P^T: lane (g, c) holds channels D/16 c .. of the keys 4 r + g, and product e gives
 //     the channels D/16 m + e, m its row.  The conversion yields two channels of one key, an
 //     operand word wants two keys of one channel: a byte permutation between two keys' words.
 // Long caches are split into parts of equally many keys (not into equally many parts: lengths
-// differ), which a second kernel joins.
+// differ), which a second kernel joins.  Prompts bring the keys to bf16 once (expand4_kernel) and run
+// kda_attn_fwd's kernel for them.
+//
+// p keeps two bf16 parts, as in kda_attn_fwd's kernel for few rows: 2-10% of the time here, and none
+// of the results' error.
+//
+// Measured (calls): one token of each of 32 requests over 1024-8192 keys, 32/8 heads, D 128, 40.8 us
+// (161 MB, 4.0 TB/s; the loads alone and the join 33.5): a byte of codes asks for four times the
+// arithmetic of one of bf16, vector instructions are busy 56%, matrix products 21%, and the join takes
+// 4.6 us; five tokens of each of 16 over 512-4096 keys, 32/4 heads, D 64, 17.2; two requests of 200 and 77 keys
+// 4.4; packed [300, 700, 1024] queries over [300, 2200, 1101] keys, 96/8 heads, 118, of which 8 expand
+// the keys.  Two and three tiles of rows a wave, which convert a key once for more rows, were slower
+// (registers, fewer waves: 40 rows 24 and 28 us), as were registers instead of LDS for what is on
+// its way (45.9 us, 37.6 two steps ahead without the second path for infinities, whose registers do
+// not fit beside it), 16 waves, and one tile a step (19-20 us for the drafted tokens).
 #include "api_util.h"
 #include "attn_rows.h"
 #include "cache4.h"
@@ -187,9 +201,9 @@ __device__ __forceinline__ void end_row_loads(u32x4_t (&q)[KS]) {
   for (int ks = 0; ks < KS; ++ks) asm volatile("" : "+v"(q[ks]));
 }
 
-template <int D, bool ONCE>
-__global__ __launch_bounds__(kAttnThreads, 2) void attn4_kernel(Attn4Params q4) {
-  constexpr int KS = D / 32, DT = D / 16, ROWS = kAttn4Rows, WAVES = kAttnThreads / 64;
+template <int D, int WAVES, bool ONCE>
+__global__ __launch_bounds__(64 * WAVES, 2) void attn4_kernel(Attn4Params q4) {
+  constexpr int KS = D / 32, DT = D / 16, ROWS = kAttn4Rows;
   constexpr int AHEAD = 2;  // pairs of tiles of a wave on their way
   constexpr int LO = D + 4;  // row stride of the join buffer (floats)
   union Smem {
@@ -394,7 +408,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn4_kernel(Attn4Params q4) 
           f32x4_t{acc.o[e][0][r], acc.o[e + 1][0][r], acc.o[e + 2][0][r], acc.o[e + 3][0][r]} * f;
   lds_barrier();
   // a thread: four columns of a row
-  for (int i = tid; i < ROWS * D / 4; i += kAttnThreads) {
+  for (int i = tid; i < ROWS * D / 4; i += 64 * WAVES) {
     const int rr = i / (D / 4), c = i % (D / 4) * 4, r = t.row0 + rr;
     if (r >= t.rows) break;
     float mr = kNone, lr = 0.f;
@@ -468,15 +482,24 @@ __global__ __launch_bounds__(kAttnThreads) void expand4_kernel(Attn4Params q4) {
   }
 }
 
+template <int D, int WAVES>
+void start(const Attn4Params& p, dim3 grid, hipStream_t stream) {
+  if (p.once) attn4_kernel<D, WAVES, true><<<grid, 64 * WAVES, 0, stream>>>(p);
+  else attn4_kernel<D, WAVES, false><<<grid, 64 * WAVES, 0, stream>>>(p);
+}
+
 template <int D>
 hipError_t go(Attn4Params p, hipStream_t stream) {
   const AttnParams& a = p.a;
   p.row_tiles = (int32_t)((a.Tq * a.G + kAttn4Rows - 1) / kAttn4Rows);
   const int64_t slots = a.cu_q == nullptr ? a.N * (int64_t)p.row_tiles
                                           : attn_slots(a.Tq_total, a.N, a.G, kAttn4Rows);
-  const dim3 grid((unsigned)(slots * a.Hk * a.splits));
-  if (p.once) attn4_kernel<D, true><<<grid, kAttnThreads, 0, stream>>>(p);
-  else attn4_kernel<D, false><<<grid, kAttnThreads, 0, stream>>>(p);
+  const int64_t groups = slots * a.Hk * a.splits;
+  // one workgroup a compute unit at most: eight waves instead of four share its keys (16 tokens, 8
+  // heads, D 64, 2048 positions, one part: 10.1 us, 11.6 with four; 8 units of 1024: 6.9 and 7.4)
+  const dim3 grid((unsigned)groups);
+  if (groups <= device_cus()) start<D, 8>(p, grid, stream);
+  else start<D, 4>(p, grid, stream);
   if (a.splits > 1) return launch_attn_join(a, D, stream);
   return hipGetLastError();
 }

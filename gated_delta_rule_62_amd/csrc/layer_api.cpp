@@ -201,17 +201,16 @@ struct Plan4 {
 
 // Keys of a part when the caller leaves the choice, for `units` (tile of rows, key/value head)
 // pairs.  Parts are of equally many keys, not as many for each sequence, whose lengths differ.
-// One part up to 1024 positions (8 units, D 64: 7.4 us, 8.6 in two).  Up to a quarter of the compute
-// units: a workgroup for each, and at least 512 keys (D 128; 8 units,
-// 2048 positions, in one part and in parts of 1024, 512, 256: 14.4, 11.7, 9.5, 8.7 us; 32 units, 8192:
-// 45, 12.4, 13.5, 17.9; 8 units, 131072, parts of 8192, 4096, 2048: 49, 31, 37).  Up to two units
-// each: five workgroups and at least 1024 keys (256 units, 8192 positions, in one part and parts of
-// 4096, 1536, 1024: 46, 43, 39.8, 41.5), but more units than half of them with 2048 positions or
-// fewer in one (256 units 15.5, 18.2 in two).  Beyond: one part (512 units of 4096 positions 37.6, in
-// four 49).
+// One part up to 1280 positions (16 units, D 64: 7.5 us, 8.7 in three).  Up to a quarter of the
+// compute units: a workgroup for each, and at least 512 keys (D 128; 8 units, 2048 positions, in one
+// part and in parts of 1024, 512, 256: 13.6, 11.6, 9.7, 8.9 us; 32 units, 8192: 37, 13.2, 14.3, 18.4;
+// 8 units, 131072, parts of 8192, 4096, 2048: 43, 33, 39).  Up to two units each: five workgroups and
+// at least 1024 keys (256 units, 8192 positions, in one part and parts of 4096, 1536, 1024: 46, 43,
+// 39.8, 41.5), but more units than half of them with 2048 positions or fewer in one (256 units 15.5,
+// 18.2 in two).  Beyond: one part (512 units of 4096 positions 37.6, in four 49).
 int64_t attn4_auto_part(int64_t units, int64_t cap) {
   const int64_t cus = kda::device_cus();
-  if (units < 1 || units >= 2 * cus || cap <= (2 * units > cus ? 2048 : 1024)) return cap;
+  if (units < 1 || units >= 2 * cus || cap <= (2 * units > cus ? 2048 : 1280)) return cap;
   const bool few = 4 * units <= cus;
   int64_t parts = (few ? 1 : 5) * cus / units;
   if (parts > cap / (few ? 512 : 1024)) parts = cap / (few ? 512 : 1024);
