@@ -22,8 +22,8 @@
 // Measured (calls): one token of each of 32 requests over 1024-8192 keys, 32/8 heads, D 128, 40.8 us
 // (161 MB, 4.0 TB/s; the loads alone and the join 33.5): a byte of codes asks for four times the
 // arithmetic of one of bf16, vector instructions are busy 56%, matrix products 21%, and the join takes
-// 4.6 us; five tokens of each of 16 over 512-4096 keys, 32/4 heads, D 64, 17.2; two requests of 200 and 77 keys
-// 4.4; packed [300, 700, 1024] queries over [300, 2200, 1101] keys, 96/8 heads, 118, of which 8 expand
+// 4.6 us; five tokens of each of 16 over 512-4096 keys, 32/4 heads, D 64, 17.2; two requests of 200 and
+// 77 keys 4.4; packed [300, 700, 1024] queries over [300, 2200, 1101] keys, 96/8 heads, 118, of which 8 expand
 // the keys.  Two and three tiles of rows a wave, which convert a key once for more rows, were slower
 // (registers, fewer waves: 40 rows 24 and 28 us), as were registers instead of LDS for what is on
 // its way (45.9 us, 37.6 two steps ahead without the second path for infinities, whose registers do
@@ -389,7 +389,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn4_kernel(Attn4Params q4) {
         std::make_integer_sequence<int, DT / 2>{});
   }
 
-  // ---- join the waves (behind the barrier every wave's reads of its tiles are done): maxima and sums first, then the outputs
+  // ---- join the waves (behind the barrier every wave's reads of its tiles are done): maxima and
+  // sums first, then the outputs
   const float l = sum_over_groups(acc.l[0]);
   if (lg == 0) {
     sml[wave][l16][0] = acc.m[0];

@@ -117,7 +117,8 @@ int rope_check(const void* q, int64_t q_row, const void* q_out, int64_t q_out_ro
     if (span_bytes(tok, both[i].row, 1, both[i].len) < 0) return KDA_ERR_BAD_SHAPE;
   }
   if (tok == 0) return KDA_OK;
-  const Range small[] = {make_range(freqs, rot / 2 * 8), make_range(positions, positions ? tok * 8 : 0),
+  const Range small[] = {make_range(freqs, rot / 2 * 8),
+                         make_range(positions, positions ? tok * 8 : 0),
                          make_range(offsets, offsets ? N * 8 : 0),
                          make_range(cu, cu ? (N + 1) * 8 : 0)};
   if (any_overlap(make_range(q_out, span_bytes(tok, q_out_row, 1, ao.len)), small, 4) ||

@@ -49,7 +49,8 @@ __device__ __forceinline__ void turns_of(const RopeParams& p, int64_t token0, in
       p.cu == nullptr ? 0 : find_last(p.N, [&](int i) { return p.cu[i] <= token0; });
   for (int e = threadIdx.x; e < tokens * half; e += kRopeThreads) {
     const int tk = e / half, i = e - tk * half;
-    const double turns = (double)position(p, token0 + tk, near) * (p.freqs[i] * 0.15915494309189535);
+    const double turns =
+        (double)position(p, token0 + tk, near) * (p.freqs[i] * 0.15915494309189535);  // 1 / (2 pi)
     float s, c;
     sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
     turn[e] = f32x2_t{c * p.amplitude, s * p.amplitude * p.sign};
