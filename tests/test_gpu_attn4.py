@@ -200,7 +200,8 @@ def test_scales_of_every_size():
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("Lq,Lk,Hq,Hk,part", [
     (1, 700, 8, 2, 0), (4, 100, 8, 2, 0), (4, 100, 8, 2, 32), (40, 500, 2, 1, 512),
-    (200, 200, 2, 2, 0), (300, 333, 4, 2, 128), (150, 130, 12, 1, 0), (1200, 1250, 24, 2, 0)])
+    (200, 200, 2, 2, 0), (300, 333, 4, 2, 128), (150, 130, 12, 1, 0), (1200, 1250, 24, 2, 0),
+    (600, 640, 16, 4, 1280), (500, 900, 8, 2, 320)])
 def test_infinities_and_nan_behind_the_last_visible_key(Lq, Lk, Hq, Hk, part, D):
     """Blocks of NaN and values beyond bf16's range, in k and v, reach the queries that see them,
     and nothing else."""
