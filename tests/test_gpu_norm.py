@@ -127,6 +127,25 @@ def test_gates_far_from_zero():
         check(out, y, yb, fn)
 
 
+def test_largest_gates():
+    """Gates at the ends of bf16's range, and beyond: closed ones give zero however large the row."""
+    g = _gen(8)
+    W, inf = 64, float("inf")
+    x = _normal(g, 5, W)
+    z = torch.empty_like(x)
+    z[0], z[1], z[2], z[3] = -3e38, -1e30, 300.0, -300.0
+    x[0], x[1, ::2] = 1e10, -1e20
+    z[4] = torch.tensor([-inf, inf, float("nan"), 3e38] * (W // 4), device=DEV)
+    x[4, 3::4] = 0.5
+    for fn in ("sigmoid", "silu"):
+        out = torch.empty_like(x)
+        kda.kda_norm(x, out, gate=z, gate_fn=fn)
+        _, _, y, yb = forms.norm(x, gate=z, gate_fn=fn)
+        assert (y[:2] == 0).all()
+        check(out[:2], y[:2], torch.full_like(y[:2], 1e-37), fn + " closed")
+        check(out[2:], y[2:], yb[2:], fn)
+
+
 def test_many_rows_of_one_head():
     """More rows than a launch of one workgroup each would like."""
     _run(_gen(4), 300001, 128, group=128, gate="sigmoid", pre=False)
