@@ -55,22 +55,6 @@ __device__ __forceinline__ u32x4_t narrow(const F8& r) {
                  pack_bf16(r.v[6], r.v[7])};
 }
 
-// u sigmoid(z), or u z sigmoid(z): sigmoid(z) = s s / (1 + t t) with t = e^(-|z| / 2) and s = t or 1.
-// Factors with one s each, that underflow only where the result does, and z joins the one without
-// u: large u and z below zero do not pass fp32's range on the way to zero.
-template <bool SILU>
-__device__ __forceinline__ F8 gated(F8 u, F8 z) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = __builtin_amdgcn_exp2f(-0.5f * kLog2e * fabsf(z.v[i]));
-    const float s = z.v[i] < 0.f ? t : 1.f;
-    float f = s * __builtin_amdgcn_rcpf(fmaf(t, t, 1.f));
-    if constexpr (SILU) f *= z.v[i];
-    u.v[i] = u.v[i] * s * f;
-  }
-  return u;
-}
-
 // Sum over aligned groups of `lanes` lanes (a power of two from 4 to 64, the same for the wave).
 __device__ __forceinline__ float lanes_sum(float v, int lanes) {
   v = group_sum<4>(v);
@@ -165,12 +149,21 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormParams 
     }
   }
   if (g != nullptr) {
-    if (p.silu) {
 #pragma unroll
-      for (int c = 0; c < C; ++c) u[c] = gated<true>(u[c], widen(gate[c]));
-    } else {
+    for (int c = 0; c < C; ++c) {
+      const F8 z = widen(gate[c]);
 #pragma unroll
-      for (int c = 0; c < C; ++c) u[c] = gated<false>(u[c], widen(gate[c]));
+      for (int i = 0; i < 8; ++i) {
+        // sigmoid(z) = s s / (1 + t t) with t = e^(-|z| / 2) and s = t or 1: factors that underflow
+        // only where the result does
+        const float t = __builtin_amdgcn_exp2f(-0.5f * kLog2e * fabsf(z.v[i]));
+        const float s = z.v[i] < 0.f ? t : 1.f;
+        u[c].v[i] = u[c].v[i] * s * (s * __builtin_amdgcn_rcpf(fmaf(t, t, 1.f)));
+      }
+      if (p.silu) {  // after the sigmoid, so that a large u does not overflow on the way to zero
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[c].v[i] *= z.v[i];
+      }
     }
   }
   if (p.res != nullptr) {
