@@ -560,7 +560,8 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_token_kernel(AttnParams 
 
 // Joins the splits of a row, one wave per (query token, head): lane s weighs split s (there
 // are at most 64), then the lanes share the row's D values.  GAPS: what the outputs of a
-// split without keys hold is loaded (the loads do not wait for the sums) but not used.
+// split without keys hold is loaded (the loads do not wait for the sums) but not used.  Each of
+// its two callers keeps the order in which its results' normalisers have always been summed.
 template <int D, bool GAPS>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
   constexpr int V = D / 64;  // values per lane
@@ -588,7 +589,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
   const uint64_t filled = GAPS ? __ballot(!(ml[0] == kNone && ml[1] == 0.f)) : ~0ull;
   const float m = wave_max(ml[0]);
   const float f = __builtin_amdgcn_exp2f(ml[0] - (m == kNone ? 0.f : m));
-  const float l = wave_sum(ml[1] * f);
+  const float l = GAPS ? wave_sum_mirrored(ml[1] * f) : wave_sum(ml[1] * f);
   vec sum = {};
   for (int s0 = 0; s0 < p.splits; s0 += 8) {
     if (s0 > 0) load(s0);

@@ -76,11 +76,25 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// Sum and maximum over the wave, in every lane.
+// Sum over the wave, in every lane: of the lanes that differ in bit 0 of their number, then in bit
+// 1, up to bit 5.  Where the compiler fuses the first addition with the product that v is, the
+// lanes' sums differ in their last bits, and the order is part of the result.
 __device__ __forceinline__ float wave_sum(float v) {
+  v += dpp<0xB1>(v);
+  v += dpp<0x4E>(v);
+  v += dpp<0x141>(dpp<0x1B>(v));  // quads reversed, then halves of a row mirrored: lane xor 4
+  v += dpp<0x128>(v);             // row_ror:8: lane xor 8
+  Two t = swap16(v);
+  v = t.a + t.b;
+  t = swap32(v);
+  return t.a + t.b;
+}
+// The same with mirrored lanes for bits 2 and 3.
+__device__ __forceinline__ float wave_sum_mirrored(float v) {
   const Two t = swap32(group_sum<32>(v));
   return t.a + t.b;
 }
+// Maximum over the wave, in every lane.
 __device__ __forceinline__ float wave_max(float v) {
   v = fmaxf(v, dpp<0xB1>(v));
   v = fmaxf(v, dpp<0x4E>(v));
