@@ -244,13 +244,21 @@ def kda_attn4_fwd(q, k4, ks, v4, vs, scale, out, lse=None, k_lens=None, cu_seqle
     ``kda_cache4_put``, D 64 or 128.  ``part``: 0 (automatic) or keys per part, a multiple of 32;
     ``workspace``: a uint8 tensor of at least ``kda_attn4_workspace_bytes(...)`` bytes for this
     call alone; None takes one from torch's allocator where the call needs it (prompts: up to
-    8 GiB for the caches in bf16); an empty one: no workspace, one part.
+    8 GiB for the caches in bf16, by their capacity); an empty one: no workspace, one part, which
+    is also what a call with ``part`` 0 falls back to where the allocator has no memory left
+    (slower for prompts, and rounded as such a call).
     """
     lib = load_library()
     args = (lib.kda_attn4_fwd_at, lib.kda_attn4_workspace_bytes_at, q, k4, ks, v4, vs, scale, out,
             lse, k_lens, cu_seqlens_q, slots, part)
     st = _calls.attn4_fwd(*args, workspace, stream)
     if st > 0:  # the bytes it wants
-        st = _calls.attn4_fwd(*args, _workspace(st, q, stream), stream)
+        try:
+            workspace = _workspace(st, q, stream)
+        except torch.OutOfMemoryError:
+            if part:  # parts are written there
+                raise
+            workspace = torch.empty(0, dtype=torch.uint8, device=q.device)
+        st = _calls.attn4_fwd(*args, workspace, stream)
     if st != 0:
         raise KdaError(st)
