@@ -16,17 +16,19 @@
 // differ), which a second kernel joins.  Prompts bring the keys to bf16 once (expand4_kernel) and run
 // kda_attn_fwd's kernel for them.
 //
-// p keeps two bf16 parts, as in kda_attn_fwd's kernel for few rows: 2-10% of the time here, and none
-// of the results' error.
+// p keeps two bf16 parts, as in kda_attn_fwd's kernel for few rows: error 1.65e-3, that of rounding
+// the output, where one part has 2.3e-3.  One part takes 38.9 instead of 41.2 us for the single tokens
+// below, and 18.2 instead of 17.5 for the drafted ones.
 //
 // Measured (calls): one token of each of 32 requests over 1024-8192 keys, 32/8 heads, D 128, 40.8 us
 // (161 MB, 4.0 TB/s; the loads alone and the join 33.5): a byte of codes asks for four times the
 // arithmetic of one of bf16, vector instructions are busy 56%, matrix products 21%, and the join takes
 // 4.6 us; five tokens of each of 16 over 512-4096 keys, 32/4 heads, D 64, 17.2; two requests of 200 and
 // 77 keys 4.4; packed [300, 700, 1024] queries over [300, 2200, 1101] keys, 96/8 heads, 118, of which 8 expand
-// the keys.  Two and three tiles of rows a wave, which convert a key once for more rows, were slower
-// (registers, fewer waves: 40 rows 24 and 28 us), as were registers instead of LDS for what is on
-// its way (45.9 us, 37.6 two steps ahead without the second path for infinities, whose registers do
+// the keys.  Two and four tiles of rows a wave, which convert a key once for more rows, were slower with
+// codes in registers (256 of them and spills: the drafted tokens 21 and 32 us, 19 in tiles of 16 then)
+// and have not been measured since codes wait in LDS.  Slower too: registers instead of LDS for what is
+// on its way (45.9 us, 37.6 two steps ahead without the second path for infinities, whose registers do
 // not fit beside it), 16 waves, and one tile a step (19-20 us for the drafted tokens).
 #include "api_util.h"
 #include "attn_rows.h"

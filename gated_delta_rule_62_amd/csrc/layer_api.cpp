@@ -209,6 +209,11 @@ struct Plan4 {
 // at least 1024 keys (256 units, 8192 positions, in one part and parts of 4096, 1536, 1024: 46, 43,
 // 39.8, 41.5), but more units than half of them with 2048 positions or fewer in one (256 units 15.5,
 // 18.2 in two).  Beyond: one part (512 units of 4096 positions 37.6, in four 49).
+// The figures are of lengths from an eighth of the capacity to all of it.  Where all caches are full
+// one part gains at 4096 positions, having no uneven lengths to level (256 units in one part and by
+// this rule, D 64: 17.4 and 21.0, D 128: 28.0 and 32.0; 192 units, three tiles of rows over the same
+// keys: 17.1 and 20.7, 22.8 and 29.1), and D 64 with 2048 positions would rather have one part or
+// parts of 512 (64 units: 10.0 and 9.7, by this rule 11.4).
 int64_t attn4_auto_part(int64_t units, int64_t cap) {
   const int64_t cus = kda::device_cus();
   if (units < 1 || units >= 2 * cus || cap <= (2 * units > cus ? 2048 : 1280)) return cap;
@@ -253,6 +258,11 @@ int attn4_plan(int64_t N, int64_t Bq, int64_t Tq, int64_t cap, int64_t Hq, int64
   // positions, 8 heads, D 128, 256 rows: 241 us, from the cache 210; 512 rows: 376 and 405), and
   // only where their tiles fill the device many times over (1 sequence of 8192, 512 rows: 36 and
   // 21, 2048 rows: 52 and 60; 3 sequences of 2208, D 64, 1024 rows: 45 and 32, 2048 rows: 53, 57).
+  // p has one bf16 part then, as in that kernel's own calls: packed [300, 700, 1024] queries over
+  // [300, 2200, 1101] keys, 96/8 heads, 119 us with an error of 2.1e-3; two parts there 149 and 1.6e-3.
+  // Both conditions go by the call's mean, as the host knows no lengths: a prompt of 2048 beside 31 single
+  // tokens over 1024-3904 positions, 32/8 heads, takes 116 us, in two calls 58 and 28; one of 8192
+  // expands all 32 caches, 625 us, in two calls 498 and 27.
   const int64_t row_bytes = Hk * D * 4;
   if (part == 0 && workspace && total * G > N * kda::kExpand4Rows &&
       units > (D == 128 ? 3 : 8) * kda::device_cus() &&

@@ -156,8 +156,9 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeParams p) {
 }
 
 // Any even rot: pieces of 8 channels as above, whose partners lie at any distance, so rows go
-// through LDS.  8192 tokens of 32/8 heads, 50 of 128 channels: 44 us (187 with a
-// pair a thread).
+// through LDS.  8192 tokens of 32/8 heads, 50 of 128 channels: 42 us, pairs side by side 45 (187 with
+// a pair a thread; 48 channels by the kernel above 39; the bytes 33).  Two barriers for every four rows
+// of a thread are the likely difference; pairs side by side would need neither them nor the LDS.
 template <bool INTER>
 __global__ __launch_bounds__(kRopeThreads) void rope_any_kernel(RopeParams p) {
   constexpr int AT_ONCE = 4;

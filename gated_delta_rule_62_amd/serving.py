@@ -158,8 +158,10 @@ def kda_rope_freqs(rot: int, base: float = 10000.0, method: str = "", factor: fl
 
     method "": powers of the base.  "linear": positions interpolated, every frequency divided by
     factor.  "yarn": a pair that turns at most ``slow`` times over the ``original`` context is
-    interpolated, one that turns ``fast`` times or more is kept, linearly blended between, and
-    the amplitude is ``0.1 ln(factor) + 1`` (1 for a factor of at most 1).
+    interpolated, one that turns ``fast`` times or more is kept, and the amplitude is
+    ``0.1 ln(factor) + 1`` (1 for a factor of at most 1).  Between the two the blend is linear in
+    the number of turns; a model whose program blends linearly in the pair's index has other
+    frequencies there and passes its own to ``kda_rope``.
     """
     if rot < 2 or rot % 2 or not base > 0 or not factor > 0 or not fast > slow:
         raise ValueError("rot must be even and positive, base and factor positive, fast above slow")

@@ -573,7 +573,9 @@ int64_t kda_attn_workspace_bytes(int64_t num_seqs, int64_t Bq, int64_t Tq, int64
  * At least one of post_weight, gate, weight and residual (KDA_ERR_NULL_ARG).
  * Everything between loads and stores is fp32; the second norm takes h before residual_out is
  * rounded.  Squares and their sums are fp32: a group's L2 norm stays below 1.8e19, and values
- * whose squares underflow count as zero beside eps.  One kernel on `stream`.
+ * whose squares underflow count as zero beside eps.  With eps zero squares below 2^-126 lose
+ * digits, and a group of nothing but zeros and such values gives NaN and infinities.  One kernel
+ * on `stream`.
  */
 int kda_norm(const void* x, int64_t x_row, const void* gate, int64_t gate_row, int gate_fn,
              const void* post_weight, int64_t group, const void* weight, int weight_dtype,
@@ -634,8 +636,8 @@ int kda_rope_check(const void* q, int64_t q_row, const void* q_out, int64_t q_ou
  *                    D  64: byte 256 g + 16 (d / 4) + 8 j + 2 i + d % 4 / 2.
  *   ks, vs         uint8 [num_slots, Hk, cap / 32, D / 32, 32]: the scales of the tile's positions
  *                  for each block of channels, position 16 j + 4 i + g at 8 g + 2 i + j.
- * (These places are those of the matrix products' operands, so that kda_attn4_fwd loads 16
- * bytes a lane and passes nothing through LDS.)  D in {64, 128}; cap up to 2^30.  A slot is
+ * (These places are those of the matrix products' operands: kda_attn4_fwd brings 16 bytes a
+ * lane and every lane uses its own, none is exchanged.)  D in {64, 128}; cap up to 2^30.  A slot is
  * contiguous in all four: copying it copies the cache of a request.
  *
  * kda_cache4_put -- new keys and values into such caches: token t of sequence n goes to
@@ -679,7 +681,10 @@ int kda_cache4_put_check(const void* k, int64_t k_row, const void* v, int64_t v_
  *                  (query token, head) pairs a sequence and key/value head on average, and enough
  *                  of them to fill the device many times over) the automatic choice expands the
  *                  caches in use to bf16 once, where that takes 8 GiB at most, and runs
- *                  kda_attn_fwd's kernels over them.
+ *                  kda_attn_fwd's kernels over them.  The choice goes by the whole call, so a
+ *                  prompt among many single tokens, or these beside a large prompt, are faster in
+ *                  a call of their own; and the expanded caches' size by their capacity, not by
+ *                  k_lens.
  *   workspace      caller-owned device memory, 16-byte aligned, of at least
  *                  kda_attn4_workspace_bytes(num_seqs, Bq, Tq, cap, Hq, Hk, D, part) bytes
  *                  (KDA_ERR_BAD_WORKSPACE), scratch on return: calls that may overlap in time
